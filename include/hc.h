@@ -82,6 +82,9 @@ typedef enum hc_wire {
 #define HC_DEVERR_SLOT 1   /* src_slots[j] or dst_slots[j] outside [0, num_slots) */
 #define HC_DEVERR_DELTA 2  /* delta_idx[j] outside [0, n_distinct) */
 #define HC_DEVERR_NVALID 4 /* n_valid[j] outside [1, block_size] */
+#define HC_DEVERR_LENGTH 8 /* a request length that is negative or more than the call holds */
+#define HC_DEVERR_FREE 16  /* fewer free slots than the step's new blocks */
+#define HC_DEVERR_POS 32   /* a position outside [0, n_positions) */
 
 /* Shape and strides of one paged buffer pair (K and V share it).
  * Supported: d_head in {64, 128}; block_size in {16, 32, 64, 128};
@@ -324,6 +327,188 @@ int hc_tenant_key(const uint8_t* master, int32_t master_len, const char* tenant,
 int hc_block_digests(const int32_t* tokens, int64_t n_tokens, int32_t block_size,
                      const uint8_t* key, int32_t key_len, uint8_t* prefix_digests,
                      uint8_t* content_digests);
+
+/* ------------------------------------------------------------------------
+ * Serving from a 4-bit cache
+ *
+ * The INT4 wire is also a cache to serve from: one layer's cache is the wire
+ * of n_layers = 1 over num_slots blocks,
+ *   codes  u8      [num_slots][2][n_kv_heads][block_size][d_head/2]
+ *   scales f16|f32 [num_slots][2][n_kv_heads][block_size][d_head/group]
+ * so that hc_encode_int4's output can be attended as it stands, and
+ * hc_fetch_rotate_scatter reads a cache back.  A request's block table names
+ * the slot of each of its blocks; its cache row of position p is
+ * row = slot * block_size + p % block_size with slot = table[p / block_size].
+ *
+ * One step of a decoder: hc_build_block_tables once; then in each layer
+ * hc_append_int4 and hc_attend_int4 on that layer's cache.
+ * ------------------------------------------------------------------------ */
+
+/* Shape of one layer's 4-bit cache.  Supported: d_head in {64, 128};
+ * block_size in {16, 32, 64, 128}; group in {32, 64, 128}, <= d_head;
+ * scale_dtype HC_F16 or HC_F32.  codes and scales 16-byte aligned. */
+typedef struct hc_int4_cache {
+  int32_t n_kv_heads;
+  int32_t d_head;
+  int32_t block_size;
+  int32_t num_slots;
+  int32_t group;
+  int32_t scale_dtype;
+} hc_int4_cache;
+
+/* A tensor of rows x[token][head][0..d_head): strides in elements, the
+ * channels of a row adjacent. */
+typedef struct hc_rows {
+  void* ptr; /* device */
+  int64_t token_stride;
+  int64_t head_stride;
+} hc_rows;
+
+/* Rotary positions with n_axes axes (1 for text; time, height and width for
+ * video): pair i < rot_dim/2 of a row turns by the angle of
+ * positions[pair_axis[i]][token], whose (cos, sin) is
+ * table[position][i] (hc_build_delta_sincos over 0..n_positions-1).
+ * Channels from rot_dim on are not rotated.  Pairs are (2i, 2i+1)
+ * (HC_PAIR_INTERLEAVED) or (i, i + rot_dim/2) (HC_PAIR_HALF_SPLIT). */
+typedef struct hc_rope_axes_desc {
+  const int32_t* positions; /* device [n_axes][position_stride] */
+  int64_t position_stride;  /* elements between axes, >= n_tokens when n_axes > 1 */
+  const float* table;       /* device f32 [n_positions][rot_dim/2][2], 8-byte aligned */
+  int32_t n_axes;           /* 1..8 */
+  int32_t n_positions;      /* >= 1 */
+  int32_t rot_dim;          /* even, 2..256, <= d_head */
+  int32_t pairing;          /* hc_pairing */
+  int32_t inverse;          /* 1: turn by the opposite angle (the rotation's gradient) */
+  uint8_t pair_axis[128];   /* axis of pair i, < n_axes */
+} hc_rope_axes_desc;
+
+/* hc_build_block_tables: one step's addressing, from request lengths.
+ * Request r holds cached_lens[r] tokens and brings new_lens[r] more.  With
+ * B = block_size, held = ceil(cached/B) and need = ceil((cached+new)/B) - held:
+ *   block_tables[r][held + i] = free_slots[(sum of need over requests < r) + i], i < need
+ *   q_starts[r] = sum of new_lens over requests < r; q_starts[n_req] = all new tokens
+ *   kv_lens[r]  = cached + new
+ *   and for new token i of request r, t = q_starts[r] + i, p = cached + i:
+ *   token_req[t] = r, token_pos[t] = p,
+ *   token_rows[t] = block_tables[r][p / B] * B + p % B
+ * Entries t >= q_starts[n_req] (a step padded to a fixed number of tokens)
+ * get token_req = -1, token_pos = 0, token_rows = -1.
+ *
+ *   cached_lens, new_lens : device int32 [n_req], read-only; n_req >= 0
+ *   free_slots   : device int32 [n_free], slots not in use, taken from the front
+ *   block_tables : device int32, entry j of request r at r * table_stride + j; the
+ *                  entries of held blocks are read, those of new blocks written
+ *   table_width  : entries per request; table_stride >= table_width
+ *   n_tokens     : entries of the token arrays (>= 0)
+ *   q_starts     : device int32 [n_req + 1];  kv_lens : device int32 [n_req]
+ *   token_req, token_pos : device int32 [n_tokens];  token_rows : device int64 [n_tokens]
+ *   n_taken      : device int32, free slots that were taken
+ *   err_flag     : HC_DEVERR_LENGTH: a negative length or a request longer than
+ *                  its table (it takes no slots, kv_lens[r] is 0, its new
+ *                  tokens get token_pos 0 and token_rows -1; a negative
+ *                  new_lens[r] counts as 0), or more new tokens than n_tokens
+ *                  (the rest is not written); HC_DEVERR_FREE: n_free is too
+ *                  few (the blocks without a slot get -1, their tokens row -1,
+ *                  and n_taken is n_free)
+ *   block_size   : 16, 32, 64 or 128
+ * All sums stay below 2^31 (precondition, not checked). */
+int hc_build_block_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t n_req,
+                          int32_t block_size, const int32_t* free_slots, int32_t n_free,
+                          int32_t* block_tables, int64_t table_stride, int32_t table_width,
+                          int32_t n_tokens, int32_t* q_starts, int32_t* kv_lens,
+                          int32_t* token_req, int32_t* token_pos, int64_t* token_rows,
+                          int32_t* n_taken, int32_t* err_flag, void* stream);
+
+/* hc_rope_axes: y = x with every pair (x1, x2) of its first rot_dim channels
+ * rotated by (c, s) = table[positions[pair_axis[i]][token]][i]:
+ *   y1 = x1*c - x2*s,  y2 = x1*s + x2*c        (inverse: s negated)
+ * in fp32, products and sums rounded one by one, then rounded once to dtype.
+ * The rest of a row is copied.  x and y may be the same tensor, and must not
+ * overlap otherwise.
+ *
+ *   dtype    : hc_dtype of x and y
+ *   n_tokens, n_heads : >= 0; 0 launches nothing
+ *   d_head   : 2..256
+ *   rope     : host pointer, read during the call only
+ *   err_flag : HC_DEVERR_POS: a token with a position outside the table is
+ *              skipped (its rows of y are left as they were)
+ * Rows whose base and strides are multiples of 16 bytes, with channels that
+ * split into 16-byte pieces, move in 16-byte pieces; others element by element. */
+int hc_rope_axes(const hc_rows* x, const hc_rows* y, int32_t dtype, int32_t n_tokens,
+                 int32_t n_heads, int32_t d_head, const hc_rope_axes_desc* rope,
+                 int32_t* err_flag, void* stream);
+
+/* hc_append_int4: the new tokens into the cache.  Queries and keys are
+ * rotated as by hc_rope_axes; q goes to q_out; the rotated keys (in fp32, with
+ * no rounding between) and the values are quantized per token, head and group
+ * and written to cache row token_rows[t]:
+ *   s32 = fp32(amax * fp32(1/7));  s = fp16_rne(s32) if scale_dtype == HC_F16, else s32;
+ *   code = clamp(round_half_even(fp32(x / s)), -7, 7) with the stored s, 0 if s == 0.
+ * hc_encode_int4 divides amax by 7: its fp32 scales may differ from these in
+ * the last bit, its fp16 scales of fp16 or bf16 elements do not for
+ * amax >= 1e-5.  A token with row -1 (a padded step) gets its q_out but no
+ * cache row.
+ *
+ *   q, q_out : [n_tokens][n_q_heads][d_head], or NULL with n_q_heads = 0
+ *   k, v     : [n_tokens][n_kv_heads][d_head]
+ *   dtype    : hc_dtype of q, k, v and q_out; all 16-byte aligned, strides
+ *              multiples of 16 bytes
+ *   rope     : as for hc_rope_axes, inverse = 0 and rot_dim a multiple of 16;
+ *              NULL: no rotation (q is copied)
+ *   token_rows : device int64 [n_tokens], distinct where >= 0 (precondition)
+ *   cache    : host pointer; codes, scales: device, written at the rows
+ *   err_flag : HC_DEVERR_SLOT: a row outside [-1, num_slots * block_size);
+ *              HC_DEVERR_POS: a position outside the table.  Such a token's
+ *              q_out and cache rows are left as they were.
+ */
+int hc_append_int4(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t dtype,
+                   int32_t n_tokens, int32_t n_q_heads, const hc_rope_axes_desc* rope,
+                   const int64_t* token_rows, const hc_int4_cache* cache, uint8_t* codes,
+                   void* scales, const hc_rows* q_out, int32_t* err_flag, void* stream);
+
+/* hc_attend_int4: attention of the new tokens over the 4-bit cache.  Request r
+ * has queries t in [q_starts[r], q_starts[r+1]), the last of its kv_lens[r]
+ * positions: query i of n has position p = kv_lens[r] - n + i.  It sees the
+ * keys j with 0 <= j < kv_lens[r], j <= p if causal, j > p - window if
+ * window > 0.  For query head h and cache head h / (n_q_heads / n_kv_heads):
+ *   x_j = softmax_scale * sum_c q[t][h][c] * K[j][c]
+ *   lse = log sum_j exp(x_j),  out[t][h] = sum_j exp(x_j - lse) * V[j]
+ * with K, V the values the codes and scales stand for.  A query that sees no
+ * key gets out = 0 and lse = -inf.  Cache rows that no query sees are not read
+ * into the result, whatever they hold.
+ *
+ *   q, out    : [n_tokens][n_q_heads][d_head], dtype HC_F16 or HC_BF16, 16-byte
+ *               aligned, strides multiples of 16 bytes; finite
+ *   lse       : device f32 [n_tokens][n_q_heads] or NULL
+ *   n_q_heads : a multiple of n_kv_heads
+ *   block_tables, table_stride, table_width, q_starts, kv_lens : as
+ *               hc_build_block_tables leaves them
+ *   max_new   : at least every request's number of queries
+ *   window    : 0 (none) or the number of positions a query sees, itself
+ *               included; needs causal
+ *   softmax_scale : finite
+ *   workspace : device, 256-byte aligned, zero before its first use; every
+ *               call leaves it ready for the next.  Calls that may run at the
+ *               same time need workspaces of their own.
+ *   workspace_bytes : hc_attend_int4_workspace() at least
+ *   err_flag  : HC_DEVERR_LENGTH: a request with more queries than max_new, or
+ *               than n_tokens holds, or a length outside its table: its rows of
+ *               out and lse are left as they were; HC_DEVERR_SLOT: a slot
+ *               outside the cache: its block is taken as zeros
+ * Keys and values enter the products as the codes they are, or as fp16 values
+ * (code times scale, scaled by a power of two); scores, softmax and sums are
+ * fp32; probabilities enter the second product in fp16. */
+int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dtype,
+                   int32_t n_tokens, int32_t n_q_heads, const hc_int4_cache* cache,
+                   const uint8_t* codes, const void* scales, const int32_t* block_tables,
+                   int64_t table_stride, int32_t table_width, const int32_t* q_starts,
+                   const int32_t* kv_lens, int32_t n_req, int32_t max_new, int32_t causal,
+                   int32_t window, float softmax_scale, void* workspace,
+                   int64_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* hc_attend_int4_workspace: bytes of workspace that any hc_attend_int4 call
+ * needs (a host function; the same on every call). */
+int64_t hc_attend_int4_workspace(void);
 
 /* Human-readable name of an hc_status value (static string, never NULL). */
 const char* hc_status_string(int32_t status);

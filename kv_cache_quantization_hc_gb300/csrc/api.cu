@@ -5,7 +5,7 @@
 #include <cstdio>
 #include <cstring>
 
-#include "hc_internal.cuh"
+#include "serve.cuh"
 
 namespace {
 
@@ -80,6 +80,10 @@ hc::EncodeParams encode_params(const void* k, const void* v, const hc_paged_desc
 }
 
 }  // namespace
+
+namespace hc {
+int record_cuda(cudaError_t e) { return record(e); }
+}  // namespace hc
 
 extern "C" {
 

@@ -1,0 +1,865 @@
+// Attention of the new tokens over the 4-bit cache, rows of few queries:
+// tensor-core products on the codes as they are, split over the keys.
+//
+// For a request and a cache head, the query rows are its new tokens times the
+// query heads that share the cache head.  A piece of work is up to 8 * NT of
+// those rows against all their keys.  The pieces of a call, laid end to end in
+// tiles of 128 keys, are cut into equal runs, one per CTA (4 warps, 32 keys
+// of a tile each), so requests of any lengths load the SMs alike; a CTA ends
+// a piece, starts the next, or does both.  A piece that one CTA holds whole
+// is written at once; otherwise each CTA leaves its partial sums in the
+// workspace and the last to arrive (a counter per piece) joins them, in the
+// order of the CTAs, so the result does not depend on which came last.
+//
+// Mathematics, per row, over tiles of keys with a running maximum m:
+//   x_j = c * sum_g s_jg * (q_g . n_jg - corr_g),  p_j = 2^(x_j - m - e),
+//   l = sum p_j,  O = sum (p_j * sv_jg) * nv_jg
+// with n the codes, s the scales of their groups and c = softmax_scale *
+// log2(e) * the power of two that the row's queries were scaled by.
+// * Keys as fp16 without conversion: the nibble u = code + 8, in the low
+//   bits of an fp16, is the subnormal u * 2^-24 exactly, so one AND-XOR makes
+//   two operands; the "+ 8" is the same for all keys, and corr_g = 8 * sum of
+//   q over the group, the products' starting value, takes it off again.
+//   Nibbles 1 and 5 of a word stay 4 bits up (16 u) against queries divided
+//   by 16.
+// * Queries as fp16: each row times a power of two that brings its largest
+//   value near 2^14, so that bf16's range fits and only values below 2^-28
+//   of the row's largest lose bits.
+// * Values as exact fp16 whole numbers.  Their scales go into the
+//   probabilities, which are rounded to fp16 once, after that product: 11
+//   bits against the 8 or 11 of the output.  2^e is the largest value scale
+//   seen, over 2^14: the products then fill fp16's range from the top.
+// * S^T = K Q^T and O^T = V^T P^T: keys and channels are the 16 rows of the
+//   matrix instruction, the queries its 8 columns, so a step of one query
+//   with 8 heads wastes nothing.
+//
+// Bound: the cache's bytes when rows are few (decoding).
+#include <algorithm>
+
+#include "serve.cuh"
+
+namespace hc {
+namespace {
+
+constexpr int kWarpsA = 4;
+constexpr int kKeysWarp = 32;                      // keys of one warp in a tile
+constexpr int kTile = kWarpsA * kKeysWarp;         // keys of a tile
+constexpr int kStages = 3;
+constexpr int kCtasPerSm = 4;
+constexpr int kMaxCtas = 1024;                     // counters in the workspace
+constexpr int kMaxRows = 16;                       // rows of a piece
+constexpr int kPartialFloats = kMaxRows * (128 + 2);
+constexpr float kNegInf = -INFINITY;
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes));
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// (w & mask) ^ flip, one LOP3
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t flip) {
+  return (w & mask) ^ flip;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+// Signed codes of nibbles 0 and 4 (resp. 1 and 5) of w as fp16: 1024 + u in
+// the mantissa, u = code + 8, less 1032; or 1024 + 16 u, over 16, less 72.
+__device__ __forceinline__ uint32_t codes_04(uint32_t w) {
+  const uint32_t m = and_xor(w, 0x000f000fu, 0x64086408u);
+  __half2 h;
+  memcpy(&h, &m, 4);
+  h = __hsub2(h, __half2half2(__ushort_as_half(0x6408)));
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+__device__ __forceinline__ uint32_t codes_15(uint32_t w) {
+  const uint32_t m = and_xor(w, 0x00f000f0u, 0x64806480u);
+  __half2 h;
+  memcpy(&h, &m, 4);
+  h = __hfma2(h, __half2half2(__ushort_as_half(0x2c00)), __half2half2(__ushort_as_half(0xd480)));
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+
+// A request as the call sees it; n = 0 where there is nothing to write.
+struct Request {
+  int q0, n, kv;
+};
+__device__ __forceinline__ Request load_request(const AttendParams& p, int r, int& bad) {
+  Request q;
+  q.q0 = __ldg(p.q_starts + r);
+  q.n = __ldg(p.q_starts + r + 1) - q.q0;
+  q.kv = __ldg(p.kv_lens + r);
+  const bool ok = q.n >= 0 && q.n <= p.max_new && q.q0 >= 0 && q.q0 <= p.n_tokens - q.n && q.kv >= 0 &&
+                  q.kv <= (static_cast<int64_t>(p.table_width) << p.B_log2);
+  if (!ok) {
+    bad |= HC_DEVERR_LENGTH;
+    q.q0 = q.n = q.kv = 0;
+  }
+  return q;
+}
+
+// Keys [lo, hi) that some of the rows [row0, row1) see, and their tiles.
+struct Range {
+  int lo, hi, tile0, tiles;
+};
+__device__ __forceinline__ Range visible(const AttendParams& p, const Request& q, int row0, int row1) {
+  const int i0 = static_cast<int>(p.by_group.div(row0)), i1 = static_cast<int>(p.by_group.div(row1 - 1));
+  Range v;
+  v.hi = p.causal ? min(q.kv, q.kv - q.n + i1 + 1) : q.kv;
+  v.lo = p.window ? max(0, q.kv - q.n + i0 - p.window + 1) : 0;
+  if (v.lo >= v.hi) v.lo = v.hi = 0;
+  v.tile0 = v.lo / kTile;
+  v.tiles = max(1, (v.hi + kTile - 1) / kTile - v.tile0);  // a piece without keys still writes its rows
+  return v;
+}
+
+template <int kRows>
+__device__ __forceinline__ int request_units(const AttendParams& p, const Request& q) {
+  int units = 0;
+  for (int r0 = 0, rows = q.n * p.G; r0 < rows; r0 += kRows)
+    units += visible(p, q, r0, min(r0 + kRows, rows)).tiles;
+  return units * p.H;
+}
+
+template <int D, int GROUP, bool kScaleF16>
+struct Layout {
+  static constexpr int kRowBytes = D / 2;
+  static constexpr int kRowChunks = kRowBytes / 16;
+  static constexpr int kGroups = D / GROUP;
+  static constexpr int kScaleBytes = kGroups * (kScaleF16 ? 2 : 4);  // of one key
+  static constexpr int kCodeBytes = kKeysWarp * kRowBytes;           // K or V of a stage
+  static constexpr int kScaleStage = kKeysWarp * kScaleBytes;
+  static constexpr int kStageBytes = 2 * kCodeBytes + 2 * kScaleStage;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+};
+
+// A 16-byte piece's place in a row of codes: rows that ldmatrix reads
+// together fall into different banks.
+template <int D>
+__device__ __forceinline__ int swizzled(int key, int chunk) {
+  return D == 128 ? chunk ^ ((key >> 1) & 3) : chunk ^ ((key >> 2) & 1);
+}
+
+template <int kGroups, bool kScaleF16>
+__device__ __forceinline__ void load_scales(float (&s)[kGroups], const unsigned char* base, int key) {
+  if constexpr (kScaleF16) {
+    const __half* h = reinterpret_cast<const __half*>(base) + key * kGroups;
+    if constexpr (kGroups == 4) {
+      const uint2 w = *reinterpret_cast<const uint2*>(h);
+      const float2 a = u32_to_float2(w.x, static_cast<const __half*>(nullptr));
+      const float2 b = u32_to_float2(w.y, static_cast<const __half*>(nullptr));
+      s[0] = a.x, s[1] = a.y, s[2] = b.x, s[3] = b.y;
+    } else if constexpr (kGroups == 2) {
+      const float2 a = u32_to_float2(*reinterpret_cast<const uint32_t*>(h), static_cast<const __half*>(nullptr));
+      s[0] = a.x, s[1] = a.y;
+    } else {
+      s[0] = __half2float(*h);
+    }
+  } else {
+    const float* f = reinterpret_cast<const float*>(base) + key * kGroups;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) s[g] = f[g];
+  }
+}
+
+struct Shared {
+  int32_t r, off;  // the request and the offset in it where the CTA's run starts
+  uint32_t warp[kWarpsA];
+  int32_t last;
+  float m[kWarpsA][kMaxRows], l[kWarpsA][kMaxRows];
+  float wt[kMaxRows], inv[kMaxRows];
+};
+
+template <int D, int GROUP, bool kScaleF16, int NT>
+__global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
+    k_attend_rows(const __grid_constant__ AttendParams p) {
+  using L = Layout<D, GROUP, kScaleF16>;
+  constexpr int kRows = 8 * NT;
+  constexpr int kChunks = D / 32;                 // 16-byte pieces of a row: 32 channels each
+  constexpr int kGroups = L::kGroups;
+  constexpr int kChunksPerGroup = GROUP / 32;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  unsigned char* stages = dyn + warp * L::kWarpBytes;
+  const uint32_t stages_addr = smem_addr(stages);
+  int bad = 0;
+
+  // ---- this CTA's run of tiles
+  const int per = (p.n_req + kWarpsA * 32 - 1) / (kWarpsA * 32);
+  const int r_first = tid * per, r_last = min(r_first + per, p.n_req);
+  uint32_t mine = 0;
+  for (int r = r_first; r < r_last; ++r) mine += request_units<kRows>(p, load_request(p, r, bad));
+  uint32_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sh.warp[warp] = inc;
+  if (tid == 0) sh.r = -1;
+  __syncthreads();
+  uint32_t before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarpsA; ++w) {
+    if (w < warp) before += sh.warp[w];
+    total += sh.warp[w];
+  }
+  const uint32_t ctas = gridDim.x, b = blockIdx.x;
+  const uint32_t share = total / ctas, extra = total - share * ctas;
+  const uint32_t begin = b * share + min(b, extra), end = begin + share + (b < extra ? 1u : 0u);
+  if (b == 0) flag_error(p.err, bad);
+  bad = 0;
+  if (begin == end) return;
+  if (before <= begin && begin < before + mine) {
+    uint32_t at = before;
+    for (int r = r_first; r < r_last; ++r) {
+      const uint32_t u = request_units<kRows>(p, load_request(p, r, bad));
+      if (begin < at + u) {
+        sh.r = r;
+        sh.off = static_cast<int>(begin - at);
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+  bad = 0;
+
+  // ---- the pieces of the run
+  int r = sh.r, off = sh.off, row0 = 0, head = 0;
+  if (r < 0) return;
+  Request rq = load_request(p, r, bad);
+  int rows_all = rq.n * p.G;
+  Range vis = visible(p, rq, 0, min(kRows, rows_all));
+  for (;;) {  // to the piece that holds `off`: rows outermost, then heads
+    if (off < vis.tiles * p.H) {
+      head = off / vis.tiles;
+      off -= head * vis.tiles;
+      break;
+    }
+    off -= vis.tiles * p.H;
+    row0 += kRows;
+    if (row0 >= rows_all) return;  // never, unless the lengths change under the kernel
+    vis = visible(p, rq, row0, min(row0 + kRows, rows_all));
+  }
+
+  for (uint32_t unit = begin; unit < end;) {
+    const int seg = static_cast<int>(min(end - unit, static_cast<uint32_t>(vis.tiles - off)));
+    const int rows = min(kRows, rows_all - row0);
+
+    // -- queries: fragments, the correction of the codes' offset, row factors
+    uint32_t qf[NT][kChunks][4];
+    float corr[NT][kGroups][2], factor[NT][2];
+    int lo_row[NT][2], hi_row[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + nt * 8 + g;
+      const bool live = row < rows_all;
+      float f[kChunks][8];
+      float amax = 0.f;
+      const int i = static_cast<int>(p.by_group.div(live ? row : 0));
+      const int64_t at = static_cast<int64_t>(rq.q0 + i) * p.q_token +
+                         static_cast<int64_t>(head * p.G + (live ? row : 0) - i * p.G) * p.q_head;
+#pragma unroll
+      for (int cc = 0; cc < kChunks; ++cc) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (live)
+          w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + cc * 32 + t * 8);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = p.bf16 ? u32_to_float2(u[k], static_cast<const __nv_bfloat16*>(nullptr))
+                                  : u32_to_float2(u[k], static_cast<const __half*>(nullptr));
+          f[cc][2 * k] = v.x;
+          f[cc][2 * k + 1] = v.y;
+          amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+        }
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 2^e <= amax < 2^(e+1); queries times 2^(14-e)
+      const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100), 100);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+      float sum[kGroups];
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) sum[k] = 0.f;
+#pragma unroll
+      for (int cc = 0; cc < kChunks; ++cc) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = f[cc][k] * up * ((k & 1) ? 0.0625f : 1.f);
+        qf[nt][cc][0] = pack_f16(x[0], x[4]);
+        qf[nt][cc][1] = pack_f16(x[1], x[5]);
+        qf[nt][cc][2] = pack_f16(x[2], x[6]);
+        qf[nt][cc][3] = pack_f16(x[3], x[7]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = u32_to_float2(qf[nt][cc][k], static_cast<const __half*>(nullptr));
+          sum[cc / kChunksPerGroup] += (v.x + v.y) * ((k & 1) ? 16.f : 1.f);
+        }
+      }
+      const float fac = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 10 + e) << 23);  // 2^(24-14+e)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int src = (2 * t + j) * 4;
+        factor[nt][j] = __shfl_sync(0xffffffffu, fac, src);
+        const int rj = row0 + nt * 8 + 2 * t + j;
+        const int pos = rq.kv - rq.n + static_cast<int>(p.by_group.div(min(rj, rows_all - 1)));
+        hi_row[nt][j] = p.causal ? min(rq.kv, pos + 1) : rq.kv;
+        lo_row[nt][j] = p.window ? pos - p.window + 1 : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
+        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
+        sum[k] *= -8.f * 0x1p-24f;
+        corr[nt][k][0] = __shfl_sync(0xffffffffu, sum[k], (2 * t) * 4);
+        corr[nt][k][1] = __shfl_sync(0xffffffffu, sum[k], (2 * t + 1) * 4);
+      }
+    }
+    // keys that every row sees: no mask needed inside
+    int all_lo, all_hi;
+    {
+      const int i0 = static_cast<int>(p.by_group.div(row0)), i1 = static_cast<int>(p.by_group.div(row0 + rows - 1));
+      all_hi = p.causal ? min(rq.kv, rq.kv - rq.n + i0 + 1) : rq.kv;
+      all_lo = p.window ? max(0, rq.kv - rq.n + i1 - p.window + 1) : 0;
+    }
+
+    float o[NT][D / 16][4], m[NT][2], l[NT][2];
+    float er = -100.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[nt][c][j] = 0.f;
+      m[nt][0] = m[nt][1] = kNegInf;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    const int32_t* table = p.tables + static_cast<int64_t>(r) * p.table_stride;
+    const int key_first = (vis.tile0 + off) * kTile + warp * kKeysWarp;
+    // the slots of a tile's two runs of 16 keys; -1: no visible key, or no such slot
+    auto load_slots = [&](int i, int (&slot)[2]) {
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb) {
+        const int key = key_first + i * kTile + sb * 16;
+        slot[sb] = -1;
+        if (i < seg && key < vis.hi && key + 16 > vis.lo) {
+          slot[sb] = __ldg(table + (key >> p.B_log2));
+          if (static_cast<uint32_t>(slot[sb]) >= static_cast<uint32_t>(p.num_slots)) {
+            bad |= HC_DEVERR_SLOT;
+            slot[sb] = -1;
+          }
+        }
+      }
+    };
+    auto load_tile = [&](int i, const int (&slot)[2]) {
+      const uint32_t st = stages_addr + (i % kStages) * L::kStageBytes;
+      const int key0 = key_first + i * kTile;
+      int64_t at[2];  // row of the run's first key among all K rows of the cache
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb)
+        at[sb] = (((static_cast<int64_t>(slot[sb]) * 2) * p.H + head) << p.B_log2) +
+                 ((key0 + sb * 16) & ((1 << p.B_log2) - 1));
+      const int64_t to_v = static_cast<int64_t>(p.H) << p.B_log2;
+#pragma unroll
+      for (int it = 0; it < L::kCodeBytes / 512; ++it) {
+        const int id = it * 32 + lane, key = id / L::kRowChunks, chunk = id % L::kRowChunks;
+        const int sb = key >> 4;
+        const bool in = slot[sb] >= 0 && key0 + key < vis.hi;
+        const uint8_t* src = in ? p.codes + (at[sb] + (key & 15)) * L::kRowBytes + chunk * 16 : p.codes;
+        const uint32_t dst = st + key * L::kRowBytes + swizzled<D>(key, chunk) * 16;
+        cp_async16(dst, src, in ? 16 : 0);
+        cp_async16(dst + L::kCodeBytes, in ? src + to_v * L::kRowBytes : src, in ? 16 : 0);
+      }
+      constexpr int kScaleChunks = L::kScaleStage / 16;  // of K; as many of V
+#pragma unroll
+      for (int id0 = 0; id0 < kScaleChunks; id0 += 32) {
+        const int id = id0 + lane;
+        if (id < kScaleChunks) {
+          const int sb = id / (kScaleChunks / 2);
+          const int first = sb * 16 + (id % (kScaleChunks / 2)) * 16 / L::kScaleBytes;  // key of the piece
+          const int left = slot[sb] >= 0 ? min(16, max(0, vis.hi - key0 - first) * L::kScaleBytes) : 0;
+          const unsigned char* base = static_cast<const unsigned char*>(p.scales);
+          const unsigned char* src = left > 0 ? base + at[sb] * L::kScaleBytes + (id % (kScaleChunks / 2)) * 16 : base;
+          const uint32_t dst = st + 2 * L::kCodeBytes + id * 16;
+          cp_async16(dst, src, left);
+          cp_async16(dst + L::kScaleStage, left > 0 ? src + to_v * L::kScaleBytes : src, left);
+        }
+      }
+    };
+
+    int slot[2];
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      load_slots(i, slot);
+      if (i < seg) load_tile(i, slot);
+      cp_async_commit();
+    }
+    load_slots(kStages - 1, slot);
+
+    for (int i = 0; i < seg; ++i) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      if (i + kStages - 1 < seg) load_tile(i + kStages - 1, slot);
+      cp_async_commit();
+      load_slots(i + kStages, slot);
+
+      const int key0 = key_first + i * kTile;
+      if (key0 >= vis.hi || key0 + kKeysWarp <= vis.lo) continue;
+      const unsigned char* stage = stages + (i % kStages) * L::kStageBytes;
+      const uint32_t ks = smem_addr(stage), vs = ks + L::kCodeBytes;
+      const unsigned char* k_scale = stage + 2 * L::kCodeBytes;
+      const unsigned char* v_scale = k_scale + L::kScaleStage;
+
+      // -- scores: S^T[key][row], keys g and g + 8 of each run of 16
+      float s[NT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t kw[2][kChunks];  // words of keys g and g + 8: word t of each 16-byte piece
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if constexpr (D == 128) {
+            const int key = mt * 16 + hf * 8 + (lane & 7);
+            uint32_t w[4];
+            ldmatrix4(w, ks + key * L::kRowBytes + swizzled<D>(key, lane >> 3) * 16);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) kw[hf][c] = w[c];
+          }
+        }
+        if constexpr (D == 64) {
+          const int key = mt * 16 + ((lane >> 4) & 1) * 8 + (lane & 7);
+          uint32_t w[4];
+          ldmatrix4(w, ks + key * L::kRowBytes + swizzled<D>(key, (lane >> 3) & 1) * 16);
+          kw[0][0] = w[0], kw[0][1] = w[1], kw[1][0] = w[2], kw[1][1] = w[3];
+        }
+        float sk[2][kGroups];
+        load_scales<kGroups, kScaleF16>(sk[0], k_scale, mt * 16 + g);
+        load_scales<kGroups, kScaleF16>(sk[1], k_scale, mt * 16 + g + 8);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[nt][mt][j] = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr) {
+          float acc[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            acc[nt][0] = acc[nt][2] = corr[nt][gr][0];
+            acc[nt][1] = acc[nt][3] = corr[nt][gr][1];
+          }
+#pragma unroll
+          for (int c = gr * kChunksPerGroup; c < (gr + 1) * kChunksPerGroup; ++c) {
+            const uint32_t w0 = kw[0][c], w1 = kw[1][c], x0 = w0 >> 8, x1 = w1 >> 8;
+            const uint32_t a0 = and_xor(w0, 0x000f000fu, 0x00080008u), a1 = and_xor(w1, 0x000f000fu, 0x00080008u);
+            const uint32_t a2 = and_xor(w0, 0x00f000f0u, 0x00800080u), a3 = and_xor(w1, 0x00f000f0u, 0x00800080u);
+            const uint32_t b0 = and_xor(x0, 0x000f000fu, 0x00080008u), b1 = and_xor(x1, 0x000f000fu, 0x00080008u);
+            const uint32_t b2 = and_xor(x0, 0x00f000f0u, 0x00800080u), b3 = and_xor(x1, 0x00f000f0u, 0x00800080u);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(acc[nt], a0, a1, a2, a3, qf[nt][c][0], qf[nt][c][1]);
+              mma16816(acc[nt], b0, b1, b2, b3, qf[nt][c][2], qf[nt][c][3]);
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[nt][mt][j] = fmaf(acc[nt][j], sk[j >> 1][gr], s[nt][mt][j]);
+        }
+      }
+
+      // -- the value scales of this lane's keys, their largest so far and the tile's smallest
+      float sv[2][2][kGroups];
+      float top = 0.f, low = INFINITY;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          load_scales<kGroups, kScaleF16>(sv[mt][hf], v_scale, mt * 16 + hf * 8 + g);
+#pragma unroll
+          for (int gr = 0; gr < kGroups; ++gr) {
+            top = fmaxf(top, sv[mt][hf][gr]);
+            low = fminf(low, sv[mt][hf][gr]);
+          }
+        }
+      const uint32_t top_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+      low = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(low)));
+      const float er_new = fmaxf(er, static_cast<float>(static_cast<int>(top_bits >> 23) - 127 - 14));
+
+      // -- running maximum, probabilities
+      const bool masked = key0 < all_lo || key0 + kKeysWarp > all_hi;
+      float m_new[NT][2];
+      bool changed = er_new != er;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float top_x = kNegInf;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float x = s[nt][mt][hf * 2 + j] * factor[nt][j];
+              const int key = key0 + mt * 16 + hf * 8 + g;
+              if (masked && (key < lo_row[nt][j] || key >= hi_row[nt][j])) x = kNegInf;
+              s[nt][mt][hf * 2 + j] = x;
+              top_x = fmaxf(top_x, x);
+            }
+          top_x = fmaxf(top_x, __shfl_xor_sync(0xffffffffu, top_x, 4));
+          top_x = fmaxf(top_x, __shfl_xor_sync(0xffffffffu, top_x, 8));
+          top_x = fmaxf(top_x, __shfl_xor_sync(0xffffffffu, top_x, 16));
+          m_new[nt][j] = fmaxf(m[nt][j], top_x);
+          changed = changed || m_new[nt][j] != m[nt][j];
+        }
+      }
+      if (__any_sync(0xffffffffu, changed)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            // nothing seen so far: l and O are 0, whatever they are multiplied by
+            const float alpha = m[nt][j] == kNegInf ? 0.f : ex2((m[nt][j] - m_new[nt][j]) + (er - er_new));
+            l[nt][j] *= alpha;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              o[nt][c][j] *= alpha;
+              o[nt][c][2 + j] *= alpha;
+            }
+            m[nt][j] = m_new[nt][j];
+          }
+        er = er_new;
+      }
+      float p_low = INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float ref = m[nt][j] == kNegInf ? 0.f : m[nt][j] + er;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const float e = ex2(s[nt][mt][hf * 2 + j] - ref);
+              s[nt][mt][hf * 2 + j] = e;
+              l[nt][j] += e;
+              p_low = fminf(p_low, e);
+            }
+        }
+
+      // -- O^T += V^T P^T, 16 keys at a time
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const int key = mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int cp = 0; cp < kChunks / 2; ++cp) {  // two 16-byte pieces: 64 channels
+          uint32_t w[4];
+          ldmatrix4_trans(w, vs + key * L::kRowBytes + swizzled<D>(key, cp * 2 + (lane >> 4)) * 16);
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2) {
+            const int c = cp * 2 + h2;
+            if (c % kChunksPerGroup == 0) {
+              const int gr = c / kChunksPerGroup;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                  pb[nt][hf] = movmatrix_trans(pack_f16(s[nt][mt][hf * 2] * sv[mt][hf][gr],
+                                                        s[nt][mt][hf * 2 + 1] * sv[mt][hf][gr]));
+            }
+            const uint32_t w0 = w[h2 * 2], w1 = w[h2 * 2 + 1], x0 = w0 >> 8, x1 = w1 >> 8;
+            const uint32_t a0 = codes_04(w0), a1 = codes_15(w0), a2 = codes_04(w1), a3 = codes_15(w1);
+            const uint32_t b0 = codes_04(x0), b1 = codes_15(x0), b2 = codes_04(x1), b3 = codes_15(x1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(o[nt][2 * c], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+              mma16816(o[nt][2 * c + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+            }
+          }
+        }
+      }
+
+      // -- products below fp16's normal range (2^-29 of the largest) lost bits or all of themselves:
+      // what was lost, 2^39 times as large, goes through the same steps.  It matters only to a channel
+      // in which the keys with larger probabilities hold zeros.
+      if (__any_sync(0xffffffffu, p_low * low < 0x1p-14f)) {
+        float down = 0x1p-39f;
+        for (int range = 0; range < 3; ++range, down *= 0x1p-39f) {
+          bool some = false;
+#pragma unroll 1
+          for (int mt = 0; mt < 2; ++mt) {
+            const int key = mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll 1
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t pb[2] = {0, 0};
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c) {
+                if (c % kChunksPerGroup == 0) {
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf) {
+                    float v[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                      const float pe = NT == 1 ? (mt ? s[0][1][hf * 2 + j] : s[0][0][hf * 2 + j])
+                                               : (nt ? (mt ? s[NT - 1][1][hf * 2 + j] : s[NT - 1][0][hf * 2 + j])
+                                                     : (mt ? s[0][1][hf * 2 + j] : s[0][0][hf * 2 + j]));
+                      const float sc = mt ? sv[1][hf][c / kChunksPerGroup] : sv[0][hf][c / kChunksPerGroup];
+                      v[j] = pe * sc;
+                      for (int k = 0; k <= range; ++k)  // a normal fp16 has lost no more than its rounding
+                        v[j] = fabsf(v[j]) >= 0x1p-14f ? 0.f : (v[j] - __half2float(__float2half_rn(v[j]))) * 0x1p39f;
+                      some = some || v[j] != 0.f;
+                    }
+                    pb[hf] = movmatrix_trans(pack_f16(v[0], v[1]));
+                  }
+                }
+                uint32_t w[4];
+                ldmatrix4_trans(w, vs + key * L::kRowBytes + swizzled<D>(key, (c & ~1) + (lane >> 4)) * 16);
+                const uint32_t w0 = w[(c & 1) * 2], w1 = w[(c & 1) * 2 + 1], x0 = w0 >> 8, x1 = w1 >> 8;
+                float add[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                mma16816(add[0], codes_04(w0), codes_15(w0), codes_04(w1), codes_15(w1), pb[0], pb[1]);
+                mma16816(add[1], codes_04(x0), codes_15(x0), codes_04(x1), codes_15(x1), pb[0], pb[1]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const float a = add[u][j] * down;
+                    o[0][2 * c + u][j] += nt == 0 ? a : 0.f;
+                    if (NT > 1) o[NT - 1][2 * c + u][j] += nt == 1 ? a : 0.f;
+                  }
+              }
+            }
+          }
+          if (!__any_sync(0xffffffffu, some)) break;
+        }
+      }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+
+    // ---- the warps' sums joined: O in shared memory, [warp][row][channel]
+    float* so = reinterpret_cast<float*>(dyn);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float sum = l[nt][j];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int row = nt * 8 + 2 * t + j;
+        if (g == 0) {
+          sh.m[warp][row] = m[nt][j] == kNegInf ? kNegInf : m[nt][j] + er;
+          sh.l[warp][row] = sum;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const int ch = (c >> 1) * 32 + 4 * g + 2 * (c & 1);
+          *reinterpret_cast<float2*>(so + (warp * kRows + row) * D + ch) = make_float2(o[nt][c][j], o[nt][c][2 + j]);
+        }
+      }
+    __syncthreads();
+    const bool whole = off == 0 && seg == vis.tiles;
+    float* ws = reinterpret_cast<float*>(p.workspace + kMaxCtas * sizeof(int32_t));
+    int32_t* counters = reinterpret_cast<int32_t*>(p.workspace);
+    float* partial = ws + (static_cast<int64_t>(b) * 2 + (off > 0 ? 0 : 1)) * kPartialFloats;
+
+    auto write_row = [&](int row, int ch, float4 v, float mref, float sum) {
+      // v: unnormalised sums of 4 channels
+      const int rr = row0 + row, i = static_cast<int>(p.by_group.div(rr)), h = head * p.G + rr - i * p.G;
+      const int64_t tok = rq.q0 + i;
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      uint2 w;
+      if (p.bf16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * inv, v.y * inv), c = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+        memcpy(&w.x, &a, 4);
+        memcpy(&w.y, &c, 4);
+      } else {
+        w.x = pack_f16(v.x * inv, v.y * inv);
+        w.y = pack_f16(v.z * inv, v.w * inv);
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + tok * p.o_token + h * p.o_head + ch) = w;
+      if (p.lse && ch == 0)
+        p.lse[tok * (static_cast<int64_t>(p.H) * p.G) + h] = sum > 0.f ? (mref + log2f(sum)) * 0.6931471805599453f : kNegInf;
+    };
+
+    for (int id = tid; id < rows * (D / 4); id += kWarpsA * 32) {
+      const int row = id / (D / 4), ch = (id % (D / 4)) * 4;
+      float top = kNegInf, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarpsA; ++w) top = fmaxf(top, sh.m[w][row]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarpsA; ++w) {
+        const float wt = sh.m[w][row] == kNegInf ? 0.f : ex2(sh.m[w][row] - top);
+        const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + row) * D + ch);
+        sum += wt * sh.l[w][row];
+        acc.x += wt * v.x, acc.y += wt * v.y, acc.z += wt * v.z, acc.w += wt * v.w;
+      }
+      if (whole) {
+        write_row(row, ch, acc, top, sum);
+      } else {
+        __stcg(reinterpret_cast<float4*>(partial + 2 * kMaxRows + row * D + ch), acc);
+        if (ch == 0) {
+          __stcg(partial + row, top);
+          __stcg(partial + kMaxRows + row, sum);
+        }
+      }
+    }
+    if (!whole) {
+      // the CTAs that hold a part of this piece: first to last
+      const uint32_t u0 = unit - off, u1 = u0 + vis.tiles - 1;
+      auto owner = [&](uint32_t u) {
+        const uint32_t big = extra * (share + 1);
+        return u < big ? u / (share + 1) : extra + (u - big) / share;
+      };
+      const uint32_t c0 = owner(u0), c1 = owner(u1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int arrived = atomicAdd(counters + c0, 1);
+        sh.last = arrived == static_cast<int>(c1 - c0);
+        if (sh.last) counters[c0] = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      if (sh.last) {
+        auto part = [&](uint32_t c) { return ws + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kPartialFloats; };
+        for (int row = warp; row < rows; row += kWarpsA) {
+          float top = kNegInf, sum = 0.f;
+          for (uint32_t c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, __ldcg(part(c) + row));
+#pragma unroll
+          for (int o2 = 16; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+          for (uint32_t c = c0 + lane; c <= c1; c += 32) {
+            const float mc = __ldcg(part(c) + row);
+            if (mc != kNegInf) sum += ex2(mc - top) * __ldcg(part(c) + kMaxRows + row);
+          }
+#pragma unroll
+          for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
+          if (lane == 0) {
+            sh.wt[row] = top;
+            sh.inv[row] = sum;
+          }
+        }
+        __syncthreads();
+        for (int id = tid; id < rows * (D / 4); id += kWarpsA * 32) {
+          const int row = id / (D / 4), ch = (id % (D / 4)) * 4;
+          const float top = sh.wt[row];
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (uint32_t c = c0; c <= c1; ++c) {
+            const float mc = __ldcg(part(c) + row);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(part(c) + 2 * kMaxRows + row * D + ch));
+            const float wt = mc == kNegInf ? 0.f : ex2(mc - top);
+            acc.x += wt * v.x, acc.y += wt * v.y, acc.z += wt * v.z, acc.w += wt * v.w;
+          }
+          write_row(row, ch, acc, top, sh.inv[row]);
+        }
+      }
+    }
+
+    // ---- the next piece
+    unit += seg;
+    off = 0;
+    if (unit < end) {
+      if (++head == p.H) {
+        head = 0;
+        row0 += kRows;
+        while (row0 >= rows_all) {
+          if (++r >= p.n_req) return;  // likewise
+          rq = load_request(p, r, bad);
+          bad &= ~HC_DEVERR_LENGTH;  // CTA 0 reports these
+          rows_all = rq.n * p.G;
+          row0 = rows_all > 0 ? 0 : 1;
+        }
+        vis = visible(p, rq, row0, min(row0 + kRows, rows_all));
+      }
+    }
+    __syncthreads();
+  }
+  if (lane == 0) flag_error(p.err, bad & HC_DEVERR_SLOT);
+}
+
+template <int D, int GROUP, bool kScaleF16, int NT>
+cudaError_t launch_rows(const AttendParams& p, cudaStream_t s) {
+  using L = Layout<D, GROUP, kScaleF16>;
+  const int smem = std::max(kWarpsA * L::kWarpBytes, kWarpsA * 8 * NT * D * 4);
+  cudaError_t e = cudaFuncSetAttribute(k_attend_rows<D, GROUP, kScaleF16, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  int per_sm = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_attend_rows<D, GROUP, kScaleF16, NT>, kWarpsA * 32, smem);
+  if (e != cudaSuccess) return e;
+  // one CTA per resident place, or per tile where there are fewer (as far as the host can tell)
+  const int64_t rows = (static_cast<int64_t>(p.max_new) * p.G + 8 * NT - 1) / (8 * NT);
+  const int64_t keys = static_cast<int64_t>(p.table_width) << p.B_log2;
+  const int64_t tiles = std::max<int64_t>(1, (keys + kTile - 1) / kTile);
+  int64_t grid = std::min<int64_t>(kMaxCtas, static_cast<int64_t>(device_sm_count()) * std::max(1, per_sm));
+  if (static_cast<double>(p.n_req) * p.H * rows * tiles < static_cast<double>(grid))
+    grid = p.n_req * p.H * rows * tiles;
+  k_attend_rows<D, GROUP, kScaleF16, NT><<<static_cast<unsigned>(grid), kWarpsA * 32, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, int GROUP, bool kScaleF16>
+cudaError_t launch_nt(const AttendParams& p, cudaStream_t s) {
+  return static_cast<int64_t>(p.max_new) * p.G <= 8 ? launch_rows<D, GROUP, kScaleF16, 1>(p, s)
+                                                    : launch_rows<D, GROUP, kScaleF16, 2>(p, s);
+}
+
+template <int D, int GROUP>
+cudaError_t launch_scale(bool scale_f16, const AttendParams& p, cudaStream_t s) {
+  return scale_f16 ? launch_nt<D, GROUP, true>(p, s) : launch_nt<D, GROUP, false>(p, s);
+}
+
+}  // namespace
+
+int64_t attend_workspace_bytes() {
+  return kMaxCtas * static_cast<int64_t>(sizeof(int32_t)) +
+         static_cast<int64_t>(kMaxCtas) * 2 * kPartialFloats * static_cast<int64_t>(sizeof(float));
+}
+
+cudaError_t launch_attend_int4(int d, int group, bool scale_f16, const AttendParams& p, cudaStream_t s) {
+  if (d == 64) return group == 32 ? launch_scale<64, 32>(scale_f16, p, s) : launch_scale<64, 64>(scale_f16, p, s);
+  if (group == 32) return launch_scale<128, 32>(scale_f16, p, s);
+  return group == 64 ? launch_scale<128, 64>(scale_f16, p, s) : launch_scale<128, 128>(scale_f16, p, s);
+}
+
+}  // namespace hc

@@ -1,0 +1,65 @@
+// Rotary positions with several axes: y = x with the pairs of its rows turned.
+// Memory-bound (each element read and written once).  A warp takes one
+// token's rows, or a part of its heads where there are few tokens: the
+// token's (cos, sin), gathered from as many rows of the table as there are
+// axes, goes to shared memory once and serves all of them.
+#include "rope.cuh"
+
+namespace hc {
+namespace {
+
+template <typename T, int kPairing, int V>
+__global__ void __launch_bounds__(kRopeWarps * 32) k_rope_axes(const __grid_constant__ RopeAxesParams p) {
+  __shared__ float2 cs[kRopeWarps][128];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
+  const int64_t t = w / p.parts;
+  if (t >= p.n_tokens) return;
+  const int h0 = static_cast<int>(w - t * p.parts) * p.heads_per_warp;
+  const int h1 = min(h0 + p.heads_per_warp, p.n_heads);
+  if (!stage_cos_sin(p.rope, static_cast<int>(t), lane, cs[warp])) {
+    if (lane == 0) flag_error(p.err, HC_DEVERR_POS);
+    return;
+  }
+  rotate_rows<T, kPairing, V, 4>(static_cast<const T*>(p.x) + t * p.x_token, p.x_head,
+                                 static_cast<T*>(p.y) + t * p.y_token, p.y_head, h0, h1, p.rope.half,
+                                 cs[warp], p.items_per_row, lane);
+}
+
+template <typename T, int kPairing, int V>
+cudaError_t launch(RopeAxesParams p, cudaStream_t s) {
+  const int items = rope_items<kPairing, V>(p.rope.half, p.d);
+  p.items_per_row = FastDivmod(static_cast<uint32_t>(items));
+  // Heads of a token are shared out among warps until the GPU has about 24
+  // warps per SM, or a warp has no more than one item per lane.
+  p.heads_per_warp = p.n_heads;
+  const int64_t enough = static_cast<int64_t>(device_sm_count()) * 24;
+  while (p.heads_per_warp > 1 && static_cast<int64_t>(p.heads_per_warp) * items > 32 &&
+         static_cast<int64_t>(p.n_tokens) * ((p.n_heads + p.heads_per_warp - 1) / p.heads_per_warp) < enough)
+    p.heads_per_warp = (p.heads_per_warp + 1) / 2;
+  p.parts = (p.n_heads + p.heads_per_warp - 1) / p.heads_per_warp;
+  const int64_t warps = static_cast<int64_t>(p.n_tokens) * p.parts;
+  k_rope_axes<T, kPairing, V><<<static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps), kRopeWarps * 32, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_dtype(int pairing, bool pieces16, const RopeAxesParams& p, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  if (pairing == HC_PAIR_HALF_SPLIT)
+    return pieces16 ? launch<T, HC_PAIR_HALF_SPLIT, V>(p, s) : launch<T, HC_PAIR_HALF_SPLIT, 1>(p, s);
+  return pieces16 ? launch<T, HC_PAIR_INTERLEAVED, V>(p, s) : launch<T, HC_PAIR_INTERLEAVED, 2>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_axes(int dtype, int pairing, bool pieces16, const RopeAxesParams& p,
+                             cudaStream_t s) {
+  switch (dtype) {
+    case HC_F32: return launch_dtype<float>(pairing, pieces16, p, s);
+    case HC_F16: return launch_dtype<__half>(pairing, pieces16, p, s);
+    default: return launch_dtype<__nv_bfloat16>(pairing, pieces16, p, s);
+  }
+}
+
+}  // namespace hc

@@ -1,0 +1,99 @@
+// Declarations of the serving operators over a 4-bit cache (block tables,
+// rotary positions with several axes, append, attention), shared by their
+// kernels and the C ABI.
+#pragma once
+
+#include "hc_internal.cuh"
+
+namespace hc {
+
+// Status of a call from its launch's error, with the text kept for
+// hc_last_cuda_error (api.cu).
+int record_cuda(cudaError_t e);
+
+struct BlockTableParams {
+  const int32_t* cached;
+  const int32_t* fresh;
+  const int32_t* free_slots;
+  int32_t* tables;
+  int64_t table_stride;
+  int32_t n_req, n_free, table_width, n_tokens, block_log2;
+  int32_t* q_starts;
+  int32_t* kv_lens;
+  int32_t* token_req;
+  int32_t* token_pos;
+  int64_t* token_rows;
+  int32_t* n_taken;
+  int32_t* err;
+  int32_t vec;  // the token arrays take 16-byte stores
+};
+
+// Rotation of rows by positions with several axes; see hc_rope_axes_desc.
+struct RopeParams {
+  const int32_t* positions;
+  int64_t position_stride;
+  const float2* table;  // null: no rotation
+  int32_t n_positions, half, inverse;
+  uint8_t pair_axis[128];
+};
+
+struct RopeAxesParams {
+  RopeParams rope;
+  const void* x;
+  void* y;
+  int64_t x_token, x_head, y_token, y_head;
+  int32_t n_tokens, n_heads, d, heads_per_warp, parts;
+  FastDivmod items_per_row;
+  int32_t* err;
+};
+
+struct AppendParams {
+  RopeParams rope;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+  int32_t n_tokens, n_q_heads, H, B_log2, group_log2, scale_f16;
+  int32_t q_heads_per_warp, q_parts, kv_parts;
+  FastDivmod items_per_row;
+  const int64_t* token_rows;
+  int64_t n_rows;  // num_slots * block_size
+  uint8_t* codes;
+  void* scales;
+  int32_t* err;
+};
+
+struct AttendParams {
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_token, q_head, o_token, o_head;
+  const uint8_t* codes;
+  const void* scales;
+  const int32_t* tables;
+  int64_t table_stride;
+  const int32_t* q_starts;
+  const int32_t* kv_lens;
+  int32_t n_req, n_tokens, max_new, table_width, num_slots;
+  int32_t H, G, B_log2, bf16, causal, window;
+  FastDivmod by_group;  // division by G
+  float scale_log2;     // softmax_scale * log2(e)
+  uint8_t* workspace;
+  int32_t* err;
+};
+
+// Bytes of the attention's workspace: one counter per CTA of the largest
+// grid, then two partial results per CTA.
+int64_t attend_workspace_bytes();
+
+cudaError_t launch_block_tables(const BlockTableParams& p, cudaStream_t s);
+// `piece`: bytes moved at once (16, or the element's size).
+cudaError_t launch_rope_axes(int dtype, int pairing, bool pieces16, const RopeAxesParams& p,
+                             cudaStream_t s);
+cudaError_t launch_append_int4(int dtype, int d, int pairing, const AppendParams& p,
+                               cudaStream_t s);
+cudaError_t launch_attend_int4(int d, int group, bool scale_f16, const AttendParams& p,
+                               cudaStream_t s);
+
+}  // namespace hc

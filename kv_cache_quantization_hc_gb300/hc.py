@@ -16,6 +16,7 @@ HC_F32, HC_F16, HC_BF16 = 0, 1, 2
 HC_PAIR_INTERLEAVED, HC_PAIR_HALF_SPLIT = 0, 1
 HC_WIRE_FP8, HC_WIRE_INT4, HC_WIRE_RAW, HC_WIRE_FP8_ROWS = 0, 1, 2, 3
 HC_DEVERR_SLOT, HC_DEVERR_DELTA, HC_DEVERR_NVALID = 1, 2, 4
+HC_DEVERR_LENGTH, HC_DEVERR_FREE, HC_DEVERR_POS = 8, 16, 32
 
 DTYPE_NAMES = {"f32": HC_F32, "f16": HC_F16, "bf16": HC_BF16}
 PAIRING_NAMES = {"interleaved": HC_PAIR_INTERLEAVED, "half_split": HC_PAIR_HALF_SPLIT}
@@ -32,6 +33,25 @@ class hc_paged_desc(ctypes.Structure):
                 ("d_head", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("num_slots", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("slot_stride", ctypes.c_int64), ("layer_stride", ctypes.c_int64)]
+
+
+class hc_int4_cache(ctypes.Structure):
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("d_head", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
+
+
+class hc_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class hc_rope_axes_desc(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("position_stride", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("n_axes", ctypes.c_int32),
+                ("n_positions", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("pair_axis", ctypes.c_uint8 * 128)]
 
 
 _LIB = None
@@ -61,6 +81,19 @@ def lib():
         L.hc_drift_select.argtypes = [_P, _P, _I32, _I32, _I32, _I32, _I64, _I64, _I32, _P, _P, _P]
         L.hc_tenant_key.argtypes = [_P, _I32, ctypes.c_char_p, _P]
         L.hc_block_digests.argtypes = [_P, _I64, _I32, _P, _I32, _P, _P]
+        rows_p, rope_p, cache_p = (ctypes.POINTER(t) for t in (hc_rows, hc_rope_axes_desc, hc_int4_cache))
+        L.hc_build_block_tables.argtypes = [_P, _P, _I32, _I32, _P, _I32, _P, _I64, _I32, _I32, _P, _P,
+                                            _P, _P, _P, _P, _P, _P]
+        L.hc_rope_axes.argtypes = [rows_p, rows_p, _I32, _I32, _I32, _I32, rope_p, _P, _P]
+        L.hc_append_int4.argtypes = [rows_p, rows_p, rows_p, _I32, _I32, _I32, rope_p, _P, cache_p, _P,
+                                     _P, rows_p, _P, _P]
+        L.hc_attend_int4.argtypes = [rows_p, rows_p, _P, _I32, _I32, _I32, cache_p, _P, _P, _P, _I64,
+                                     _I32, _P, _P, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _I64, _P,
+                                     _P]
+        for fn in ("hc_build_block_tables", "hc_rope_axes", "hc_append_int4", "hc_attend_int4"):
+            getattr(L, fn).restype = ctypes.c_int
+        L.hc_attend_int4_workspace.argtypes = []
+        L.hc_attend_int4_workspace.restype = _I64
         for fn in ("hc_encode_fp8", "hc_encode_fp8_crc", "hc_encode_int4", "hc_encode_fp8_rows",
                    "hc_build_delta_sincos",
                    "hc_fetch_rotate_scatter", "hc_crc32", "hc_drift_select", "hc_tenant_key",
