@@ -146,7 +146,7 @@ cudaError_t launch(AppendParams p, cudaStream_t s) {
   p.items_per_row = FastDivmod(static_cast<uint32_t>(items));
   p.kv_parts = (p.H + kKvHeads<D> - 1) / kKvHeads<D>;
   p.q_heads_per_warp = std::max(1, p.n_q_heads);
-  const int64_t enough = static_cast<int64_t>(device_sm_count()) * 24;
+  constexpr int64_t enough = 152 * 24;
   while (p.q_heads_per_warp > 1 && static_cast<int64_t>(p.q_heads_per_warp) * items > 32 &&
          static_cast<int64_t>(p.n_tokens) *
                  (p.kv_parts + (p.n_q_heads + p.q_heads_per_warp - 1) / p.q_heads_per_warp) < enough)

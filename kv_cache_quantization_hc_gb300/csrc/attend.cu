@@ -821,17 +821,16 @@ template <int D, int GROUP, bool kScaleF16, int NT>
 cudaError_t launch_rows(const AttendParams& p, cudaStream_t s) {
   using L = Layout<D, GROUP, kScaleF16>;
   const int smem = std::max(kWarpsA * L::kWarpBytes, kWarpsA * 8 * NT * D * 4);
-  cudaError_t e = cudaFuncSetAttribute(k_attend_rows<D, GROUP, kScaleF16, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_attend_rows<D, GROUP, kScaleF16, NT>, kWarpsA * 32, smem);
+  static KernelOnDevice kernel;
+  int resident = 0;
+  const cudaError_t e = kernel.resident(reinterpret_cast<const void*>(k_attend_rows<D, GROUP, kScaleF16, NT>),
+                                        kWarpsA * 32, smem, &resident);
   if (e != cudaSuccess) return e;
   // one CTA per resident place, or per tile where there are fewer (as far as the host can tell)
   const int64_t rows = (static_cast<int64_t>(p.max_new) * p.G + 8 * NT - 1) / (8 * NT);
   const int64_t keys = static_cast<int64_t>(p.table_width) << p.B_log2;
   const int64_t tiles = std::max<int64_t>(1, (keys + kTile - 1) / kTile);
-  int64_t grid = std::min<int64_t>(kMaxCtas, static_cast<int64_t>(device_sm_count()) * std::max(1, per_sm));
+  int64_t grid = std::min(kMaxCtas, resident);
   if (static_cast<double>(p.n_req) * p.H * rows * tiles < static_cast<double>(grid))
     grid = p.n_req * p.H * rows * tiles;
   k_attend_rows<D, GROUP, kScaleF16, NT><<<static_cast<unsigned>(grid), kWarpsA * 32, smem, s>>>(p);

@@ -186,14 +186,16 @@ __global__ void __launch_bounds__(kTableThreads) k_block_tables(BlockTableParams
 }  // namespace
 
 cudaError_t launch_block_tables(const BlockTableParams& p, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(k_block_tables, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(sizeof(ChunkSmem)));
+  static KernelOnDevice kernel;
+  int resident = 0;
+  const cudaError_t e = kernel.resident(reinterpret_cast<const void*>(k_block_tables), kTableThreads,
+                                        static_cast<int>(sizeof(ChunkSmem)), &resident);
   if (e != cudaSuccess) return e;
   // one thread per 4 tokens or per new block (at most one per request and block of tokens)
   const int64_t blocks = (static_cast<int64_t>(p.n_tokens) >> p.block_log2) + p.n_req;
   const int64_t items = std::max<int64_t>((p.n_tokens + 3) / 4, blocks);
   const int64_t ctas = (items + kTableThreads - 1) / kTableThreads;
-  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ctas, device_sm_count())));
+  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ctas, resident)));
   k_block_tables<<<grid, kTableThreads, sizeof(ChunkSmem), s>>>(p);
   return cudaGetLastError();
 }

@@ -33,7 +33,7 @@ cudaError_t launch(RopeAxesParams p, cudaStream_t s) {
   // Heads of a token are shared out among warps until the GPU has about 24
   // warps per SM, or a warp has no more than one item per lane.
   p.heads_per_warp = p.n_heads;
-  const int64_t enough = static_cast<int64_t>(device_sm_count()) * 24;
+  constexpr int64_t enough = 152 * 24;
   while (p.heads_per_warp > 1 && static_cast<int64_t>(p.heads_per_warp) * items > 32 &&
          static_cast<int64_t>(p.n_tokens) * ((p.n_heads + p.heads_per_warp - 1) / p.heads_per_warp) < enough)
     p.heads_per_warp = (p.heads_per_warp + 1) / 2;

@@ -3,9 +3,36 @@
 // kernels and the C ABI.
 #pragma once
 
+#include <atomic>
+
 #include "hc_internal.cuh"
 
 namespace hc {
+
+// What a launch needs to know of a kernel and its device, asked once per
+// process and device (a query costs about as much host time as a launch).
+struct KernelOnDevice {
+  static constexpr int kDevices = 32;
+  std::atomic<int> grid[kDevices] = {};  // CTAs that are resident at once; 0: not asked yet
+
+  // Lets `f` use `smem` bytes of dynamic shared memory on the current device
+  // and gives the number of its CTAs that the device holds at once.
+  cudaError_t resident(const void* f, int threads, int smem, int* ctas) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool kept = dev >= 0 && dev < kDevices;
+    if (kept && (*ctas = grid[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, f, threads, smem);
+    if (e != cudaSuccess) return e;
+    *ctas = device_sm_count() * (per_sm > 0 ? per_sm : 1);
+    if (kept) grid[dev].store(*ctas, std::memory_order_relaxed);
+    return cudaSuccess;
+  }
+};
 
 // Status of a call from its launch's error, with the text kept for
 // hc_last_cuda_error (api.cu).
