@@ -12,7 +12,7 @@
 // order of the CTAs, so the result does not depend on which came last.
 //
 // Mathematics, per row, over tiles of keys with a running maximum m:
-//   x_j = c * sum_g s_jg * (q_g . n_jg - corr_g),  p_j = 2^(x_j - m - e),
+//   x_j = c * sum_g s_jg * (q_g . n_jg - corr_g),  p_j = 2^(x_j - m),
 //   l = sum p_j,  O = sum (p_j * sv_jg) * nv_jg
 // with n the codes, s the scales of their groups and c = softmax_scale *
 // log2(e) * the power of two that the row's queries were scaled by.
@@ -25,10 +25,11 @@
 // * Queries as fp16: each row times a power of two that brings its largest
 //   value near 2^14, so that bf16's range fits and only values below 2^-28
 //   of the row's largest lose bits.
-// * Values as exact fp16 whole numbers.  Their scales go into the
-//   probabilities, which are rounded to fp16 once, after that product: 11
-//   bits against the 8 or 11 of the output.  2^e is the largest value scale
-//   seen, over 2^14: the products then fill fp16's range from the top.
+// * Values as exact bf16 whole numbers.  Their scales go into the
+//   probabilities, and those into two bf16 (16 bits of mantissa, fp32's
+//   range) for two products: an fp16 would flush what is below 2^-39 of the
+//   largest, which a channel keeps where the larger keys' values are zero,
+//   and its rounding is as large as that of an fp16 output.
 // * S^T = K Q^T and O^T = V^T P^T: keys and channels are the 16 rows of the
 //   matrix instruction, the queries its 8 columns, so a step of one query
 //   with 8 heads wastes nothing.
@@ -45,7 +46,10 @@ constexpr int kWarpsA = 4;
 constexpr int kKeysWarp = 32;                      // keys of one warp in a tile
 constexpr int kTile = kWarpsA * kKeysWarp;         // keys of a tile
 constexpr int kStages = 3;
-constexpr int kCtasPerSm = 4;
+#ifndef HC_ATTEND_CTAS
+#define HC_ATTEND_CTAS 4
+#endif
+constexpr int kCtasPerSm = HC_ATTEND_CTAS;
 constexpr int kMaxCtas = 1024;                     // counters in the workspace
 constexpr int kMaxRows = 16;                       // rows of a piece
 constexpr int kPartialFloats = kMaxRows * (128 + 2);
@@ -80,6 +84,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 // (w & mask) ^ flip, one LOP3
 __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t flip) {
   return (w & mask) ^ flip;
@@ -95,25 +105,25 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   memcpy(&u, &h, 4);
   return u;
 }
-// Signed codes of nibbles 0 and 4 (resp. 1 and 5) of w as fp16: 1024 + u in
-// the mantissa, u = code + 8, less 1032; or 1024 + 16 u, over 16, less 72.
-__device__ __forceinline__ uint32_t codes_04(uint32_t w) {
-  const uint32_t m = and_xor(w, 0x000f000fu, 0x64086408u);
-  __half2 h;
+// Signed codes of nibbles 0 and 4 of w as bf16: 128 + u in the mantissa,
+// u = code + 8, less 136.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+  const uint32_t m = and_xor(w, 0x000f000fu, 0x43084308u);
+  __nv_bfloat162 h;
   memcpy(&h, &m, 4);
-  h = __hsub2(h, __half2half2(__ushort_as_half(0x6408)));
+  h = __hsub2(h, __bfloat162bfloat162(__ushort_as_bfloat16(0x4308)));
   uint32_t u;
   memcpy(&u, &h, 4);
   return u;
 }
-__device__ __forceinline__ uint32_t codes_15(uint32_t w) {
-  const uint32_t m = and_xor(w, 0x00f000f0u, 0x64806480u);
-  __half2 h;
-  memcpy(&h, &m, 4);
-  h = __hfma2(h, __half2half2(__ushort_as_half(0x2c00)), __half2half2(__ushort_as_half(0xd480)));
-  uint32_t u;
-  memcpy(&u, &h, 4);
-  return u;
+// Two fp32 as pairs of bf16, high and low: the upper halves as they stand,
+// and what is left of them rounded to bf16: 16 bits in all.
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& high, uint32_t& low) {
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  high = __byte_perm(ua, ub, 0x7632);
+  const __nv_bfloat162 rest = __floats2bfloat162_rn(a - __uint_as_float(ua & 0xffff0000u),
+                                                    b - __uint_as_float(ub & 0xffff0000u));
+  memcpy(&low, &rest, 4);
 }
 
 // A request as the call sees it; n = 0 where there is nothing to write.
@@ -204,6 +214,7 @@ struct Shared {
   int32_t last;
   float m[kWarpsA][kMaxRows], l[kWarpsA][kMaxRows];
   float wt[kMaxRows], inv[kMaxRows];
+  alignas(8) float corr[kWarpsA][4][kMaxRows];  // of a group and row, for the warp's products
 };
 
 template <int D, int GROUP, bool kScaleF16, int NT>
@@ -286,8 +297,7 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
 
     // -- queries: fragments, the correction of the codes' offset, row factors
     uint32_t qf[NT][kChunks][4];
-    float corr[NT][kGroups][2], factor[NT][2];
-    int lo_row[NT][2], hi_row[NT][2];
+    float factor[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = row0 + nt * 8 + g;
@@ -340,20 +350,15 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
       for (int j = 0; j < 2; ++j) {
         const int src = (2 * t + j) * 4;
         factor[nt][j] = __shfl_sync(0xffffffffu, fac, src);
-        const int rj = row0 + nt * 8 + 2 * t + j;
-        const int pos = rq.kv - rq.n + static_cast<int>(p.by_group.div(min(rj, rows_all - 1)));
-        hi_row[nt][j] = p.causal ? min(rq.kv, pos + 1) : rq.kv;
-        lo_row[nt][j] = p.window ? pos - p.window + 1 : 0;
       }
 #pragma unroll
       for (int k = 0; k < kGroups; ++k) {
         sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
         sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
-        sum[k] *= -8.f * 0x1p-24f;
-        corr[nt][k][0] = __shfl_sync(0xffffffffu, sum[k], (2 * t) * 4);
-        corr[nt][k][1] = __shfl_sync(0xffffffffu, sum[k], (2 * t + 1) * 4);
+        if (t == 0) sh.corr[warp][k][nt * 8 + g] = sum[k] * (-8.f * 0x1p-24f);
       }
     }
+    __syncwarp();
     // keys that every row sees: no mask needed inside
     int all_lo, all_hi;
     {
@@ -363,7 +368,6 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
     }
 
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
-    float er = -100.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -483,8 +487,9 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
           float acc[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            acc[nt][0] = acc[nt][2] = corr[nt][gr][0];
-            acc[nt][1] = acc[nt][3] = corr[nt][gr][1];
+            const float2 corr = *reinterpret_cast<const float2*>(&sh.corr[warp][gr][nt * 8 + 2 * t]);
+            acc[nt][0] = acc[nt][2] = corr.x;
+            acc[nt][1] = acc[nt][3] = corr.y;
           }
 #pragma unroll
           for (int c = gr * kChunksPerGroup; c < (gr + 1) * kChunksPerGroup; ++c) {
@@ -506,40 +511,29 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
         }
       }
 
-      // -- the value scales of this lane's keys, their largest so far and the tile's smallest
-      float sv[2][2][kGroups];
-      float top = 0.f, low = INFINITY;
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          load_scales<kGroups, kScaleF16>(sv[mt][hf], v_scale, mt * 16 + hf * 8 + g);
-#pragma unroll
-          for (int gr = 0; gr < kGroups; ++gr) {
-            top = fmaxf(top, sv[mt][hf][gr]);
-            low = fminf(low, sv[mt][hf][gr]);
-          }
-        }
-      const uint32_t top_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      low = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(low)));
-      const float er_new = fmaxf(er, static_cast<float>(static_cast<int>(top_bits >> 23) - 127 - 14));
-
       // -- running maximum, probabilities
       const bool masked = key0 < all_lo || key0 + kKeysWarp > all_hi;
       float m_new[NT][2];
-      bool changed = er_new != er;
+      bool changed = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float top_x = kNegInf;
+          int first = 0, last = 0x7fffffff;  // keys that the row sees
+          if (masked) {
+            const int row = min(row0 + nt * 8 + 2 * t + j, rows_all - 1);
+            const int pos = rq.kv - rq.n + static_cast<int>(p.by_group.div(row));
+            last = p.causal ? min(rq.kv, pos + 1) : rq.kv;
+            if (p.window) first = pos - p.window + 1;
+          }
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               float x = s[nt][mt][hf * 2 + j] * factor[nt][j];
               const int key = key0 + mt * 16 + hf * 8 + g;
-              if (masked && (key < lo_row[nt][j] || key >= hi_row[nt][j])) x = kNegInf;
+              if (masked && (key < first || key >= last)) x = kNegInf;
               s[nt][mt][hf * 2 + j] = x;
               top_x = fmaxf(top_x, x);
             }
@@ -556,7 +550,7 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // nothing seen so far: l and O are 0, whatever they are multiplied by
-            const float alpha = m[nt][j] == kNegInf ? 0.f : ex2((m[nt][j] - m_new[nt][j]) + (er - er_new));
+            const float alpha = m[nt][j] == kNegInf ? 0.f : ex2(m[nt][j] - m_new[nt][j]);
             l[nt][j] *= alpha;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
@@ -565,14 +559,12 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
             }
             m[nt][j] = m_new[nt][j];
           }
-        er = er_new;
       }
-      float p_low = INFINITY;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float ref = m[nt][j] == kNegInf ? 0.f : m[nt][j] + er;
+          const float ref = m[nt][j] == kNegInf ? 0.f : m[nt][j];
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -580,7 +572,6 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
               const float e = ex2(s[nt][mt][hf * 2 + j] - ref);
               s[nt][mt][hf * 2 + j] = e;
               l[nt][j] += e;
-              p_low = fminf(p_low, e);
             }
         }
 
@@ -588,7 +579,10 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         const int key = mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
-        uint32_t pb[NT][2];
+        float sv[2][kGroups];
+        load_scales<kGroups, kScaleF16>(sv[0], v_scale, mt * 16 + g);
+        load_scales<kGroups, kScaleF16>(sv[1], v_scale, mt * 16 + g + 8);
+        uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
         for (int cp = 0; cp < kChunks / 2; ++cp) {  // two 16-byte pieces: 64 channels
           uint32_t w[4];
@@ -601,77 +595,30 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-                  pb[nt][hf] = movmatrix_trans(pack_f16(s[nt][mt][hf * 2] * sv[mt][hf][gr],
-                                                        s[nt][mt][hf * 2 + 1] * sv[mt][hf][gr]));
-            }
-            const uint32_t w0 = w[h2 * 2], w1 = w[h2 * 2 + 1], x0 = w0 >> 8, x1 = w1 >> 8;
-            const uint32_t a0 = codes_04(w0), a1 = codes_15(w0), a2 = codes_04(w1), a3 = codes_15(w1);
-            const uint32_t b0 = codes_04(x0), b1 = codes_15(x0), b2 = codes_04(x1), b3 = codes_15(x1);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma16816(o[nt][2 * c], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-              mma16816(o[nt][2 * c + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
-            }
-          }
-        }
-      }
-
-      // -- products below fp16's normal range (2^-29 of the largest) lost bits or all of themselves:
-      // what was lost, 2^39 times as large, goes through the same steps.  It matters only to a channel
-      // in which the keys with larger probabilities hold zeros.
-      if (__any_sync(0xffffffffu, p_low * low < 0x1p-14f)) {
-        float down = 0x1p-39f;
-        for (int range = 0; range < 3; ++range, down *= 0x1p-39f) {
-          bool some = false;
-#pragma unroll 1
-          for (int mt = 0; mt < 2; ++mt) {
-            const int key = mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
-#pragma unroll 1
-            for (int nt = 0; nt < NT; ++nt) {
-              uint32_t pb[2] = {0, 0};
-#pragma unroll
-              for (int c = 0; c < kChunks; ++c) {
-                if (c % kChunksPerGroup == 0) {
-#pragma unroll
-                  for (int hf = 0; hf < 2; ++hf) {
-                    float v[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                      const float pe = NT == 1 ? (mt ? s[0][1][hf * 2 + j] : s[0][0][hf * 2 + j])
-                                               : (nt ? (mt ? s[NT - 1][1][hf * 2 + j] : s[NT - 1][0][hf * 2 + j])
-                                                     : (mt ? s[0][1][hf * 2 + j] : s[0][0][hf * 2 + j]));
-                      const float sc = mt ? sv[1][hf][c / kChunksPerGroup] : sv[0][hf][c / kChunksPerGroup];
-                      v[j] = pe * sc;
-                      for (int k = 0; k <= range; ++k)  // a normal fp16 has lost no more than its rounding
-                        v[j] = fabsf(v[j]) >= 0x1p-14f ? 0.f : (v[j] - __half2float(__float2half_rn(v[j]))) * 0x1p39f;
-                      some = some || v[j] != 0.f;
-                    }
-                    pb[hf] = movmatrix_trans(pack_f16(v[0], v[1]));
-                  }
+                for (int hf = 0; hf < 2; ++hf) {
+                  uint32_t high, low;
+                  split_bf16(s[nt][mt][hf * 2] * sv[hf][gr], s[nt][mt][hf * 2 + 1] * sv[hf][gr], high, low);
+                  ph[nt][hf] = movmatrix_trans(high);
+                  pl[nt][hf] = movmatrix_trans(low);
                 }
-                uint32_t w[4];
-                ldmatrix4_trans(w, vs + key * L::kRowBytes + swizzled<D>(key, (c & ~1) + (lane >> 4)) * 16);
-                const uint32_t w0 = w[(c & 1) * 2], w1 = w[(c & 1) * 2 + 1], x0 = w0 >> 8, x1 = w1 >> 8;
-                float add[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                mma16816(add[0], codes_04(w0), codes_15(w0), codes_04(w1), codes_15(w1), pb[0], pb[1]);
-                mma16816(add[1], codes_04(x0), codes_15(x0), codes_04(x1), codes_15(x1), pb[0], pb[1]);
+            }
+            const uint32_t w0 = w[h2 * 2], w1 = w[h2 * 2 + 1];
+            const uint32_t a0 = codes_bf16(w0), a1 = codes_bf16(w0 >> 4), a2 = codes_bf16(w1), a3 = codes_bf16(w1 >> 4);
+            const uint32_t b0 = codes_bf16(w0 >> 8), b1 = codes_bf16(w0 >> 12), b2 = codes_bf16(w1 >> 8),
+                           b3 = codes_bf16(w1 >> 12);
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const float a = add[u][j] * down;
-                    o[0][2 * c + u][j] += nt == 0 ? a : 0.f;
-                    if (NT > 1) o[NT - 1][2 * c + u][j] += nt == 1 ? a : 0.f;
-                  }
-              }
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_bf16(o[nt][2 * c], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+              mma_bf16(o[nt][2 * c + 1], b0, b1, b2, b3, ph[nt][0], ph[nt][1]);
+              mma_bf16(o[nt][2 * c], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+              mma_bf16(o[nt][2 * c + 1], b0, b1, b2, b3, pl[nt][0], pl[nt][1]);
             }
           }
-          if (!__any_sync(0xffffffffu, some)) break;
         }
       }
     }
     cp_async_wait<0>();
+
     __syncthreads();
 
     // ---- the warps' sums joined: O in shared memory, [warp][row][channel]
@@ -686,7 +633,7 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int row = nt * 8 + 2 * t + j;
         if (g == 0) {
-          sh.m[warp][row] = m[nt][j] == kNegInf ? kNegInf : m[nt][j] + er;
+          sh.m[warp][row] = m[nt][j];
           sh.l[warp][row] = sum;
         }
 #pragma unroll
