@@ -90,9 +90,12 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// (w & mask) ^ flip, one LOP3
+// (w & mask) ^ flip in one LOP3: left to itself the compiler makes two, each
+// with its constant, and the integer pipe is what the loop is bound by.
 __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t flip) {
-  return (w & mask) ^ flip;
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(w), "r"(mask), "r"(flip));
+  return d;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -395,38 +398,40 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
         }
       }
     };
+    // A run of 16 keys is contiguous in the cache, codes and scales alike: lane l copies piece l of each 512 bytes.
+    const int64_t to_v = static_cast<int64_t>(p.H) << p.B_log2;  // rows from K to V
+    constexpr int kRunCopies = 16 * L::kRowBytes / 512;
+    constexpr int kScalePieces = 16 * L::kScaleBytes / 16;        // of a run, of K; as many of V
+    const uint32_t code_dst = stages_addr + (lane / L::kRowChunks) * L::kRowBytes +
+                              swizzled<D>(lane / L::kRowChunks, lane % L::kRowChunks) * 16;
     auto load_tile = [&](int i, const int (&slot)[2]) {
-      const uint32_t st = stages_addr + (i % kStages) * L::kStageBytes;
+      const uint32_t stage = (i % kStages) * L::kStageBytes;
       const int key0 = key_first + i * kTile;
-      int64_t at[2];  // row of the run's first key among all K rows of the cache
 #pragma unroll
-      for (int sb = 0; sb < 2; ++sb)
-        at[sb] = (((static_cast<int64_t>(slot[sb]) * 2) * p.H + head) << p.B_log2) +
-                 ((key0 + sb * 16) & ((1 << p.B_log2) - 1));
-      const int64_t to_v = static_cast<int64_t>(p.H) << p.B_log2;
+      for (int sb = 0; sb < 2; ++sb) {
+        const int key = key0 + sb * 16, keys = slot[sb] < 0 ? 0 : min(16, vis.hi - key);  // keys to copy
+        const int64_t row = (((static_cast<int64_t>(slot[sb]) * 2) * p.H + head) << p.B_log2) +
+                            (key & ((1 << p.B_log2) - 1));
+        const uint8_t* src = p.codes + (keys > 0 ? row * L::kRowBytes + lane * 16 : 0);
+        const int64_t v_bytes = keys > 0 ? to_v * L::kRowBytes : 0;
+        const uint32_t dst = code_dst + stage + sb * 16 * L::kRowBytes;
 #pragma unroll
-      for (int it = 0; it < L::kCodeBytes / 512; ++it) {
-        const int id = it * 32 + lane, key = id / L::kRowChunks, chunk = id % L::kRowChunks;
-        const int sb = key >> 4;
-        const bool in = slot[sb] >= 0 && key0 + key < vis.hi;
-        const uint8_t* src = in ? p.codes + (at[sb] + (key & 15)) * L::kRowBytes + chunk * 16 : p.codes;
-        const uint32_t dst = st + key * L::kRowBytes + swizzled<D>(key, chunk) * 16;
-        cp_async16(dst, src, in ? 16 : 0);
-        cp_async16(dst + L::kCodeBytes, in ? src + to_v * L::kRowBytes : src, in ? 16 : 0);
-      }
-      constexpr int kScaleChunks = L::kScaleStage / 16;  // of K; as many of V
-#pragma unroll
-      for (int id0 = 0; id0 < kScaleChunks; id0 += 32) {
-        const int id = id0 + lane;
-        if (id < kScaleChunks) {
-          const int sb = id / (kScaleChunks / 2);
-          const int first = sb * 16 + (id % (kScaleChunks / 2)) * 16 / L::kScaleBytes;  // key of the piece
-          const int left = slot[sb] >= 0 ? min(16, max(0, vis.hi - key0 - first) * L::kScaleBytes) : 0;
-          const unsigned char* base = static_cast<const unsigned char*>(p.scales);
-          const unsigned char* src = left > 0 ? base + at[sb] * L::kScaleBytes + (id % (kScaleChunks / 2)) * 16 : base;
-          const uint32_t dst = st + 2 * L::kCodeBytes + id * 16;
-          cp_async16(dst, src, left);
-          cp_async16(dst + L::kScaleStage, left > 0 ? src + to_v * L::kScaleBytes : src, left);
+        for (int it = 0; it < kRunCopies; ++it) {
+          // rows that ldmatrix reads together differ by less than the 512 bytes, so the swizzle repeats
+          const bool in = keys == 16 || it * (16 / kRunCopies) + lane / L::kRowChunks < keys;
+          const uint8_t* at = in ? src + it * 512 : p.codes;
+          cp_async16(dst + it * 512, at, in ? 16 : 0);
+          cp_async16(dst + it * 512 + L::kCodeBytes, at + (in ? v_bytes : 0), in ? 16 : 0);
+        }
+        // scales: K's pieces by the lanes from 0, V's by the lanes after them
+        if (lane < 2 * kScalePieces) {
+          const bool v = lane >= kScalePieces;
+          const int piece = v ? lane - kScalePieces : lane;
+          const int left = min(16, max(0, keys * L::kScaleBytes - piece * 16));
+          const uint8_t* from = static_cast<const uint8_t*>(p.scales);
+          if (left > 0) from += (row + (v ? to_v : 0)) * L::kScaleBytes + piece * 16;
+          cp_async16(stages_addr + stage + 2 * L::kCodeBytes + (v ? L::kScaleStage : 0) +
+                         (sb * kScalePieces + piece) * 16, from, left);
         }
       }
     };
