@@ -85,6 +85,7 @@ typedef enum hc_wire {
 #define HC_DEVERR_LENGTH 8 /* a request length that is negative or more than the call holds */
 #define HC_DEVERR_FREE 16  /* fewer free slots than the step's new blocks */
 #define HC_DEVERR_POS 32   /* a position outside [0, n_positions) */
+#define HC_DEVERR_WAIT 64  /* a kernel gave up waiting for its own loads or products: a defect, results unusable */
 
 /* Shape and strides of one paged buffer pair (K and V share it).
  * Supported: d_head in {64, 128}; block_size in {16, 32, 64, 128};

@@ -27,6 +27,7 @@ BINDING = os.path.join(PKG, "_serve" + (sysconfig.get_config_var("EXT_SUFFIX") o
 SOURCES = ["api.cu", "encode.cu", "encode_rows.cu", "fetch_fp8.cu", "fetch_fp8_rows.cu",
            "fetch_int4.cu", "fetch_raw.cu", "table.cu", "crc32.cu", "select.cu",
            "api_serve.cu", "block_tables.cu", "rope_axes.cu", "append.cu", "attend.cu",
+           "attend_tiles.cu",
            "hash.cpp"]
 
 

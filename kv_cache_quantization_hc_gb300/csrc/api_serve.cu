@@ -67,6 +67,15 @@ int check_rope(const hc_rope_axes_desc* r, int d_head, int64_t n_tokens, hc::Rop
   return HC_OK;
 }
 
+// A request with more query rows (new tokens times query heads per cache
+// head) than this is attended in tiles of 256 rows on the 5th-generation
+// tensor cores, one with fewer in pieces of 8 or 16 rows whose keys are split
+// over the SMs.
+#ifndef HC_ATTEND_TILE_ROWS
+#define HC_ATTEND_TILE_ROWS 192
+#endif
+constexpr int kTileRows = HC_ATTEND_TILE_ROWS;
+
 }  // namespace
 
 extern "C" {
@@ -258,8 +267,14 @@ int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dty
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.workspace = static_cast<uint8_t*>(workspace);
   p.err = err_flag;
-  return hc::record_cuda(hc::launch_attend_int4(cache->d_head, cache->group, cache->scale_dtype == HC_F16, p,
-                                                static_cast<cudaStream_t>(stream)));
+  p.rows_above = kTileRows;
+  const bool scale_f16 = cache->scale_dtype == HC_F16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (int64_t{max_new} * G > p.rows_above) {
+    const int t = hc::record_cuda(hc::launch_attend_tiles(cache->d_head, cache->group, scale_f16, p, s));
+    if (t != HC_OK) return t;
+  }
+  return hc::record_cuda(hc::launch_attend_rows(cache->d_head, cache->group, scale_f16, p, s));
 }
 
 }  // extern "C"

@@ -37,7 +37,7 @@
 // Bound: the cache's bytes when rows are few (decoding).
 #include <algorithm>
 
-#include "serve.cuh"
+#include "attend_common.cuh"
 
 namespace hc {
 namespace {
@@ -53,11 +53,7 @@ constexpr int kCtasPerSm = HC_ATTEND_CTAS;
 constexpr int kMaxCtas = 1024;                     // counters in the workspace
 constexpr int kMaxRows = 16;                       // rows of a piece
 constexpr int kPartialFloats = kMaxRows * (128 + 2);
-constexpr float kNegInf = -INFINITY;
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes));
 }
@@ -90,24 +86,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// (w & mask) ^ flip in one LOP3: left to itself the compiler makes two, each
-// with its constant, and the integer pipe is what the loop is bound by.
-__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t flip) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(w), "r"(mask), "r"(flip));
-  return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  uint32_t u;
-  memcpy(&u, &h, 4);
-  return u;
-}
 // Signed codes of nibbles 0 and 4 of w as bf16: 128 + u in the mantissa,
 // u = code + 8, less 136.
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
@@ -129,44 +107,12 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& high, uin
   memcpy(&low, &rest, 4);
 }
 
-// A request as the call sees it; n = 0 where there is nothing to write.
-struct Request {
-  int q0, n, kv;
-};
-__device__ __forceinline__ Request load_request(const AttendParams& p, int r, int& bad) {
-  Request q;
-  q.q0 = __ldg(p.q_starts + r);
-  q.n = __ldg(p.q_starts + r + 1) - q.q0;
-  q.kv = __ldg(p.kv_lens + r);
-  const bool ok = q.n >= 0 && q.n <= p.max_new && q.q0 >= 0 && q.q0 <= p.n_tokens - q.n && q.kv >= 0 &&
-                  q.kv <= (static_cast<int64_t>(p.table_width) << p.B_log2);
-  if (!ok) {
-    bad |= HC_DEVERR_LENGTH;
-    q.q0 = q.n = q.kv = 0;
-  }
-  return q;
-}
-
-// Keys [lo, hi) that some of the rows [row0, row1) see, and their tiles.
-struct Range {
-  int lo, hi, tile0, tiles;
-};
-__device__ __forceinline__ Range visible(const AttendParams& p, const Request& q, int row0, int row1) {
-  const int i0 = static_cast<int>(p.by_group.div(row0)), i1 = static_cast<int>(p.by_group.div(row1 - 1));
-  Range v;
-  v.hi = p.causal ? min(q.kv, q.kv - q.n + i1 + 1) : q.kv;
-  v.lo = p.window ? max(0, q.kv - q.n + i0 - p.window + 1) : 0;
-  if (v.lo >= v.hi) v.lo = v.hi = 0;
-  v.tile0 = v.lo / kTile;
-  v.tiles = max(1, (v.hi + kTile - 1) / kTile - v.tile0);  // a piece without keys still writes its rows
-  return v;
-}
-
 template <int kRows>
 __device__ __forceinline__ int request_units(const AttendParams& p, const Request& q) {
   int units = 0;
+  if (q.n * p.G > p.rows_above) return 0;  // k_attend_tiles does these
   for (int r0 = 0, rows = q.n * p.G; r0 < rows; r0 += kRows)
-    units += visible(p, q, r0, min(r0 + kRows, rows)).tiles;
+    units += visible<kTile>(p, q, r0, min(r0 + kRows, rows)).tiles;
   return units * p.H;
 }
 
@@ -281,7 +227,7 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
   if (r < 0) return;
   Request rq = load_request(p, r, bad);
   int rows_all = rq.n * p.G;
-  Range vis = visible(p, rq, 0, min(kRows, rows_all));
+  Range vis = visible<kTile>(p, rq, 0, min(kRows, rows_all));
   for (;;) {  // to the piece that holds `off`: rows outermost, then heads
     if (off < vis.tiles * p.H) {
       head = off / vis.tiles;
@@ -291,7 +237,7 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
     off -= vis.tiles * p.H;
     row0 += kRows;
     if (row0 >= rows_all) return;  // never, unless the lengths change under the kernel
-    vis = visible(p, rq, row0, min(row0 + kRows, rows_all));
+    vis = visible<kTile>(p, rq, row0, min(row0 + kRows, rows_all));
   }
 
   for (uint32_t unit = begin; unit < end;) {
@@ -318,8 +264,7 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 v = p.bf16 ? u32_to_float2(u[k], static_cast<const __nv_bfloat16*>(nullptr))
-                                  : u32_to_float2(u[k], static_cast<const __half*>(nullptr));
+          const float2 v = widen(u[k], p.bf16);
           f[cc][2 * k] = v.x;
           f[cc][2 * k + 1] = v.y;
           amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
@@ -659,14 +604,8 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
       const int64_t tok = rq.q0 + i;
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       uint2 w;
-      if (p.bf16) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * inv, v.y * inv), c = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-        memcpy(&w.x, &a, 4);
-        memcpy(&w.y, &c, 4);
-      } else {
-        w.x = pack_f16(v.x * inv, v.y * inv);
-        w.y = pack_f16(v.z * inv, v.w * inv);
-      }
+      w.x = p.bf16 ? pack_bf16(v.x * inv, v.y * inv) : pack_f16(v.x * inv, v.y * inv);
+      w.y = p.bf16 ? pack_bf16(v.z * inv, v.w * inv) : pack_f16(v.z * inv, v.w * inv);
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + tok * p.o_token + h * p.o_head + ch) = w;
       if (p.lse && ch == 0)
         p.lse[tok * (static_cast<int64_t>(p.H) * p.G) + h] = sum > 0.f ? (mref + log2f(sum)) * 0.6931471805599453f : kNegInf;
@@ -758,10 +697,10 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
           if (++r >= p.n_req) return;  // likewise
           rq = load_request(p, r, bad);
           bad &= ~HC_DEVERR_LENGTH;  // CTA 0 reports these
-          rows_all = rq.n * p.G;
+          rows_all = rq.n * p.G <= p.rows_above ? rq.n * p.G : 0;
           row0 = rows_all > 0 ? 0 : 1;
         }
-        vis = visible(p, rq, row0, min(row0 + kRows, rows_all));
+        vis = visible<kTile>(p, rq, row0, min(row0 + kRows, rows_all));
       }
     }
     __syncthreads();
@@ -779,7 +718,8 @@ cudaError_t launch_rows(const AttendParams& p, cudaStream_t s) {
                                         kWarpsA * 32, smem, &resident);
   if (e != cudaSuccess) return e;
   // one CTA per resident place, or per tile where there are fewer (as far as the host can tell)
-  const int64_t rows = (static_cast<int64_t>(p.max_new) * p.G + 8 * NT - 1) / (8 * NT);
+  const int64_t rows =
+      (std::min<int64_t>(static_cast<int64_t>(p.max_new) * p.G, p.rows_above) + 8 * NT - 1) / (8 * NT);
   const int64_t keys = static_cast<int64_t>(p.table_width) << p.B_log2;
   const int64_t tiles = std::max<int64_t>(1, (keys + kTile - 1) / kTile);
   int64_t grid = std::min(kMaxCtas, resident);
@@ -791,7 +731,7 @@ cudaError_t launch_rows(const AttendParams& p, cudaStream_t s) {
 
 template <int D, int GROUP, bool kScaleF16>
 cudaError_t launch_nt(const AttendParams& p, cudaStream_t s) {
-  return static_cast<int64_t>(p.max_new) * p.G <= 8 ? launch_rows<D, GROUP, kScaleF16, 1>(p, s)
+  return std::min<int64_t>(static_cast<int64_t>(p.max_new) * p.G, p.rows_above) <= 8 ? launch_rows<D, GROUP, kScaleF16, 1>(p, s)
                                                     : launch_rows<D, GROUP, kScaleF16, 2>(p, s);
 }
 
@@ -807,7 +747,7 @@ int64_t attend_workspace_bytes() {
          static_cast<int64_t>(kMaxCtas) * 2 * kPartialFloats * static_cast<int64_t>(sizeof(float));
 }
 
-cudaError_t launch_attend_int4(int d, int group, bool scale_f16, const AttendParams& p, cudaStream_t s) {
+cudaError_t launch_attend_rows(int d, int group, bool scale_f16, const AttendParams& p, cudaStream_t s) {
   if (d == 64) return group == 32 ? launch_scale<64, 32>(scale_f16, p, s) : launch_scale<64, 64>(scale_f16, p, s);
   if (group == 32) return launch_scale<128, 32>(scale_f16, p, s);
   return group == 64 ? launch_scale<128, 64>(scale_f16, p, s) : launch_scale<128, 128>(scale_f16, p, s);

@@ -1,0 +1,618 @@
+// Attention of the new tokens over the 4-bit cache, many query rows: tiles of
+// 256 rows (new tokens times the query heads of one cache head) against tiles
+// of 128 keys on the 5th-generation tensor cores.
+//
+// One CTA per 256 rows, 13 warps:
+//   warps 0-3, 4-7  the softmax of rows 0-127 and 128-255, a thread per row;
+//   warps 8-11      codes and scales into fp16 tiles of keys and values in
+//                   shared memory, two of each ahead;
+//   warp 12         one thread issues the products: S = Q K^T into tensor
+//                   memory, O += P V with P from tensor memory.
+// While one half's softmax runs, the other half's products do: per half the
+// order is S(j), softmax(j), O += P(j) V(j), S(j + 1).  Tensor memory is full:
+// two S of 128 columns, over which P is written, and two O of d.
+//
+// Mathematics, per row, with a reference m near the running maximum:
+//   x_j = f * 2^(ek - 12) * (q . k_j),  p_j = 2^(x_j - m + 7),
+//   l = sum p_j,  O = sum p_j v_j,      out = O / l * 2^(ev - 12)
+// * k_j = code * scale * 2^(12 - ek) in fp16, 2^ek the largest key scale of the
+//   tile; v_j likewise with 2^ev the largest value scale so far.  Powers of
+//   two, so that scales of any size use fp16's range from the top and each
+//   element is rounded once.
+// * Queries in fp16: each row times a power of two that brings its largest
+//   value near 2^14 (f holds the inverse).
+// * m moves only when the maximum exceeds it by 8, so that O (in tensor
+//   memory) is rarely rescaled; p_j stays below 2^15.
+// * The channels of keys, queries and values are permuted within eights
+//   (0 4 1 5 2 6 3 7), the order in which a word of codes comes apart; the
+//   products over channels do not see it and the output is put back in order.
+//
+// Bound: the tensor cores (4 d flops per row and key), with the softmax's
+// exponentials and the conversion of the codes beside them.
+#include <algorithm>
+
+#include "attend_common.cuh"
+
+namespace hc {
+namespace {
+
+constexpr int kKeys = 128;       // keys of a tile
+constexpr int kHalf = 128;       // rows of a half
+constexpr int kRowsTile = 2 * kHalf;
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
+constexpr int kThreadsTiles = (kSoftmaxWarps + kConvertWarps + 1) * 32;
+constexpr int kBlockBytes = kKeys * 128;  // 128 rows of 64 channels, swizzled in 128-byte rows
+constexpr float kMoveAt = 8.f;   // the reference moves when the maximum is this far above it
+
+template <int D>
+struct TileSmem {
+  static constexpr int kTileBytes = D / 64 * kBlockBytes;
+  static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + 2 * kTileBytes;
+  static constexpr int kBytes = kV + 2 * kTileBytes;
+  // with 1 KiB to align, and enough for one CTA per SM: each takes all of tensor memory
+  static constexpr int kAsk = (kBytes > 120 * 1024 ? kBytes : 120 * 1024) + 1024;
+};
+
+struct TileShared {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], e_full[4], drain;
+  uint32_t tmem;
+  int32_t dead;               // some wait ran out
+  uint32_t top[2][2][kConvertWarps];  // [tile & 1][keys, values][warp]: largest scale's bits
+  int32_t ek[4], ev[4];       // of tile j at j & 3
+};
+
+// ------------------------------------------------------------ PTX
+__device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t a, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done) : "r"(a), "r"(parity) : "memory");
+  return done != 0;
+}
+// Waits for the phase of this parity to end; false when the wait ran out
+// (two seconds), here or elsewhere in the CTA.
+__device__ __noinline__ bool mbar_wait_long(uint32_t a, uint32_t parity, int32_t* dead) {
+  uint64_t start, now;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
+  do {
+    if (mbar_try(a, parity)) return true;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+  } while (now - start < 2000000000ull && !*static_cast<volatile int32_t*>(dead));
+  *static_cast<volatile int32_t*>(dead) = 1;
+  return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, int32_t* dead) {
+  const uint32_t a = smem_addr(b);
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try(a, parity)) return true;
+  return mbar_wait_long(a, parity, dead);
+}
+__device__ __forceinline__ void commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(b))
+               : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(add)) : "memory");
+}
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(add)) : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+            "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+// The loads so far are done; the registers may be used from here on.
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                     "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                       "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :: "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11"
+      ", %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29"
+      ", %30, %31, %32};"
+               :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+                   "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+                     "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+                       "r"(r[30]), "r"(r[31])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11"
+      ", %12, %13, %14, %15, %16};"
+               :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+                   "r"(r[15])
+               : "memory");
+}
+
+// Shared-memory descriptor of a tile in 128-byte swizzled rows: groups of 8
+// rows 1024 bytes apart; for channel-major use (values), blocks of 64
+// channels `block_stride` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t block_stride) {
+  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (static_cast<uint64_t>(block_stride >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// M = 128, fp16 operands, fp32 sums; `n_major`: B's rows are the reduction
+__device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool n_major) {
+  return (1u << 4) | (n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// Signed codes of nibbles 0 and 4 (resp. 1 and 5) of w as fp16: 1024 + u in
+// the mantissa, u = code + 8, less 1032; or 1024 + 16 u, over 16, less 72.
+__device__ __forceinline__ __half2 as_half2(uint32_t u) {
+  __half2 h;
+  memcpy(&h, &u, 4);
+  return h;
+}
+__device__ __forceinline__ __half2 both(uint16_t h) { return __half2half2(__ushort_as_half(h)); }
+__device__ __forceinline__ __half2 codes_04(uint32_t w) {
+  return __hsub2(as_half2(and_xor(w, 0x000f000fu, 0x64086408u)), both(0x6408));
+}
+__device__ __forceinline__ __half2 codes_15(uint32_t w) {
+  return __hfma2(as_half2(and_xor(w, 0x00f000f0u, 0x64806480u)), both(0x2c00), both(0xd480));
+}
+
+// The scale of 32 channels: fp16, with what fp16 leaves of an fp32 scale
+// apart, so that the product is rounded once.
+template <bool kScaleF16>
+struct ScaleH {
+  __half2 s, rest;
+  __device__ __forceinline__ explicit ScaleH(float v) {
+    s = __float2half2_rn(v);
+    if (!kScaleF16) rest = __float2half2_rn(v - __low2float(s));
+  }
+  __device__ __forceinline__ uint32_t times(__half2 codes) const {
+    const __half2 r = kScaleF16 ? __hmul2(codes, s) : __hfma2(codes, s, __hmul2(codes, rest));
+    uint32_t u;
+    memcpy(&u, &r, 4);
+    return u;
+  }
+};
+
+__device__ __forceinline__ float load_scale(const void* scales, int64_t i, bool f16) {
+  return f16 ? __half2float(static_cast<const __half*>(scales)[i]) : static_cast<const float*>(scales)[i];
+}
+
+template <int D, int GROUP, bool kScaleF16>
+__global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_constant__ AttendParams p, int tiles_per_head) {
+  using Smem = TileSmem<D>;
+  extern __shared__ unsigned char dyn_raw[];
+  __shared__ TileShared sh;
+  unsigned char* const dyn = dyn_raw + (1024 - (smem_addr(dyn_raw) & 1023)) % 1024;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  int bad = 0;
+
+  // ---- this CTA's rows: the last tiles of a request first, they have the most keys
+  const int rh = blockIdx.x / tiles_per_head, rt = tiles_per_head - 1 - (blockIdx.x - rh * tiles_per_head);
+  const int r = rh / p.H, head = rh - r * p.H;
+  const Request rq = load_request(p, r, bad);
+  bad = 0;  // lengths are reported by k_attend_rows
+  const int rows_all = rq.n * p.G, row0 = rt * kRowsTile;
+  if (rows_all <= p.rows_above || row0 >= rows_all) return;
+  const Range vis = visible<kKeys>(p, rq, row0, min(row0 + kRowsTile, rows_all));
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], kConvertWarps * 32);
+      mbar_init(&sh.v_full[i], kConvertWarps * 32);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], kHalf);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.e_full[i], kConvertWarps * 32);
+    mbar_init(&sh.drain, 1);
+    sh.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kSoftmaxWarps + kConvertWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+
+  // ---- queries: a softmax thread per row
+  float factor = 0.f;
+  int first = 0, last = 0x7fffffff;  // keys that the thread's row sees
+  const int row = row0 + tid;        // of a softmax thread
+  int token = 0, q_head = 0;
+  if (warp < kSoftmaxWarps) {
+    const bool live = row < rows_all;
+    uint4 raw[D / 8];
+    float amax = 0.f;
+    if (live) {
+      const int i = static_cast<int>(p.by_group.div(row));
+      token = rq.q0 + i;
+      q_head = head * p.G + row - i * p.G;
+      const int pos = rq.kv - rq.n + i;
+      last = p.causal ? min(rq.kv, pos + 1) : rq.kv;
+      if (p.window) first = pos - p.window + 1;
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + token * p.q_token + q_head * p.q_head;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + c * 8);
+    } else {
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) raw[c] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      const uint32_t u[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = widen(u[k], p.bf16);
+        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+      }
+    }
+    const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100), 100);
+    const float up = p.scale_log2 < 0.f ? -pow2(14 - e) : pow2(14 - e);
+    factor = fabsf(p.scale_log2) * pow2(e - 14);
+    unsigned char* q = dyn + Smem::kQ + (tid / kHalf) * Smem::kTileBytes;
+    const int rr = tid % kHalf;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      const float2 a = widen(raw[c].x, p.bf16), b = widen(raw[c].y, p.bf16), cc = widen(raw[c].z, p.bf16),
+                   d = widen(raw[c].w, p.bf16);
+      uint4 w;  // channels 0 4 1 5 2 6 3 7
+      w.x = pack_f16(a.x * up, cc.x * up);
+      w.y = pack_f16(a.y * up, cc.y * up);
+      w.z = pack_f16(b.x * up, d.x * up);
+      w.w = pack_f16(b.y * up, d.y * up);
+      *reinterpret_cast<uint4*>(q + (c / 8) * kBlockBytes + rr * 128 + (((c % 8) ^ (rr & 7)) << 4)) = w;
+    }
+    fence_async();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int tiles = vis.tiles;
+
+  if (warp < kSoftmaxWarps) {
+    // ================================================== softmax
+    const int half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes of tensor memory per warp
+    const uint32_t s_at = tmem + lanes + half * 128, o_at = tmem + lanes + 256 + half * D;
+    float m = kNegInf, l = 0.f;
+    int ev = -100;
+    bool ok = true;
+    for (int j = 0; j < tiles && ok; ++j) {
+      ok = mbar_wait(&sh.e_full[j & 3], (j >> 2) & 1, &sh.dead) && mbar_wait(&sh.s_full[half], j & 1, &sh.dead);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      fence_after();
+      const float f = factor * pow2(sh.ek[j & 3] - 12);
+      const int ev_new = sh.ev[j & 3];
+      const int key0 = (vis.tile0 + j) * kKeys;
+      const bool masked = __any_sync(0xffffffffu, key0 < first || key0 + kKeys > last);
+      const int lo = first - key0, hi = last - key0;  // columns [lo, hi) count
+
+      uint32_t a[2][32];
+      float top = kNegInf;
+      tmem_load32(a[0], s_at);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t(&x)[32] = a[c & 1];
+        tmem_wait_load(x);
+        if (c < 3) tmem_load32(a[(c + 1) & 1], s_at + (c + 1) * 32);
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (c * 32 + k >= lo && c * 32 + k < hi) top = fmaxf(top, __uint_as_float(x[k]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+        }
+      }
+      tmem_load32(a[0], s_at);
+      top *= f;
+      // the reference of the row, and O with it
+      const float m_new = top > m + kMoveAt || m == kNegInf ? fmaxf(m, top) : m;
+      if (__any_sync(0xffffffffu, m_new != m || ev_new != ev)) {
+        const float by = m == kNegInf ? 0.f : ex2(m - m_new);
+        l *= by;
+        if (j > 0) {
+          const float by_o = by * pow2(max(ev - ev_new, -126));
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            tmem_load32(a[1], o_at + c * 32);
+            tmem_wait_load(a[1]);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) a[1][k] = __float_as_uint(__uint_as_float(a[1][k]) * by_o);
+            tmem_store32(o_at + c * 32, a[1]);
+          }
+        }
+        m = m_new;
+        ev = ev_new;
+      }
+      const float off = m == kNegInf ? 0.f : 7.f - m;
+      const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t(&x)[32] = a[c & 1];
+        tmem_wait_load(x);
+        if (c < 3) tmem_load32(a[(c + 1) & 1], s_at + (c + 1) * 32);
+        uint32_t h[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float2 v = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, off2);
+          if (masked) {
+            if (!(c * 32 + k >= lo && c * 32 + k < hi)) v.x = kNegInf;
+            if (!(c * 32 + k + 1 >= lo && c * 32 + k + 1 < hi)) v.y = kNegInf;
+          }
+          v.x = ex2(v.x);
+          v.y = ex2(v.y);
+          sum = __fadd2_rn(sum, v);
+          h[k / 2] = pack_f16(v.x, v.y);
+        }
+        tmem_store16(s_at + c * 16, h);  // over columns already read
+      }
+      l += sum.x + sum.y;
+      wait_store();
+      fence_before();
+      mbar_arrive(&sh.p_full[half]);
+    }
+    // ---- the result
+    ok = ok && mbar_wait(&sh.s_full[half], tiles & 1, &sh.dead);
+    if (__all_sync(0xffffffffu, ok)) {
+      fence_after();
+      const float by = l > 0.f ? pow2(ev - 12) / l : 0.f;
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + token * p.o_token + q_head * p.o_head;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        tmem_load32(x, o_at + c * 32);
+        tmem_wait_load(x);
+        if (row < rows_all) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float v[8];  // channels 0 4 1 5 2 6 3 7 back in order
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[i] = __uint_as_float(x[k * 8 + 2 * i]) * by;
+              v[i + 4] = __uint_as_float(x[k * 8 + 2 * i + 1]) * by;
+            }
+            uint4 w;
+            w.x = p.bf16 ? pack_bf16(v[0], v[1]) : pack_f16(v[0], v[1]);
+            w.y = p.bf16 ? pack_bf16(v[2], v[3]) : pack_f16(v[2], v[3]);
+            w.z = p.bf16 ? pack_bf16(v[4], v[5]) : pack_f16(v[4], v[5]);
+            w.w = p.bf16 ? pack_bf16(v[6], v[7]) : pack_f16(v[6], v[7]);
+            *reinterpret_cast<uint4*>(dst + c * 32 + k * 8) = w;
+          }
+        }
+      }
+      if (p.lse && row < rows_all)
+        p.lse[static_cast<int64_t>(token) * (static_cast<int64_t>(p.H) * p.G) + q_head] =
+            l > 0.f ? (m - 7.f + log2f(l)) * 0.6931471805599453f : kNegInf;
+      fence_before();
+    }
+  } else if (warp < kSoftmaxWarps + kConvertWarps) {
+    // ================================================== codes to fp16 tiles
+    constexpr int kParts = D / 32;   // threads of a key, 32 channels each: one group's scale
+    constexpr int kIters = kParts;   // 128 keys * kParts / 128 threads
+    constexpr int kGroups = D / GROUP;
+    const int t = tid - kSoftmaxWarps * 32, w = warp - kSoftmaxWarps;
+    const int part = t % kParts;
+    const int32_t* table = p.tables + static_cast<int64_t>(r) * p.table_stride;
+    const int64_t to_v = static_cast<int64_t>(p.H) << p.B_log2;  // rows from K to V
+    const int swap = (part >> 1) & 1;  // block 1 writes its words in the order 2 3 0 1: other banks than block 0's
+
+    auto slot_of = [&](int j, int it) {  // -1: no such key, or no such slot
+      const int key = (vis.tile0 + j) * kKeys + (it * 128 + t) / kParts;
+      if (j >= tiles || key >= vis.hi || key < vis.lo) return -1;
+      int slot = __ldg(table + (key >> p.B_log2));
+      if (static_cast<uint32_t>(slot) >= static_cast<uint32_t>(p.num_slots)) {
+        bad |= HC_DEVERR_SLOT;
+        slot = -1;
+      }
+      return slot;
+    };
+    uint4 code[2][kIters];
+    float scale[2][kIters];
+    int slots[kIters];
+    auto load = [&](int j, int kv) {
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) {
+        code[kv][it] = make_uint4(0, 0, 0, 0);
+        scale[kv][it] = 0.f;
+        if (slots[it] >= 0) {
+          const int key = (vis.tile0 + j) * kKeys + (it * 128 + t) / kParts;
+          const int64_t at = (((static_cast<int64_t>(slots[it]) * 2) * p.H + head) << p.B_log2) +
+                             (key & ((1 << p.B_log2) - 1)) + (kv ? to_v : 0);
+          code[kv][it] = __ldg(reinterpret_cast<const uint4*>(p.codes + at * (D / 2) + part * 16));
+          scale[kv][it] = load_scale(p.scales, at * kGroups + part * 32 / GROUP, kScaleF16);
+        }
+      }
+    };
+    auto convert = [&](unsigned char* tile, int kv, int e) {
+      const float up = pow2(12 - e);
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) {
+        const int key = (it * 128 + t) / kParts;
+        const ScaleH<kScaleF16> s(scale[kv][it] * up);
+        const uint4 c = code[kv][it];
+        const uint32_t words[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+        unsigned char* base = tile + (part >> 1) * kBlockBytes + key * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo = words[i], hi = lo >> 8;
+          uint4 v;
+          v.x = s.times(codes_04(lo));
+          v.y = s.times(codes_15(lo));
+          v.z = s.times(codes_04(hi));
+          v.w = s.times(codes_15(hi));
+          const int chunk = (part & 1) * 4 + (i ^ (swap * 2));
+          *reinterpret_cast<uint4*>(base + ((chunk ^ (key & 7)) << 4)) = v;
+        }
+      }
+    };
+
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) slots[it] = slot_of(0, it);
+    load(0, 0);
+    load(0, 1);
+    int ev = -100;
+    bool ok = true;
+    for (int j = 0; j < tiles; ++j) {
+      // the tile's largest scales
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) top = max(top, __float_as_uint(scale[kv][it]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) sh.top[j & 1][kv][w] = top;
+      }
+      // all of these warps go on, or none
+      uint32_t stop;
+      asm volatile(
+          "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}"
+          : "=r"(stop) : "r"(static_cast<uint32_t>(!ok)) : "memory");
+      if (stop) break;
+      uint32_t top_k = 0, top_v = 0;
+#pragma unroll
+      for (int i = 0; i < kConvertWarps; ++i) {
+        top_k = max(top_k, sh.top[j & 1][0][i]);
+        top_v = max(top_v, sh.top[j & 1][1][i]);
+      }
+      const int ek = max(static_cast<int>(top_k >> 23) - 127, -100);
+      ev = max(ev, static_cast<int>(top_v >> 23) - 127);
+      if (t == 0) {
+        sh.ek[j & 3] = ek;
+        sh.ev[j & 3] = ev;
+      }
+      mbar_arrive(&sh.e_full[j & 3]);
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) slots[it] = slot_of(j + 1, it);
+
+      const int st = j & 1;
+      if (j >= 2) ok = ok && mbar_wait(&sh.k_empty[st], ((j >> 1) - 1) & 1, &sh.dead);
+      convert(dyn + Smem::kK + st * Smem::kTileBytes, 0, ek);
+      fence_async();
+      mbar_arrive(&sh.k_full[st]);
+      if (j + 1 < tiles) load(j + 1, 0);
+      if (j >= 2) ok = ok && mbar_wait(&sh.v_empty[st], ((j >> 1) - 1) & 1, &sh.dead);
+      convert(dyn + Smem::kV + st * Smem::kTileBytes, 1, ev);
+      fence_async();
+      mbar_arrive(&sh.v_full[st]);
+      if (j + 1 < tiles) load(j + 1, 1);
+    }
+  } else {
+    // ================================================== products, by one thread
+    if (lane == 0) {
+    const uint32_t base = smem_addr(dyn);
+    bool ok = true;
+    auto scores = [&](int i, int j) {  // S_i = Q_i K(j)^T
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t step = (k / 4) * kBlockBytes + (k % 4) * 32;
+        mma_smem(tmem + i * 128, smem_desc(base + Smem::kQ + i * Smem::kTileBytes + step, 16),
+                 smem_desc(base + Smem::kK + (j & 1) * Smem::kTileBytes + step, 16), instr_desc(kKeys, false), k > 0);
+      }
+      commit(&sh.s_full[i]);
+    };
+    auto values = [&](int i, int j) {  // O_i += P_i(j) V(j)
+#pragma unroll
+      for (int k = 0; k < kKeys / 16; ++k)
+        mma_tmem(tmem + 256 + i * D, tmem + i * 128 + k * 8,
+                 smem_desc(base + Smem::kV + (j & 1) * Smem::kTileBytes + k * 2048, kBlockBytes), instr_desc(D, true),
+                 j > 0 || k > 0);
+    };
+    for (int j = 0; j <= tiles && ok; ++j) {
+      for (int i = 0; i < 2 && ok; ++i) {
+        if (j > 0) {
+          ok = mbar_wait(&sh.v_full[(j - 1) & 1], ((j - 1) >> 1) & 1, &sh.dead) &&
+               mbar_wait(&sh.p_full[i], (j - 1) & 1, &sh.dead);
+          if (!ok) break;
+          fence_after();
+          values(i, j - 1);
+          if (i == 1) commit(&sh.v_empty[(j - 1) & 1]);
+        }
+        if (j < tiles) {
+          ok = mbar_wait(&sh.k_full[j & 1], (j >> 1) & 1, &sh.dead);
+          if (!ok) break;
+          fence_after();
+          scores(i, j);
+          if (i == 1) commit(&sh.k_empty[j & 1]);
+        } else {
+          commit(&sh.s_full[i]);  // O_i is complete
+        }
+      }
+    }
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  if (warp == kSoftmaxWarps + kConvertWarps) {
+    if (sh.dead) {  // products may still be on their way: wait for them before their memory goes
+      if (lane == 0) {
+        flag_error(p.err, HC_DEVERR_WAIT);
+        int32_t no = 0;
+        commit(&sh.drain);
+        mbar_wait(&sh.drain, 0, &no);
+      }
+      __syncwarp();
+    }
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+  if (bad) flag_error(p.err, bad);
+}
+
+template <int D, int GROUP, bool kScaleF16>
+cudaError_t launch(const AttendParams& p, cudaStream_t s) {
+  static KernelOnDevice kernel;
+  int resident = 0;
+  const cudaError_t e = kernel.resident(reinterpret_cast<const void*>(k_attend_tiles<D, GROUP, kScaleF16>), kThreadsTiles,
+                                        TileSmem<D>::kAsk, &resident);
+  if (e != cudaSuccess) return e;
+  const int64_t per_head = (static_cast<int64_t>(p.max_new) * p.G + kRowsTile - 1) / kRowsTile;
+  const int64_t grid = per_head * p.n_req * p.H;
+  if (grid >= (int64_t{1} << 31)) return cudaErrorInvalidConfiguration;
+  k_attend_tiles<D, GROUP, kScaleF16><<<static_cast<unsigned>(grid), kThreadsTiles, TileSmem<D>::kAsk, s>>>(
+      p, static_cast<int>(per_head));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tiles(int d, int group, bool scale_f16, const AttendParams& p, cudaStream_t s) {
+  if (d == 64) {
+    if (group == 32) return scale_f16 ? launch<64, 32, true>(p, s) : launch<64, 32, false>(p, s);
+    return scale_f16 ? launch<64, 64, true>(p, s) : launch<64, 64, false>(p, s);
+  }
+  if (group == 32) return scale_f16 ? launch<128, 32, true>(p, s) : launch<128, 32, false>(p, s);
+  if (group == 64) return scale_f16 ? launch<128, 64, true>(p, s) : launch<128, 64, false>(p, s);
+  return scale_f16 ? launch<128, 128, true>(p, s) : launch<128, 128, false>(p, s);
+}
+
+}  // namespace hc

@@ -106,6 +106,7 @@ struct AttendParams {
   int32_t H, G, B_log2, bf16, causal, window;
   FastDivmod by_group;  // division by G
   float scale_log2;     // softmax_scale * log2(e)
+  int32_t rows_above;   // requests with more query rows than this go to k_attend_tiles
   uint8_t* workspace;
   int32_t* err;
 };
@@ -120,7 +121,10 @@ cudaError_t launch_rope_axes(int dtype, int pairing, bool pieces16, const RopeAx
                              cudaStream_t s);
 cudaError_t launch_append_int4(int dtype, int d, int pairing, const AppendParams& p,
                                cudaStream_t s);
-cudaError_t launch_attend_int4(int d, int group, bool scale_f16, const AttendParams& p,
+// The requests with at most p.rows_above query rows, and those with more.
+cudaError_t launch_attend_rows(int d, int group, bool scale_f16, const AttendParams& p,
                                cudaStream_t s);
+cudaError_t launch_attend_tiles(int d, int group, bool scale_f16, const AttendParams& p,
+                                cudaStream_t s);
 
 }  // namespace hc

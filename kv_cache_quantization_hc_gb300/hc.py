@@ -16,7 +16,7 @@ HC_F32, HC_F16, HC_BF16 = 0, 1, 2
 HC_PAIR_INTERLEAVED, HC_PAIR_HALF_SPLIT = 0, 1
 HC_WIRE_FP8, HC_WIRE_INT4, HC_WIRE_RAW, HC_WIRE_FP8_ROWS = 0, 1, 2, 3
 HC_DEVERR_SLOT, HC_DEVERR_DELTA, HC_DEVERR_NVALID = 1, 2, 4
-HC_DEVERR_LENGTH, HC_DEVERR_FREE, HC_DEVERR_POS = 8, 16, 32
+HC_DEVERR_LENGTH, HC_DEVERR_FREE, HC_DEVERR_POS, HC_DEVERR_WAIT = 8, 16, 32, 64
 
 DTYPE_NAMES = {"f32": HC_F32, "f16": HC_F16, "bf16": HC_BF16}
 PAIRING_NAMES = {"interleaved": HC_PAIR_INTERLEAVED, "half_split": HC_PAIR_HALF_SPLIT}
