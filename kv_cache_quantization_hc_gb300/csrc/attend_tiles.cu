@@ -199,10 +199,6 @@ struct ScaleH {
   }
 };
 
-__device__ __forceinline__ float load_scale(const void* scales, int64_t i, bool f16) {
-  return f16 ? __half2float(static_cast<const __half*>(scales)[i]) : static_cast<const float*>(scales)[i];
-}
-
 template <int D, int GROUP, bool kScaleF16>
 __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_constant__ AttendParams p, int tiles_per_head) {
   using Smem = TileSmem<D>;
@@ -317,17 +313,28 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
 
       uint32_t a[2][32];
       float top = kNegInf;
-      tmem_load32(a[0], s_at);
+      if (masked) {  // hidden columns become -inf where they are
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tmem_load32(a[0], s_at + c * 32);
+          tmem_wait_load(a[0]);
+          const int n = min(max(hi - c * 32, 0), 32), skip = min(max(lo - c * 32, 0), 32);
+          const uint32_t seen = (n == 32 ? ~0u : (1u << n) - 1u) & (skip == 32 ? 0u : ~0u << skip);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t(&x)[32] = a[c & 1];
-        tmem_wait_load(x);
-        if (c < 3) tmem_load32(a[(c + 1) & 1], s_at + (c + 1) * 32);
-        if (masked) {
+          for (int k = 0; k < 32; ++k) {
+            if (!(seen >> k & 1u)) a[0][k] = __float_as_uint(kNegInf);
+            top = fmaxf(top, __uint_as_float(a[0][k]));
+          }
+          tmem_store32(s_at + c * 32, a[0]);
+        }
+        wait_store();
+      } else {
+        tmem_load32(a[0], s_at);
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (c * 32 + k >= lo && c * 32 + k < hi) top = fmaxf(top, __uint_as_float(x[k]));
-        } else {
+        for (int c = 0; c < 4; ++c) {
+          uint32_t(&x)[32] = a[c & 1];
+          tmem_wait_load(x);
+          if (c < 3) tmem_load32(a[(c + 1) & 1], s_at + (c + 1) * 32);
 #pragma unroll
           for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
         }
@@ -365,10 +372,6 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
           float2 v = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, off2);
-          if (masked) {
-            if (!(c * 32 + k >= lo && c * 32 + k < hi)) v.x = kNegInf;
-            if (!(c * 32 + k + 1 >= lo && c * 32 + k + 1 < hi)) v.y = kNegInf;
-          }
           v.x = ex2(v.x);
           v.y = ex2(v.y);
           sum = __fadd2_rn(sum, v);
@@ -426,39 +429,63 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     const int64_t to_v = static_cast<int64_t>(p.H) << p.B_log2;  // rows from K to V
     const int swap = (part >> 1) & 1;  // block 1 writes its words in the order 2 3 0 1: other banks than block 0's
 
-    auto slot_of = [&](int j, int it) {  // -1: no such key, or no such slot
-      const int key = (vis.tile0 + j) * kKeys + (it * 128 + t) / kParts;
-      if (j >= tiles || key >= vis.hi || key < vis.lo) return -1;
-      int slot = __ldg(table + (key >> p.B_log2));
-      if (static_cast<uint32_t>(slot) >= static_cast<uint32_t>(p.num_slots)) {
-        bad |= HC_DEVERR_SLOT;
-        slot = -1;
-      }
-      return slot;
-    };
+    // Loads are issued far ahead of their use and without branches: what must not be read (a key that no row
+    // sees, a slot that does not exist) is read from the start of its array instead, and gets scale 0.
+    auto key_of = [&](int j, int it) { return (vis.tile0 + j) * kKeys + (it * 128 + t) / kParts; };
+    auto sees = [&](int key) { return key >= vis.lo && key < vis.hi; };
     uint4 code[2][kIters];
-    float scale[2][kIters];
-    int slots[kIters];
-    auto load = [&](int j, int kv) {
+    uint32_t scale[2][kIters], scale_next[2][kIters];  // as stored
+    int32_t slots[kIters];                             // of the next tile to load
+    int64_t at[kIters];                                // K row of the tile being loaded; -1: nothing there
+    auto load_slots = [&](int j) {
 #pragma unroll
       for (int it = 0; it < kIters; ++it) {
-        code[kv][it] = make_uint4(0, 0, 0, 0);
-        scale[kv][it] = 0.f;
-        if (slots[it] >= 0) {
-          const int key = (vis.tile0 + j) * kKeys + (it * 128 + t) / kParts;
-          const int64_t at = (((static_cast<int64_t>(slots[it]) * 2) * p.H + head) << p.B_log2) +
-                             (key & ((1 << p.B_log2) - 1)) + (kv ? to_v : 0);
-          code[kv][it] = __ldg(reinterpret_cast<const uint4*>(p.codes + at * (D / 2) + part * 16));
-          scale[kv][it] = load_scale(p.scales, at * kGroups + part * 32 / GROUP, kScaleF16);
-        }
+        const int key = key_of(j, it);
+        slots[it] = __ldg(j < tiles && sees(key) ? table + (key >> p.B_log2) : p.q_starts);
       }
+    };
+    auto find_rows = [&](int j) {
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) {
+        const int key = key_of(j, it);
+        const bool seen = j < tiles && sees(key), in = static_cast<uint32_t>(slots[it]) < static_cast<uint32_t>(p.num_slots);
+        if (seen && !in) bad |= HC_DEVERR_SLOT;
+        at[it] = seen && in ? (((static_cast<int64_t>(slots[it]) * 2) * p.H + head) << p.B_log2) + (key & ((1 << p.B_log2) - 1))
+                            : -1;
+      }
+    };
+    auto load_codes = [&](int kv) {
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) {
+        const int64_t row = at[it] < 0 ? 0 : at[it] + (kv ? to_v : 0);
+        code[kv][it] = __ldg(reinterpret_cast<const uint4*>(p.codes + row * (D / 2) + part * 16));
+      }
+    };
+    auto load_scales = [&]() {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+          const int64_t i = (at[it] < 0 ? 0 : at[it] + (kv ? to_v : 0)) * kGroups + part * 32 / GROUP;
+          scale_next[kv][it] = kScaleF16 ? __ldg(static_cast<const uint16_t*>(p.scales) + i)
+                                         : __ldg(static_cast<const uint32_t*>(p.scales) + i);
+        }
+    };
+    auto take_scales = [&]() {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) scale[kv][it] = at[it] < 0 ? 0u : scale_next[kv][it];
+    };
+    auto scale_value = [&](uint32_t bits) {
+      return kScaleF16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(bits))) : __uint_as_float(bits);
     };
     auto convert = [&](unsigned char* tile, int kv, int e) {
       const float up = pow2(12 - e);
 #pragma unroll
       for (int it = 0; it < kIters; ++it) {
         const int key = (it * 128 + t) / kParts;
-        const ScaleH<kScaleF16> s(scale[kv][it] * up);
+        const ScaleH<kScaleF16> s(scale_value(scale[kv][it]) * up);
         const uint4 c = code[kv][it];
         const uint32_t words[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
         unsigned char* base = tile + (part >> 1) * kBlockBytes + key * 128;
@@ -476,21 +503,24 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       }
     };
 
-#pragma unroll
-    for (int it = 0; it < kIters; ++it) slots[it] = slot_of(0, it);
-    load(0, 0);
-    load(0, 1);
+    load_slots(0);
+    find_rows(0);
+    load_scales();
+    load_codes(0);
+    load_codes(1);
+    load_slots(1);
     int ev = -100;
     bool ok = true;
     for (int j = 0; j < tiles; ++j) {
+      take_scales();
       // the tile's largest scales
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         uint32_t top = 0;
 #pragma unroll
-        for (int it = 0; it < kIters; ++it) top = max(top, __float_as_uint(scale[kv][it]) & 0x7fffffffu);
+        for (int it = 0; it < kIters; ++it) top = max(top, scale[kv][it] & (kScaleF16 ? 0x7fffu : 0x7fffffffu));
         top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) sh.top[j & 1][kv][w] = top;
+        if (lane == 0) sh.top[j & 1][kv][w] = __float_as_uint(scale_value(top));
       }
       // all of these warps go on, or none
       uint32_t stop;
@@ -511,20 +541,21 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
         sh.ev[j & 3] = ev;
       }
       mbar_arrive(&sh.e_full[j & 3]);
-#pragma unroll
-      for (int it = 0; it < kIters; ++it) slots[it] = slot_of(j + 1, it);
 
       const int st = j & 1;
       if (j >= 2) ok = ok && mbar_wait(&sh.k_empty[st], ((j >> 1) - 1) & 1, &sh.dead);
       convert(dyn + Smem::kK + st * Smem::kTileBytes, 0, ek);
       fence_async();
       mbar_arrive(&sh.k_full[st]);
-      if (j + 1 < tiles) load(j + 1, 0);
+      find_rows(j + 1);
+      load_scales();
+      load_codes(0);
+      load_slots(j + 2);
       if (j >= 2) ok = ok && mbar_wait(&sh.v_empty[st], ((j >> 1) - 1) & 1, &sh.dead);
       convert(dyn + Smem::kV + st * Smem::kTileBytes, 1, ev);
       fence_async();
       mbar_arrive(&sh.v_full[st]);
-      if (j + 1 < tiles) load(j + 1, 1);
+      load_codes(1);
     }
   } else {
     // ================================================== products, by one thread
