@@ -13,12 +13,12 @@
 // two S of 128 columns, over which P is written, and two O of d.
 //
 // Mathematics, per row, with a reference m near the running maximum:
-//   x_j = f * 2^(ek - 12) * (q . k_j),  p_j = 2^(x_j - m + 7),
-//   l = sum p_j,  O = sum p_j v_j,      out = O / l * 2^(ev - 12)
-// * k_j = code * scale * 2^(12 - ek) in fp16, 2^ek the largest key scale of the
-//   tile; v_j likewise with 2^ev the largest value scale so far.  Powers of
-//   two, so that scales of any size use fp16's range from the top and each
-//   element is rounded once.
+//   x_j = f * 2^(ek + 10) * (q . k_j),  p_j = 2^(x_j - m + 7),
+//   l = sum p_j,  O = sum p_j v_j,     out = O / l * 2^(ev - 12)
+// * k_j = code * scale * 2^(-10 - ek) in fp16, 2^ek the largest key scale of the
+//   tile; v_j = code * scale * 2^(12 - ev), 2^ev the largest value scale so
+//   far.  Powers of two, so that scales of any size fit, and each element is
+//   rounded once.
 // * Queries in fp16: each row times a power of two that brings its largest
 //   value near 2^14 (f holds the inverse).
 // * m moves only when the maximum exceeds it by 8, so that O (in tensor
@@ -30,6 +30,7 @@
 // Bound: the tensor cores (4 d flops per row and key), with the softmax's
 // exponentials and the conversion of the codes beside them.
 #include <algorithm>
+#include <type_traits>
 
 #include "attend_common.cuh"
 
@@ -42,6 +43,7 @@ constexpr int kRowsTile = 2 * kHalf;
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kThreadsTiles = (kSoftmaxWarps + kConvertWarps + 1) * 32;
 constexpr int kBlockBytes = kKeys * 128;  // 128 rows of 64 channels, swizzled in 128-byte rows
+constexpr int kKeyExp = -10;     // keys times 2^(kKeyExp - exponent of the tile's largest scale)
 constexpr float kMoveAt = 8.f;   // the reference moves when the maximum is this far above it
 
 template <int D>
@@ -94,25 +96,37 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, int32_t*
     if (mbar_try(a, parity)) return true;
   return mbar_wait_long(a, parity, dead);
 }
-__device__ __forceinline__ void commit(uint64_t* b) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(b))
-               : "memory");
+// The products are issued by one thread (`leader`), but the whole warp goes
+// along: what it computes on the way is then the same in all lanes, and stays
+// in uniform registers.
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t leader;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(leader));
+  return leader;
+}
+__device__ __forceinline__ void commit(uint64_t* b, uint32_t leader) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.u32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_addr(b)),
+      "r"(leader) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add,
+                                         uint32_t leader) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(static_cast<uint32_t>(add)) : "memory");
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add),
+      "r"(leader) : "memory");
 }
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add,
+                                         uint32_t leader) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"(static_cast<uint32_t>(add)) : "memory");
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add),
+      "r"(leader) : "memory");
 }
 __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr) {
   asm volatile(
@@ -133,6 +147,20 @@ __device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[32]) {
                    "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
                      "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
                        "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :: "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_load16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :: "memory");
 }
 __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
@@ -174,6 +202,11 @@ __device__ __forceinline__ __half2 as_half2(uint32_t u) {
   memcpy(&h, &u, 4);
   return h;
 }
+__device__ __forceinline__ uint32_t as_bits(__half2 h) {
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
 __device__ __forceinline__ __half2 both(uint16_t h) { return __half2half2(__ushort_as_half(h)); }
 __device__ __forceinline__ __half2 codes_04(uint32_t w) {
   return __hsub2(as_half2(and_xor(w, 0x000f000fu, 0x64086408u)), both(0x6408));
@@ -192,10 +225,7 @@ struct ScaleH {
     if (!kScaleF16) rest = __float2half2_rn(v - __low2float(s));
   }
   __device__ __forceinline__ uint32_t times(__half2 codes) const {
-    const __half2 r = kScaleF16 ? __hmul2(codes, s) : __hfma2(codes, s, __hmul2(codes, rest));
-    uint32_t u;
-    memcpy(&u, &r, 4);
-    return u;
+    return as_bits(kScaleF16 ? __hmul2(codes, s) : __hfma2(codes, s, __hmul2(codes, rest)));
   }
 };
 
@@ -305,79 +335,112 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       ok = mbar_wait(&sh.e_full[j & 3], (j >> 2) & 1, &sh.dead) && mbar_wait(&sh.s_full[half], j & 1, &sh.dead);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after();
-      const float f = factor * pow2(sh.ek[j & 3] - 12);
+      const float f = factor * pow2(sh.ek[j & 3] - kKeyExp);
       const int ev_new = sh.ev[j & 3];
       const int key0 = (vis.tile0 + j) * kKeys;
       const bool masked = __any_sync(0xffffffffu, key0 < first || key0 + kKeys > last);
-      const int lo = first - key0, hi = last - key0;  // columns [lo, hi) count
-
-      uint32_t a[2][32];
-      float top = kNegInf;
-      if (masked) {  // hidden columns become -inf where they are
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          tmem_load32(a[0], s_at + c * 32);
-          tmem_wait_load(a[0]);
-          const int n = min(max(hi - c * 32, 0), 32), skip = min(max(lo - c * 32, 0), 32);
-          const uint32_t seen = (n == 32 ? ~0u : (1u << n) - 1u) & (skip == 32 ? 0u : ~0u << skip);
+      // Most tiles: all of it seen, and no score more than 8 above the reference.  One pass then, with P kept
+      // in registers until the maximum is known, since it goes over the scores.
+      float2 sum = make_float2(0.f, 0.f);
+      bool done = false;
+      if (!masked && j > 0 && ev_new == ev) {
+        const float off = m == kNegInf ? 0.f : 7.f - m;
+        const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
+        uint32_t x[2][16], h[2][32];
+        float top = kNegInf;
+        tmem_load16(x[0], s_at);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (!(seen >> k & 1u)) a[0][k] = __float_as_uint(kNegInf);
-            top = fmaxf(top, __uint_as_float(a[0][k]));
+        for (int c = 0; c < 8; ++c) {
+          uint32_t(&y)[16] = x[c & 1];
+          tmem_wait_load16(y);
+          if (c < 7) tmem_load16(x[(c + 1) & 1], s_at + (c + 1) * 16);
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            float2 v = make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+            top = fmaxf(top, fmaxf(v.x, v.y));
+            v = __ffma2_rn(v, f2, off2);
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            sum = __fadd2_rn(sum, v);
+            h[c / 4][(c % 4) * 8 + k / 2] = pack_f16(v.x, v.y);
           }
-          tmem_store32(s_at + c * 32, a[0]);
         }
-        wait_store();
-      } else {
+        done = __all_sync(0xffffffffu, top * f <= m + kMoveAt);
+        if (done) {
+          tmem_store32(s_at, h[0]);
+          tmem_store32(s_at + 32, h[1]);
+        }
+      }
+      if (!done) {
+        const int lo = first - key0, hi = last - key0;  // columns [lo, hi) count
+        sum = make_float2(0.f, 0.f);
+        uint32_t a[2][32];
+        float top = kNegInf;
+        if (masked) {  // hidden columns become -inf where they are
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            tmem_load32(a[0], s_at + c * 32);
+            tmem_wait_load(a[0]);
+            const int n = min(max(hi - c * 32, 0), 32), skip = min(max(lo - c * 32, 0), 32);
+            const uint32_t seen = (n == 32 ? ~0u : (1u << n) - 1u) & (skip == 32 ? 0u : ~0u << skip);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              if (!(seen >> k & 1u)) a[0][k] = __float_as_uint(kNegInf);
+              top = fmaxf(top, __uint_as_float(a[0][k]));
+            }
+            tmem_store32(s_at + c * 32, a[0]);
+          }
+          wait_store();
+        } else {
+          tmem_load32(a[0], s_at);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&x)[32] = a[c & 1];
+            tmem_wait_load(x);
+            if (c < 3) tmem_load32(a[(c + 1) & 1], s_at + (c + 1) * 32);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+          }
+        }
         tmem_load32(a[0], s_at);
+        top *= f;
+        // the reference of the row, and O with it
+        const float m_new = top > m + kMoveAt || m == kNegInf ? fmaxf(m, top) : m;
+        if (__any_sync(0xffffffffu, m_new != m || ev_new != ev)) {
+          const float by = m == kNegInf ? 0.f : ex2(m - m_new);
+          l *= by;
+          if (j > 0) {
+            const float by_o = by * pow2(max(ev - ev_new, -126));
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_load32(a[1], o_at + c * 32);
+              tmem_wait_load(a[1]);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) a[1][k] = __float_as_uint(__uint_as_float(a[1][k]) * by_o);
+              tmem_store32(o_at + c * 32, a[1]);
+            }
+          }
+          m = m_new;
+          ev = ev_new;
+        }
+        const float off = m == kNegInf ? 0.f : 7.f - m;
+        const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t(&x)[32] = a[c & 1];
           tmem_wait_load(x);
           if (c < 3) tmem_load32(a[(c + 1) & 1], s_at + (c + 1) * 32);
+          uint32_t h[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
-        }
-      }
-      tmem_load32(a[0], s_at);
-      top *= f;
-      // the reference of the row, and O with it
-      const float m_new = top > m + kMoveAt || m == kNegInf ? fmaxf(m, top) : m;
-      if (__any_sync(0xffffffffu, m_new != m || ev_new != ev)) {
-        const float by = m == kNegInf ? 0.f : ex2(m - m_new);
-        l *= by;
-        if (j > 0) {
-          const float by_o = by * pow2(max(ev - ev_new, -126));
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            tmem_load32(a[1], o_at + c * 32);
-            tmem_wait_load(a[1]);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) a[1][k] = __float_as_uint(__uint_as_float(a[1][k]) * by_o);
-            tmem_store32(o_at + c * 32, a[1]);
+          for (int k = 0; k < 32; k += 2) {
+            float2 v = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, off2);
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            sum = __fadd2_rn(sum, v);
+            h[k / 2] = pack_f16(v.x, v.y);
           }
+          tmem_store16(s_at + c * 16, h);  // over columns already read
         }
-        m = m_new;
-        ev = ev_new;
-      }
-      const float off = m == kNegInf ? 0.f : 7.f - m;
-      const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
-      float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t(&x)[32] = a[c & 1];
-        tmem_wait_load(x);
-        if (c < 3) tmem_load32(a[(c + 1) & 1], s_at + (c + 1) * 32);
-        uint32_t h[16];
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float2 v = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, off2);
-          v.x = ex2(v.x);
-          v.y = ex2(v.y);
-          sum = __fadd2_rn(sum, v);
-          h[k / 2] = pack_f16(v.x, v.y);
-        }
-        tmem_store16(s_at + c * 16, h);  // over columns already read
       }
       l += sum.x + sum.y;
       wait_store();
@@ -425,67 +488,88 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     constexpr int kGroups = D / GROUP;
     const int t = tid - kSoftmaxWarps * 32, w = warp - kSoftmaxWarps;
     const int part = t % kParts;
-    const int32_t* table = p.tables + static_cast<int64_t>(r) * p.table_stride;
-    const int64_t to_v = static_cast<int64_t>(p.H) << p.B_log2;  // rows from K to V
     const int swap = (part >> 1) & 1;  // block 1 writes its words in the order 2 3 0 1: other banks than block 0's
 
-    // Loads are issued far ahead of their use and without branches: what must not be read (a key that no row
-    // sees, a slot that does not exist) is read from the start of its array instead, and gets scale 0.
-    auto key_of = [&](int j, int it) { return (vis.tile0 + j) * kKeys + (it * 128 + t) / kParts; };
-    auto sees = [&](int key) { return key >= vis.lo && key < vis.hi; };
+    // Loads are issued far ahead of their use and without branches: a key that no row sees, or one in a slot
+    // that does not exist, is read from a place that does (the nearest seen key's table entry; slot 0) and
+    // gets scale 0.  A thread's keys keep their places within their blocks from tile to tile, as a block's
+    // size divides a tile's, so an address is the slot times a stride away from one of kIters starts.
+    const int32_t* const table = vis.hi > 0 ? p.tables + static_cast<int64_t>(r) * p.table_stride : p.q_starts;
+    constexpr int kScaleSize = kScaleF16 ? 2 : 4;
+    const uint32_t slab = static_cast<uint32_t>(p.H) << p.B_log2;  // rows of K, or of V, in a slot
+    const uint32_t slot_codes = 2 * slab * (D / 2), slot_scales = 2 * slab * kGroups * kScaleSize;
+    const uint8_t* code_start[kIters];
+    const uint8_t* scale_start[kIters];
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int64_t row = (static_cast<int64_t>(head) << p.B_log2) + (((it * 128 + t) / kParts) & ((1 << p.B_log2) - 1));
+      code_start[it] = p.codes + row * (D / 2) + part * 16;
+      scale_start[it] = static_cast<const uint8_t*>(p.scales) + (row * kGroups + part * 32 / GROUP) * kScaleSize;
+    }
     uint4 code[2][kIters];
     uint32_t scale[2][kIters], scale_next[2][kIters];  // as stored
-    int32_t slots[kIters];                             // of the next tile to load
-    int64_t at[kIters];                                // K row of the tile being loaded; -1: nothing there
+    int32_t slots[kIters], slots_after[kIters];        // of the tile being loaded, and of the one after it
+    uint32_t there = 0;                                // bit it: the tile being loaded has that key
+    auto key_of = [&](int j, int it) { return (vis.tile0 + j) * kKeys + (it * 128 + t) / kParts; };
     auto load_slots = [&](int j) {
 #pragma unroll
-      for (int it = 0; it < kIters; ++it) {
-        const int key = key_of(j, it);
-        slots[it] = __ldg(j < tiles && sees(key) ? table + (key >> p.B_log2) : p.q_starts);
-      }
+      for (int it = 0; it < kIters; ++it)
+        slots_after[it] = __ldg(table + (max(min(key_of(j, it), vis.hi - 1), vis.lo) >> p.B_log2));
     };
-    auto find_rows = [&](int j) {
+    auto check_slots = [&](int j) {
+      there = 0;
 #pragma unroll
       for (int it = 0; it < kIters; ++it) {
         const int key = key_of(j, it);
-        const bool seen = j < tiles && sees(key), in = static_cast<uint32_t>(slots[it]) < static_cast<uint32_t>(p.num_slots);
+        const bool seen = j < tiles && key >= vis.lo && key < vis.hi;
+        const bool in = static_cast<uint32_t>(slots[it]) < static_cast<uint32_t>(p.num_slots);
         if (seen && !in) bad |= HC_DEVERR_SLOT;
-        at[it] = seen && in ? (((static_cast<int64_t>(slots[it]) * 2) * p.H + head) << p.B_log2) + (key & ((1 << p.B_log2) - 1))
-                            : -1;
+        if (seen && in) there |= 1u << it;
+        if (!in) slots[it] = 0;
       }
     };
     auto load_codes = [&](int kv) {
 #pragma unroll
-      for (int it = 0; it < kIters; ++it) {
-        const int64_t row = at[it] < 0 ? 0 : at[it] + (kv ? to_v : 0);
-        code[kv][it] = __ldg(reinterpret_cast<const uint4*>(p.codes + row * (D / 2) + part * 16));
-      }
+      for (int it = 0; it < kIters; ++it)
+        code[kv][it] = __ldg(reinterpret_cast<const uint4*>(
+            code_start[it] + static_cast<uint64_t>(static_cast<uint32_t>(slots[it])) * slot_codes +
+            (kv ? slab * (D / 2) : 0u)));
     };
     auto load_scales = [&]() {
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
-          const int64_t i = (at[it] < 0 ? 0 : at[it] + (kv ? to_v : 0)) * kGroups + part * 32 / GROUP;
-          scale_next[kv][it] = kScaleF16 ? __ldg(static_cast<const uint16_t*>(p.scales) + i)
-                                         : __ldg(static_cast<const uint32_t*>(p.scales) + i);
+          const uint8_t* at = scale_start[it] + static_cast<uint64_t>(static_cast<uint32_t>(slots[it])) * slot_scales +
+                              (kv ? slab * (kGroups * kScaleSize) : 0u);
+          scale_next[kv][it] = kScaleF16 ? __ldg(reinterpret_cast<const uint16_t*>(at))
+                                         : __ldg(reinterpret_cast<const uint32_t*>(at));
         }
     };
     auto take_scales = [&]() {
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-        for (int it = 0; it < kIters; ++it) scale[kv][it] = at[it] < 0 ? 0u : scale_next[kv][it];
+        for (int it = 0; it < kIters; ++it) scale[kv][it] = there >> it & 1u ? scale_next[kv][it] : 0u;
     };
     auto scale_value = [&](uint32_t bits) {
       return kScaleF16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(bits))) : __uint_as_float(bits);
     };
-    auto convert = [&](unsigned char* tile, int kv, int e) {
-      const float up = pow2(12 - e);
+    // Values: code times scale, the code as fp16 by way of 1024 + u.
+    // Keys: u * 2^-24 is the fp16 subnormal that the nibble u = code + 8 already is (u * 2^-20 four bits up), so
+    // one fused multiply-add by scale * 2^24 takes off 8 scales and rounds once; the tile's scales come to
+    // 2^-9 at most for that, and what is below 2^-25 then is lost: 2^-18 of the tile's largest key.  An fp32
+    // scale's rest would need two more steps there, so those keys go the values' way.
+    auto convert = [&](unsigned char* tile, auto which, int e) {
+      constexpr int kv = decltype(which)::value;
+      const float up = pow2((kv ? 12 : kKeyExp) - e);
 #pragma unroll
       for (int it = 0; it < kIters; ++it) {
         const int key = (it * 128 + t) / kParts;
-        const ScaleH<kScaleF16> s(scale_value(scale[kv][it]) * up);
+        const float sc = scale_value(scale[kv][it]) * up;
+        const ScaleH<kScaleF16> s(sc);
+        const __half2 s24 = __float2half2_rn(sc * 0x1p24f), s20 = __float2half2_rn(sc * 0x1p20f),
+                      off = __float2half2_rn(sc * -8.f);
         const uint4 c = code[kv][it];
         const uint32_t words[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
         unsigned char* base = tile + (part >> 1) * kBlockBytes + key * 128;
@@ -493,10 +577,17 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
         for (int i = 0; i < 4; ++i) {
           const uint32_t lo = words[i], hi = lo >> 8;
           uint4 v;
-          v.x = s.times(codes_04(lo));
-          v.y = s.times(codes_15(lo));
-          v.z = s.times(codes_04(hi));
-          v.w = s.times(codes_15(hi));
+          if (kv || !kScaleF16) {
+            v.x = s.times(codes_04(lo));
+            v.y = s.times(codes_15(lo));
+            v.z = s.times(codes_04(hi));
+            v.w = s.times(codes_15(hi));
+          } else {
+            v.x = as_bits(__hfma2(as_half2(and_xor(lo, 0x000f000fu, 0x00080008u)), s24, off));
+            v.y = as_bits(__hfma2(as_half2(and_xor(lo, 0x00f000f0u, 0x00800080u)), s20, off));
+            v.z = as_bits(__hfma2(as_half2(and_xor(hi, 0x000f000fu, 0x00080008u)), s24, off));
+            v.w = as_bits(__hfma2(as_half2(and_xor(hi, 0x00f000f0u, 0x00800080u)), s20, off));
+          }
           const int chunk = (part & 1) * 4 + (i ^ (swap * 2));
           *reinterpret_cast<uint4*>(base + ((chunk ^ (key & 7)) << 4)) = v;
         }
@@ -504,7 +595,9 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     };
 
     load_slots(0);
-    find_rows(0);
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) slots[it] = slots_after[it];
+    check_slots(0);
     load_scales();
     load_codes(0);
     load_codes(1);
@@ -534,8 +627,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
         top_k = max(top_k, sh.top[j & 1][0][i]);
         top_v = max(top_v, sh.top[j & 1][1][i]);
       }
-      const int ek = max(static_cast<int>(top_k >> 23) - 127, -100);
-      ev = max(ev, static_cast<int>(top_v >> 23) - 127);
+      const int ek = min(max(static_cast<int>(top_k >> 23) - 127, -100), 110);
+      ev = max(ev, min(static_cast<int>(top_v >> 23) - 127, 110));
       if (t == 0) {
         sh.ek[j & 3] = ek;
         sh.ev[j & 3] = ev;
@@ -544,73 +637,74 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
 
       const int st = j & 1;
       if (j >= 2) ok = ok && mbar_wait(&sh.k_empty[st], ((j >> 1) - 1) & 1, &sh.dead);
-      convert(dyn + Smem::kK + st * Smem::kTileBytes, 0, ek);
+      convert(dyn + Smem::kK + st * Smem::kTileBytes, std::integral_constant<int, 0>(), ek);
       fence_async();
       mbar_arrive(&sh.k_full[st]);
-      find_rows(j + 1);
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) slots[it] = slots_after[it];
+      check_slots(j + 1);
       load_scales();
       load_codes(0);
       load_slots(j + 2);
       if (j >= 2) ok = ok && mbar_wait(&sh.v_empty[st], ((j >> 1) - 1) & 1, &sh.dead);
-      convert(dyn + Smem::kV + st * Smem::kTileBytes, 1, ev);
+      convert(dyn + Smem::kV + st * Smem::kTileBytes, std::integral_constant<int, 1>(), ev);
       fence_async();
       mbar_arrive(&sh.v_full[st]);
       load_codes(1);
     }
   } else {
-    // ================================================== products, by one thread
-    if (lane == 0) {
-    const uint32_t base = smem_addr(dyn);
-    bool ok = true;
+    // ================================================== products
+    const uint32_t leader = elect_leader();
+    const uint32_t at = __shfl_sync(0xffffffffu, tmem, 0), base = __shfl_sync(0xffffffffu, smem_addr(dyn), 0);
     auto scores = [&](int i, int j) {  // S_i = Q_i K(j)^T
+      const uint64_t q = smem_desc(base + Smem::kQ + i * Smem::kTileBytes, 16);
+      const uint64_t k = smem_desc(base + Smem::kK + (j & 1) * Smem::kTileBytes, 16);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t step = (k / 4) * kBlockBytes + (k % 4) * 32;
-        mma_smem(tmem + i * 128, smem_desc(base + Smem::kQ + i * Smem::kTileBytes + step, 16),
-                 smem_desc(base + Smem::kK + (j & 1) * Smem::kTileBytes + step, 16), instr_desc(kKeys, false), k > 0);
+      for (int s = 0; s < D / 16; ++s) {
+        const uint64_t step = ((s / 4) * kBlockBytes + (s % 4) * 32) >> 4;
+        mma_smem(at + i * 128, q + step, k + step, instr_desc(kKeys, false), s > 0, leader);
       }
-      commit(&sh.s_full[i]);
+      commit(&sh.s_full[i], leader);
     };
     auto values = [&](int i, int j) {  // O_i += P_i(j) V(j)
+      const uint64_t v = smem_desc(base + Smem::kV + (j & 1) * Smem::kTileBytes, kBlockBytes);
 #pragma unroll
-      for (int k = 0; k < kKeys / 16; ++k)
-        mma_tmem(tmem + 256 + i * D, tmem + i * 128 + k * 8,
-                 smem_desc(base + Smem::kV + (j & 1) * Smem::kTileBytes + k * 2048, kBlockBytes), instr_desc(D, true),
-                 j > 0 || k > 0);
+      for (int s = 0; s < kKeys / 16; ++s)
+        mma_tmem(at + 256 + i * D, at + i * 128 + s * 8, v + s * (2048 >> 4), instr_desc(D, true), j > 0 || s > 0, leader);
     };
+    bool ok = true;
     for (int j = 0; j <= tiles && ok; ++j) {
-      for (int i = 0; i < 2 && ok; ++i) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
         if (j > 0) {
-          ok = mbar_wait(&sh.v_full[(j - 1) & 1], ((j - 1) >> 1) & 1, &sh.dead) &&
+          ok = ok && mbar_wait(&sh.v_full[(j - 1) & 1], ((j - 1) >> 1) & 1, &sh.dead) &&
                mbar_wait(&sh.p_full[i], (j - 1) & 1, &sh.dead);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           fence_after();
           values(i, j - 1);
-          if (i == 1) commit(&sh.v_empty[(j - 1) & 1]);
+          if (i == 1) commit(&sh.v_empty[(j - 1) & 1], leader);
         }
         if (j < tiles) {
-          ok = mbar_wait(&sh.k_full[j & 1], (j >> 1) & 1, &sh.dead);
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.k_full[j & 1], (j >> 1) & 1, &sh.dead));
           if (!ok) break;
           fence_after();
           scores(i, j);
-          if (i == 1) commit(&sh.k_empty[j & 1]);
+          if (i == 1) commit(&sh.k_empty[j & 1], leader);
         } else {
-          commit(&sh.s_full[i]);  // O_i is complete
+          commit(&sh.s_full[i], leader);  // O_i is complete
         }
       }
-    }
     }
     __syncwarp();
   }
   __syncthreads();
   if (warp == kSoftmaxWarps + kConvertWarps) {
     if (sh.dead) {  // products may still be on their way: wait for them before their memory goes
-      if (lane == 0) {
-        flag_error(p.err, HC_DEVERR_WAIT);
-        int32_t no = 0;
-        commit(&sh.drain);
-        mbar_wait(&sh.drain, 0, &no);
-      }
+      if (lane == 0) flag_error(p.err, HC_DEVERR_WAIT);
+      int32_t no = 0;
+      commit(&sh.drain, elect_leader());
+      mbar_wait(&sh.drain, 0, &no);
       __syncwarp();
     }
     fence_after();
