@@ -13,12 +13,13 @@
 // two S of 128 columns, over which P is written, and two O of d.
 //
 // Mathematics, per row, with a reference m near the running maximum:
-//   x_j = f * 2^(ek + 10) * (q . k_j),  p_j = 2^(x_j - m + 7),
-//   l = sum p_j,  O = sum p_j v_j,     out = O / l * 2^(ev - 12)
-// * k_j = code * scale * 2^(-10 - ek) in fp16, 2^ek the largest key scale of the
-//   tile; v_j = code * scale * 2^(12 - ev), 2^ev the largest value scale so
-//   far.  Powers of two, so that scales of any size fit, and each element is
-//   rounded once.
+//   x_j = f * 2^(ek + 10) * (q . k_j),  p_j = 2^(x_j - m + 7),  l = sum p_j,
+//   O = sum (p_j * 2^(ev_j - ev)) v_j,  out = O / l * 2^(ev - 12)
+// * k_j = code * scale * 2^(-10 - ek) and v_j = code * scale * 2^(12 - ev_j) in
+//   fp16, 2^ek and 2^ev_j the largest scales of the run of 32 keys that j is
+//   in, 2^ev the largest so far.  Powers of two, so that scales of any size
+//   fit, and each element is rounded once.  A run is one warp's to convert, so
+//   its exponents are too: no barrier among those warps.
 // * Queries in fp16: each row times a power of two that brings its largest
 //   value near 2^14 (f holds the inverse).
 // * m moves only when the maximum exceeds it by 8, so that O (in tensor
@@ -43,7 +44,7 @@ constexpr int kRowsTile = 2 * kHalf;
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kThreadsTiles = (kSoftmaxWarps + kConvertWarps + 1) * 32;
 constexpr int kBlockBytes = kKeys * 128;  // 128 rows of 64 channels, swizzled in 128-byte rows
-constexpr int kKeyExp = -10;     // keys times 2^(kKeyExp - exponent of the tile's largest scale)
+constexpr int kKeyExp = -10;     // keys times 2^(kKeyExp - exponent of the run's largest scale)
 constexpr float kMoveAt = 8.f;   // the reference moves when the maximum is this far above it
 
 template <int D>
@@ -59,8 +60,7 @@ struct TileShared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], e_full[4], drain;
   uint32_t tmem;
   int32_t dead;               // some wait ran out
-  uint32_t top[2][2][kConvertWarps];  // [tile & 1][keys, values][warp]: largest scale's bits
-  int32_t ek[4], ev[4];       // of tile j at j & 3
+  int4 ek[4], ev[4];          // of tile j at j & 3: the exponents of its 4 runs of 32 keys
 };
 
 // ------------------------------------------------------------ PTX
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], kHalf);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.e_full[i], kConvertWarps * 32);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.e_full[i], kConvertWarps);
     mbar_init(&sh.drain, 1);
     sh.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -335,37 +335,49 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       ok = mbar_wait(&sh.e_full[j & 3], (j >> 2) & 1, &sh.dead) && mbar_wait(&sh.s_full[half], j & 1, &sh.dead);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after();
-      const float f = factor * pow2(sh.ek[j & 3] - kKeyExp);
-      const int ev_new = sh.ev[j & 3];
+      const int4 ek4 = sh.ek[j & 3], ev4 = sh.ev[j & 3];
+      const int ek[4] = {ek4.x, ek4.y, ek4.z, ek4.w}, evs[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
+      const int ev_new = max(ev, max(max(evs[0], evs[1]), max(evs[2], evs[3])));
+      float f[4];  // the scores' factor, of each run of 32 keys
+#pragma unroll
+      for (int c = 0; c < 4; ++c) f[c] = factor * pow2(ek[c] - kKeyExp);
       const int key0 = (vis.tile0 + j) * kKeys;
       const bool masked = __any_sync(0xffffffffu, key0 < first || key0 + kKeys > last);
       // Most tiles: all of it seen, and no score more than 8 above the reference.  One pass then, with P kept
       // in registers until the maximum is known, since it goes over the scores.
-      float2 sum = make_float2(0.f, 0.f);
+      float sum = 0.f;
       bool done = false;
       if (!masked && j > 0 && ev_new == ev) {
-        const float off = m == kNegInf ? 0.f : 7.f - m;
-        const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
         uint32_t x[2][16], h[2][32];
         float top = kNegInf;
         tmem_load16(x[0], s_at);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t(&y)[16] = x[c & 1];
-          tmem_wait_load16(y);
-          if (c < 7) tmem_load16(x[(c + 1) & 1], s_at + (c + 1) * 16);
+        for (int c = 0; c < 4; ++c) {
+          const int d = max(evs[c] - ev, -126);
+          const float off = m == kNegInf ? 0.f : 7.f - m + static_cast<float>(d);
+          const float2 f2 = make_float2(f[c], f[c]), off2 = make_float2(off, off);
+          float2 part = make_float2(0.f, 0.f);
+          float most = kNegInf;
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float2 v = make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
-            top = fmaxf(top, fmaxf(v.x, v.y));
-            v = __ffma2_rn(v, f2, off2);
-            v.x = ex2(v.x);
-            v.y = ex2(v.y);
-            sum = __fadd2_rn(sum, v);
-            h[c / 4][(c % 4) * 8 + k / 2] = pack_f16(v.x, v.y);
+          for (int u = 0; u < 2; ++u) {
+            uint32_t(&y)[16] = x[u];
+            tmem_wait_load16(y);
+            if (c < 3 || u < 1) tmem_load16(x[u ^ 1], s_at + c * 32 + (u + 1) * 16);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float2 v = make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+              most = fmaxf(most, fmaxf(v.x, v.y));
+              v = __ffma2_rn(v, f2, off2);
+              v.x = ex2(v.x);
+              v.y = ex2(v.y);
+              part = __fadd2_rn(part, v);
+              h[c / 2][(c % 2) * 16 + u * 8 + k / 2] = pack_f16(v.x, v.y);
+            }
           }
+          top = fmaxf(top, most * f[c]);
+          sum = fmaf(part.x + part.y, pow2(-d), sum);
         }
-        done = __all_sync(0xffffffffu, top * f <= m + kMoveAt);
+        done = __all_sync(0xffffffffu, top <= m + kMoveAt);
         if (done) {
           tmem_store32(s_at, h[0]);
           tmem_store32(s_at + 32, h[1]);
@@ -373,37 +385,27 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       }
       if (!done) {
         const int lo = first - key0, hi = last - key0;  // columns [lo, hi) count
-        sum = make_float2(0.f, 0.f);
-        uint32_t a[2][32];
+        sum = 0.f;
+        uint32_t a[32];
         float top = kNegInf;
-        if (masked) {  // hidden columns become -inf where they are
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            tmem_load32(a[0], s_at + c * 32);
-            tmem_wait_load(a[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_load32(a, s_at + c * 32);
+          tmem_wait_load(a);
+          float most = kNegInf;
+          if (masked) {  // hidden columns become -inf where they are
             const int n = min(max(hi - c * 32, 0), 32), skip = min(max(lo - c * 32, 0), 32);
             const uint32_t seen = (n == 32 ? ~0u : (1u << n) - 1u) & (skip == 32 ? 0u : ~0u << skip);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if (!(seen >> k & 1u)) a[0][k] = __float_as_uint(kNegInf);
-              top = fmaxf(top, __uint_as_float(a[0][k]));
-            }
-            tmem_store32(s_at + c * 32, a[0]);
+            for (int k = 0; k < 32; ++k)
+              if (!(seen >> k & 1u)) a[k] = __float_as_uint(kNegInf);
+            tmem_store32(s_at + c * 32, a);
           }
-          wait_store();
-        } else {
-          tmem_load32(a[0], s_at);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&x)[32] = a[c & 1];
-            tmem_wait_load(x);
-            if (c < 3) tmem_load32(a[(c + 1) & 1], s_at + (c + 1) * 32);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
-          }
+          for (int k = 0; k < 32; k += 2) most = fmaxf(most, fmaxf(__uint_as_float(a[k]), __uint_as_float(a[k + 1])));
+          top = fmaxf(top, most * f[c]);
         }
-        tmem_load32(a[0], s_at);
-        top *= f;
+        if (masked) wait_store();
         // the reference of the row, and O with it
         const float m_new = top > m + kMoveAt || m == kNegInf ? fmaxf(m, top) : m;
         if (__any_sync(0xffffffffu, m_new != m || ev_new != ev)) {
@@ -411,38 +413,40 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
           l *= by;
           if (j > 0) {
             const float by_o = by * pow2(max(ev - ev_new, -126));
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-              tmem_load32(a[1], o_at + c * 32);
-              tmem_wait_load(a[1]);
+              tmem_load32(a, o_at + c * 32);
+              tmem_wait_load(a);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) a[1][k] = __float_as_uint(__uint_as_float(a[1][k]) * by_o);
-              tmem_store32(o_at + c * 32, a[1]);
+              for (int k = 0; k < 32; ++k) a[k] = __float_as_uint(__uint_as_float(a[k]) * by_o);
+              tmem_store32(o_at + c * 32, a);
             }
           }
           m = m_new;
           ev = ev_new;
         }
-        const float off = m == kNegInf ? 0.f : 7.f - m;
-        const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t(&x)[32] = a[c & 1];
-          tmem_wait_load(x);
-          if (c < 3) tmem_load32(a[(c + 1) & 1], s_at + (c + 1) * 32);
+          const int d = max(evs[c] - ev, -126);
+          const float off = m == kNegInf ? 0.f : 7.f - m + static_cast<float>(d);
+          const float2 f2 = make_float2(f[c], f[c]), off2 = make_float2(off, off);
+          float2 part = make_float2(0.f, 0.f);
           uint32_t h[16];
+          tmem_load32(a, s_at + c * 32);
+          tmem_wait_load(a);
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
-            float2 v = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, off2);
+            float2 v = __ffma2_rn(make_float2(__uint_as_float(a[k]), __uint_as_float(a[k + 1])), f2, off2);
             v.x = ex2(v.x);
             v.y = ex2(v.y);
-            sum = __fadd2_rn(sum, v);
+            part = __fadd2_rn(part, v);
             h[k / 2] = pack_f16(v.x, v.y);
           }
           tmem_store16(s_at + c * 16, h);  // over columns already read
+          sum = fmaf(part.x + part.y, pow2(-d), sum);
         }
       }
-      l += sum.x + sum.y;
+      l += sum;
       wait_store();
       fence_before();
       mbar_arrive(&sh.p_full[half]);
@@ -484,10 +488,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
   } else if (warp < kSoftmaxWarps + kConvertWarps) {
     // ================================================== codes to fp16 tiles
     constexpr int kParts = D / 32;   // threads of a key, 32 channels each: one group's scale
-    constexpr int kIters = kParts;   // 128 keys * kParts / 128 threads
+    constexpr int kIters = kParts;   // a warp has 32 keys of the tile, 32 / kParts at a time
     constexpr int kGroups = D / GROUP;
     const int t = tid - kSoftmaxWarps * 32, w = warp - kSoftmaxWarps;
     const int part = t % kParts;
+    auto place = [&](int it) { return w * 32 + it * (32 / kParts) + lane / kParts; };  // a key's, in the tile
     const int swap = (part >> 1) & 1;  // block 1 writes its words in the order 2 3 0 1: other banks than block 0's
 
     // Loads are issued far ahead of their use and without branches: a key that no row sees, or one in a slot
@@ -502,37 +507,39 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     const uint8_t* scale_start[kIters];
 #pragma unroll
     for (int it = 0; it < kIters; ++it) {
-      const int64_t row = (static_cast<int64_t>(head) << p.B_log2) + (((it * 128 + t) / kParts) & ((1 << p.B_log2) - 1));
+      const int64_t row = (static_cast<int64_t>(head) << p.B_log2) + (place(it) & ((1 << p.B_log2) - 1));
       code_start[it] = p.codes + row * (D / 2) + part * 16;
       scale_start[it] = static_cast<const uint8_t*>(p.scales) + (row * kGroups + part * 32 / GROUP) * kScaleSize;
     }
     uint4 code[2][kIters];
-    uint32_t scale[2][kIters], scale_next[2][kIters];  // as stored
-    int32_t slots[kIters], slots_after[kIters];        // of the tile being loaded, and of the one after it
-    uint32_t there = 0;                                // bit it: the tile being loaded has that key
-    auto key_of = [&](int j, int it) { return (vis.tile0 + j) * kKeys + (it * 128 + t) / kParts; };
+    // While tile j is converted, the codes and scales of j + 1 and the slots of j + 2 are on their way (L2 answers
+    // in 1000 cycles and more under this load; a tile takes 2500).
+    uint32_t scale[2][kIters], scale_next[2][kIters];  // of tiles j and j + 1, as stored
+    int32_t slots_next[kIters], slots_after[kIters];   // of tiles j + 1 and j + 2
+    uint32_t there = 0;                                // bit it: the tile of slots_next has that key
+    auto key_of = [&](int j, int it) { return (vis.tile0 + j) * kKeys + place(it); };
     auto load_slots = [&](int j) {
 #pragma unroll
       for (int it = 0; it < kIters; ++it)
         slots_after[it] = __ldg(table + (max(min(key_of(j, it), vis.hi - 1), vis.lo) >> p.B_log2));
     };
-    auto check_slots = [&](int j) {
+    auto next_slots = [&](int j) {  // slots_after, of tile j, become slots_next
       there = 0;
 #pragma unroll
       for (int it = 0; it < kIters; ++it) {
         const int key = key_of(j, it);
         const bool seen = j < tiles && key >= vis.lo && key < vis.hi;
-        const bool in = static_cast<uint32_t>(slots[it]) < static_cast<uint32_t>(p.num_slots);
+        const bool in = static_cast<uint32_t>(slots_after[it]) < static_cast<uint32_t>(p.num_slots);
         if (seen && !in) bad |= HC_DEVERR_SLOT;
         if (seen && in) there |= 1u << it;
-        if (!in) slots[it] = 0;
+        slots_next[it] = in ? slots_after[it] : 0;
       }
     };
     auto load_codes = [&](int kv) {
 #pragma unroll
       for (int it = 0; it < kIters; ++it)
         code[kv][it] = __ldg(reinterpret_cast<const uint4*>(
-            code_start[it] + static_cast<uint64_t>(static_cast<uint32_t>(slots[it])) * slot_codes +
+            code_start[it] + static_cast<uint64_t>(static_cast<uint32_t>(slots_next[it])) * slot_codes +
             (kv ? slab * (D / 2) : 0u)));
     };
     auto load_scales = [&]() {
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
-          const uint8_t* at = scale_start[it] + static_cast<uint64_t>(static_cast<uint32_t>(slots[it])) * slot_scales +
+          const uint8_t* at = scale_start[it] + static_cast<uint64_t>(static_cast<uint32_t>(slots_next[it])) * slot_scales +
                               (kv ? slab * (kGroups * kScaleSize) : 0u);
           scale_next[kv][it] = kScaleF16 ? __ldg(reinterpret_cast<const uint16_t*>(at))
                                          : __ldg(reinterpret_cast<const uint32_t*>(at));
@@ -557,15 +564,15 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     };
     // Values: code times scale, the code as fp16 by way of 1024 + u.
     // Keys: u * 2^-24 is the fp16 subnormal that the nibble u = code + 8 already is (u * 2^-20 four bits up), so
-    // one fused multiply-add by scale * 2^24 takes off 8 scales and rounds once; the tile's scales come to
-    // 2^-9 at most for that, and what is below 2^-25 then is lost: 2^-18 of the tile's largest key.  An fp32
+    // one fused multiply-add by scale * 2^24 takes off 8 scales and rounds once; the run's scales come to
+    // 2^-9 at most for that, and what is below 2^-25 then is lost: 2^-18 of the run's largest key.  An fp32
     // scale's rest would need two more steps there, so those keys go the values' way.
     auto convert = [&](unsigned char* tile, auto which, int e) {
       constexpr int kv = decltype(which)::value;
       const float up = pow2((kv ? 12 : kKeyExp) - e);
 #pragma unroll
       for (int it = 0; it < kIters; ++it) {
-        const int key = (it * 128 + t) / kParts;
+        const int key = place(it);
         const float sc = scale_value(scale[kv][it]) * up;
         const ScaleH<kScaleF16> s(sc);
         const __half2 s24 = __float2half2_rn(sc * 0x1p24f), s20 = __float2half2_rn(sc * 0x1p20f),
@@ -595,62 +602,50 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     };
 
     load_slots(0);
-#pragma unroll
-    for (int it = 0; it < kIters; ++it) slots[it] = slots_after[it];
-    check_slots(0);
+    next_slots(0);
+    load_slots(1);
     load_scales();
     load_codes(0);
     load_codes(1);
-    load_slots(1);
-    int ev = -100;
+    take_scales();
+    next_slots(1);
+    load_scales();
+    load_slots(2);
     bool ok = true;
     for (int j = 0; j < tiles; ++j) {
-      take_scales();
-      // the tile's largest scales
+      // the exponents of the run's largest scales
+      int e[2];
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         uint32_t top = 0;
 #pragma unroll
         for (int it = 0; it < kIters; ++it) top = max(top, scale[kv][it] & (kScaleF16 ? 0x7fffu : 0x7fffffffu));
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) sh.top[j & 1][kv][w] = __float_as_uint(scale_value(top));
+        top = __float_as_uint(scale_value(__reduce_max_sync(0xffffffffu, top)));
+        e[kv] = min(max(static_cast<int>(top >> 23) - 127, -100), 110);
       }
-      // all of these warps go on, or none
-      uint32_t stop;
-      asm volatile(
-          "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}"
-          : "=r"(stop) : "r"(static_cast<uint32_t>(!ok)) : "memory");
-      if (stop) break;
-      uint32_t top_k = 0, top_v = 0;
-#pragma unroll
-      for (int i = 0; i < kConvertWarps; ++i) {
-        top_k = max(top_k, sh.top[j & 1][0][i]);
-        top_v = max(top_v, sh.top[j & 1][1][i]);
+      if (lane == 0) {
+        reinterpret_cast<int*>(&sh.ek[j & 3])[w] = e[0];
+        reinterpret_cast<int*>(&sh.ev[j & 3])[w] = e[1];
+        mbar_arrive(&sh.e_full[j & 3]);
       }
-      const int ek = min(max(static_cast<int>(top_k >> 23) - 127, -100), 110);
-      ev = max(ev, min(static_cast<int>(top_v >> 23) - 127, 110));
-      if (t == 0) {
-        sh.ek[j & 3] = ek;
-        sh.ev[j & 3] = ev;
-      }
-      mbar_arrive(&sh.e_full[j & 3]);
+      ok = __all_sync(0xffffffffu, ok);  // the warp goes on, or not
+      if (!ok) break;
 
       const int st = j & 1;
       if (j >= 2) ok = ok && mbar_wait(&sh.k_empty[st], ((j >> 1) - 1) & 1, &sh.dead);
-      convert(dyn + Smem::kK + st * Smem::kTileBytes, std::integral_constant<int, 0>(), ek);
+      convert(dyn + Smem::kK + st * Smem::kTileBytes, std::integral_constant<int, 0>(), e[0]);
       fence_async();
       mbar_arrive(&sh.k_full[st]);
-#pragma unroll
-      for (int it = 0; it < kIters; ++it) slots[it] = slots_after[it];
-      check_slots(j + 1);
-      load_scales();
-      load_codes(0);
-      load_slots(j + 2);
+      load_codes(0);  // of j + 1
       if (j >= 2) ok = ok && mbar_wait(&sh.v_empty[st], ((j >> 1) - 1) & 1, &sh.dead);
-      convert(dyn + Smem::kV + st * Smem::kTileBytes, std::integral_constant<int, 1>(), ev);
+      convert(dyn + Smem::kV + st * Smem::kTileBytes, std::integral_constant<int, 1>(), e[1]);
       fence_async();
       mbar_arrive(&sh.v_full[st]);
       load_codes(1);
+      take_scales();
+      next_slots(j + 2);
+      load_scales();
+      load_slots(j + 3);
     }
   } else {
     // ================================================== products
