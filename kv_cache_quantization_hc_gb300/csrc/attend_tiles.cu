@@ -2,7 +2,10 @@
 // 256 rows (new tokens times the query heads of one cache head) against tiles
 // of 128 keys on the 5th-generation tensor cores.
 //
-// One CTA per 256 rows, 13 warps:
+// One CTA per SM takes runs of 256 rows one after another, the longest first
+// (k-th run: number k * CTAs + i, or the mirror of it for odd k, which evens
+// the sums out).  Its 13 warps each go through the runs by themselves, so that
+// one's codes are converted while the last one's result is still written:
 //   warps 0-3, 4-7  the softmax of rows 0-127 and 128-255, a thread per row;
 //   warps 8-11      codes and scales into fp16 tiles of keys and values in
 //                   shared memory, two of each ahead;
@@ -57,10 +60,11 @@ struct TileSmem {
 };
 
 struct TileShared {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], e_full[4], drain;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], q_full[2], e_full[4], drain;
   uint32_t tmem;
   int32_t dead;               // some wait ran out
   int4 ek[4], ev[4];          // of tile j at j & 3: the exponents of its 4 runs of 32 keys
+  int32_t q_exp[kRowsTile];   // of a row's largest query
 };
 
 // ------------------------------------------------------------ PTX
@@ -229,8 +233,56 @@ struct ScaleH {
   }
 };
 
+// Work of a CTA: 256 rows of one request and cache head.
+struct Work {
+  Request rq;
+  int r, head, row0, rows_all, tiles;
+  Range vis;
+};
+// Number `idx` of the call's works, found by a warp (all lanes get it); false
+// past the last.  `c` goes forward only, so idx may not fall.
+struct Cursor {
+  int r0 = 0, before = 0;  // first request of 32, works of those before it
+};
+__device__ __forceinline__ bool find_work(const AttendParams& p, Cursor& c, int idx, int lane, Work& w) {
+  for (; c.r0 < p.n_req; c.r0 += 32) {
+    Request q{0, 0, 0};
+    int bad = 0;  // lengths are reported by k_attend_rows
+    if (c.r0 + lane < p.n_req) q = load_request(p, c.r0 + lane, bad);
+    const int rows = q.n * p.G > p.rows_above ? q.n * p.G : 0;
+    const int works = (rows + kRowsTile - 1) / kRowsTile * p.H;
+    int inc = works;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const uint32_t upto = __ballot_sync(0xffffffffu, idx < c.before + inc);
+    if (upto == 0) {
+      c.before += __shfl_sync(0xffffffffu, inc, 31);
+      continue;
+    }
+    const int src = __ffs(static_cast<int>(upto)) - 1;
+    w.r = c.r0 + src;
+    w.rq = {__shfl_sync(0xffffffffu, q.q0, src), __shfl_sync(0xffffffffu, q.n, src), __shfl_sync(0xffffffffu, q.kv, src)};
+    w.rows_all = __shfl_sync(0xffffffffu, rows, src);
+    const int left = __shfl_sync(0xffffffffu, c.before + inc, src) - 1 - idx;  // the last rows first: most keys
+    const int rt = left / p.H;
+    w.head = left - rt * p.H;
+    w.row0 = rt * kRowsTile;
+    w.vis = visible<kKeys>(p, w.rq, w.row0, min(w.row0 + kRowsTile, w.rows_all));
+    w.tiles = w.vis.tiles;
+    return true;
+  }
+  return false;
+}
+__device__ __forceinline__ int work_number(int k) {
+  const int g = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+  return k * g + (k & 1 ? g - 1 - b : b);
+}
+
 template <int D, int GROUP, bool kScaleF16>
-__global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_constant__ AttendParams p, int tiles_per_head) {
+__global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_constant__ AttendParams p) {
   using Smem = TileSmem<D>;
   extern __shared__ unsigned char dyn_raw[];
   __shared__ TileShared sh;
@@ -238,14 +290,9 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   int bad = 0;
 
-  // ---- this CTA's rows: the last tiles of a request first, they have the most keys
-  const int rh = blockIdx.x / tiles_per_head, rt = tiles_per_head - 1 - (blockIdx.x - rh * tiles_per_head);
-  const int r = rh / p.H, head = rh - r * p.H;
-  const Request rq = load_request(p, r, bad);
-  bad = 0;  // lengths are reported by k_attend_rows
-  const int rows_all = rq.n * p.G, row0 = rt * kRowsTile;
-  if (rows_all <= p.rows_above || row0 >= rows_all) return;
-  const Range vis = visible<kKeys>(p, rq, row0, min(row0 + kRowsTile, rows_all));
+  Cursor cursor;
+  Work work;
+  if (!find_work(p, cursor, work_number(0), lane, work)) return;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -255,6 +302,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       mbar_init(&sh.v_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], kHalf);
+      mbar_init(&sh.q_full[i], kHalf);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&sh.e_full[i], kConvertWarps);
     mbar_init(&sh.drain, 1);
@@ -267,75 +315,84 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
 
-  // ---- queries: a softmax thread per row
-  float factor = 0.f;
-  int first = 0, last = 0x7fffffff;  // keys that the thread's row sees
-  const int row = row0 + tid;        // of a softmax thread
-  int token = 0, q_head = 0;
-  if (warp < kSoftmaxWarps) {
-    const bool live = row < rows_all;
-    uint4 raw[D / 8];
-    float amax = 0.f;
-    if (live) {
-      const int i = static_cast<int>(p.by_group.div(row));
-      token = rq.q0 + i;
-      q_head = head * p.G + row - i * p.G;
-      const int pos = rq.kv - rq.n + i;
-      last = p.causal ? min(rq.kv, pos + 1) : rq.kv;
-      if (p.window) first = pos - p.window + 1;
-      const uint16_t* src = static_cast<const uint16_t*>(p.q) + token * p.q_token + q_head * p.q_head;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + c * 8);
-    } else {
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) raw[c] = make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const uint32_t u[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 v = widen(u[k], p.bf16);
-        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
-      }
-    }
-    const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100), 100);
-    const float up = p.scale_log2 < 0.f ? -pow2(14 - e) : pow2(14 - e);
-    factor = fabsf(p.scale_log2) * pow2(e - 14);
-    unsigned char* q = dyn + Smem::kQ + (tid / kHalf) * Smem::kTileBytes;
-    const int rr = tid % kHalf;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const float2 a = widen(raw[c].x, p.bf16), b = widen(raw[c].y, p.bf16), cc = widen(raw[c].z, p.bf16),
-                   d = widen(raw[c].w, p.bf16);
-      uint4 w;  // channels 0 4 1 5 2 6 3 7
-      w.x = pack_f16(a.x * up, cc.x * up);
-      w.y = pack_f16(a.y * up, cc.y * up);
-      w.z = pack_f16(b.x * up, d.x * up);
-      w.w = pack_f16(b.y * up, d.y * up);
-      *reinterpret_cast<uint4*>(q + (c / 8) * kBlockBytes + rr * 128 + (((c % 8) ^ (rr & 7)) << 4)) = w;
-    }
-    fence_async();
-  }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = sh.tmem;
-  const int tiles = vis.tiles;
+  bool ok = true;
+  int base = 0;  // tiles of the works so far
 
   if (warp < kSoftmaxWarps) {
     // ================================================== softmax
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes of tensor memory per warp
     const uint32_t s_at = tmem + lanes + half * 128, o_at = tmem + lanes + 256 + half * D;
+    // A row's 16-byte pieces belong to D / 8 lanes where rows are read and written.
+    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
+    const int piece = lane % kLanes;
+    unsigned char* const rows_smem = dyn + Smem::kQ + half * Smem::kTileBytes + (warp & 3) * 32 * 128;
+    auto piece_at = [&](int at, int c) {  // piece c of the warp's row `at`: queries, then the result
+      return reinterpret_cast<uint4*>(rows_smem + (c / 8) * kBlockBytes + at * 128 + (((c % 8) ^ (at & 7)) << 4));
+    };
+    for (int k = 0; k == 0 || find_work(p, cursor, work_number(k), lane, work); ++k) {
+    const Request rq = work.rq;
+    const Range vis = work.vis;
+    const int head = work.head, rows_all = work.rows_all, tiles = work.tiles, row = work.row0 + tid;
+    auto row_offset = [&](int rr, int64_t token, int64_t head_stride) {  // of row rr in q or out
+      const int i = static_cast<int>(p.by_group.div(rr));
+      return static_cast<int64_t>(rq.q0 + i) * token + static_cast<int64_t>(head * p.G + rr - i * p.G) * head_stride;
+    };
+    // ---- queries
+    const int row_first = work.row0 + warp * 32 + lane / kLanes;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 8 * kRowsAt) {
+      uint4 raw[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int rr = row_first + r0 + u * kRowsAt;
+        raw[u] = make_uint4(0, 0, 0, 0);
+        if (rr < rows_all)
+          raw[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row_offset(rr, p.q_token, p.q_head) + piece * 8);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float2 a = widen(raw[u].x, p.bf16), b = widen(raw[u].y, p.bf16), c = widen(raw[u].z, p.bf16),
+                     d = widen(raw[u].w, p.bf16);
+        float amax = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
+                           fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100), 100);
+        const float up = p.scale_log2 < 0.f ? -pow2(14 - e) : pow2(14 - e);
+        uint4 w;  // channels 0 4 1 5 2 6 3 7
+        w.x = pack_f16(a.x * up, c.x * up);
+        w.y = pack_f16(a.y * up, c.y * up);
+        w.z = pack_f16(b.x * up, d.x * up);
+        w.w = pack_f16(b.y * up, d.y * up);
+        const int at = r0 + u * kRowsAt + lane / kLanes;
+        *piece_at(at, piece) = w;
+        if (piece == 0) sh.q_exp[warp * 32 + at] = e;
+      }
+    }
+    fence_async();
+    mbar_arrive(&sh.q_full[half]);
+    int first = 0, last = 0x7fffffff;  // keys that the thread's row sees
+    if (row < rows_all) {
+      const int pos = rq.kv - rq.n + static_cast<int>(p.by_group.div(row));
+      last = p.causal ? min(rq.kv, pos + 1) : rq.kv;
+      if (p.window) first = pos - p.window + 1;
+    }
+    __syncwarp();
+    const float factor = fabsf(p.scale_log2) * pow2(sh.q_exp[tid] - 14);
+
     float m = kNegInf, l = 0.f;
     int ev = -100;
-    bool ok = true;
     for (int j = 0; j < tiles && ok; ++j) {
-      ok = mbar_wait(&sh.e_full[j & 3], (j >> 2) & 1, &sh.dead) && mbar_wait(&sh.s_full[half], j & 1, &sh.dead);
+      const int jj = base + j;
+      ok = mbar_wait(&sh.e_full[jj & 3], (jj >> 2) & 1, &sh.dead) && mbar_wait(&sh.s_full[half], (jj + k) & 1, &sh.dead);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after();
-      const int4 ek4 = sh.ek[j & 3], ev4 = sh.ev[j & 3];
+      const int4 ek4 = sh.ek[jj & 3], ev4 = sh.ev[jj & 3];
       const int ek[4] = {ek4.x, ek4.y, ek4.z, ek4.w}, evs[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
       const int ev_new = max(ev, max(max(evs[0], evs[1]), max(evs[2], evs[3])));
       float f[4];  // the scores' factor, of each run of 32 keys
@@ -451,39 +508,45 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       fence_before();
       mbar_arrive(&sh.p_full[half]);
     }
-    // ---- the result
-    ok = ok && mbar_wait(&sh.s_full[half], tiles & 1, &sh.dead);
-    if (__all_sync(0xffffffffu, ok)) {
-      fence_after();
-      const float by = l > 0.f ? pow2(ev - 12) / l : 0.f;
-      uint16_t* dst = static_cast<uint16_t*>(p.out) + token * p.o_token + q_head * p.o_head;
+    base += tiles;
+    // ---- the result, through the queries' place in shared memory, which no product reads any more
+    ok = ok && mbar_wait(&sh.s_full[half], (base + k) & 1, &sh.dead);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    fence_after();
+    const float by = l > 0.f ? pow2(ev - 12) / l : 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t x[32];
-        tmem_load32(x, o_at + c * 32);
-        tmem_wait_load(x);
-        if (row < rows_all) {
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t x[32];
+      tmem_load32(x, o_at + c * 32);
+      tmem_wait_load(x);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float v[8];  // channels 0 4 1 5 2 6 3 7 back in order
+      for (int u = 0; u < 4; ++u) {
+        float v[8];  // channels 0 4 1 5 2 6 3 7 back in order
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[i] = __uint_as_float(x[k * 8 + 2 * i]) * by;
-              v[i + 4] = __uint_as_float(x[k * 8 + 2 * i + 1]) * by;
-            }
-            uint4 w;
-            w.x = p.bf16 ? pack_bf16(v[0], v[1]) : pack_f16(v[0], v[1]);
-            w.y = p.bf16 ? pack_bf16(v[2], v[3]) : pack_f16(v[2], v[3]);
-            w.z = p.bf16 ? pack_bf16(v[4], v[5]) : pack_f16(v[4], v[5]);
-            w.w = p.bf16 ? pack_bf16(v[6], v[7]) : pack_f16(v[6], v[7]);
-            *reinterpret_cast<uint4*>(dst + c * 32 + k * 8) = w;
-          }
+        for (int i = 0; i < 4; ++i) {
+          v[i] = __uint_as_float(x[u * 8 + 2 * i]) * by;
+          v[i + 4] = __uint_as_float(x[u * 8 + 2 * i + 1]) * by;
         }
+        uint4 w;
+        w.x = p.bf16 ? pack_bf16(v[0], v[1]) : pack_f16(v[0], v[1]);
+        w.y = p.bf16 ? pack_bf16(v[2], v[3]) : pack_f16(v[2], v[3]);
+        w.z = p.bf16 ? pack_bf16(v[4], v[5]) : pack_f16(v[4], v[5]);
+        w.w = p.bf16 ? pack_bf16(v[6], v[7]) : pack_f16(v[6], v[7]);
+        *piece_at(lane, c * 4 + u) = w;
       }
-      if (p.lse && row < rows_all)
-        p.lse[static_cast<int64_t>(token) * (static_cast<int64_t>(p.H) * p.G) + q_head] =
-            l > 0.f ? (m - 7.f + log2f(l)) * 0.6931471805599453f : kNegInf;
-      fence_before();
+    }
+    fence_before();
+    if (p.lse && row < rows_all)
+      p.lse[row_offset(row, static_cast<int64_t>(p.H) * p.G, 1)] = l > 0.f ? (m - 7.f + log2f(l)) * 0.6931471805599453f : kNegInf;
+    __syncwarp();
+#pragma unroll 4
+    for (int r0 = 0; r0 < 32; r0 += kRowsAt) {
+      const uint4 w = *piece_at(r0 + lane / kLanes, piece);
+      if (row_first + r0 < rows_all)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row_offset(row_first + r0, p.o_token, p.o_head) + piece * 8) = w;
+    }
+    __syncwarp();
     }
   } else if (warp < kSoftmaxWarps + kConvertWarps) {
     // ================================================== codes to fp16 tiles
@@ -493,6 +556,9 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     const int t = tid - kSoftmaxWarps * 32, w = warp - kSoftmaxWarps;
     const int part = t % kParts;
     auto place = [&](int it) { return w * 32 + it * (32 / kParts) + lane / kParts; };  // a key's, in the tile
+    for (int k = 0; k == 0 || find_work(p, cursor, work_number(k), lane, work); ++k) {
+    const Range vis = work.vis;
+    const int r = work.r, head = work.head, tiles = work.tiles;
     const int swap = (part >> 1) & 1;  // block 1 writes its words in the order 2 3 0 1: other banks than block 0's
 
     // Loads are issued far ahead of their use and without branches: a key that no row sees, or one in a slot
@@ -611,8 +677,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     next_slots(1);
     load_scales();
     load_slots(2);
-    bool ok = true;
     for (int j = 0; j < tiles; ++j) {
+      const int jj = base + j;
       // the exponents of the run's largest scales
       int e[2];
 #pragma unroll
@@ -624,20 +690,20 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
         e[kv] = min(max(static_cast<int>(top >> 23) - 127, -100), 110);
       }
       if (lane == 0) {
-        reinterpret_cast<int*>(&sh.ek[j & 3])[w] = e[0];
-        reinterpret_cast<int*>(&sh.ev[j & 3])[w] = e[1];
-        mbar_arrive(&sh.e_full[j & 3]);
+        reinterpret_cast<int*>(&sh.ek[jj & 3])[w] = e[0];
+        reinterpret_cast<int*>(&sh.ev[jj & 3])[w] = e[1];
+        mbar_arrive(&sh.e_full[jj & 3]);
       }
       ok = __all_sync(0xffffffffu, ok);  // the warp goes on, or not
       if (!ok) break;
 
-      const int st = j & 1;
-      if (j >= 2) ok = ok && mbar_wait(&sh.k_empty[st], ((j >> 1) - 1) & 1, &sh.dead);
+      const int st = jj & 1;
+      if (jj >= 2) ok = ok && mbar_wait(&sh.k_empty[st], ((jj >> 1) - 1) & 1, &sh.dead);
       convert(dyn + Smem::kK + st * Smem::kTileBytes, std::integral_constant<int, 0>(), e[0]);
       fence_async();
       mbar_arrive(&sh.k_full[st]);
       load_codes(0);  // of j + 1
-      if (j >= 2) ok = ok && mbar_wait(&sh.v_empty[st], ((j >> 1) - 1) & 1, &sh.dead);
+      if (jj >= 2) ok = ok && mbar_wait(&sh.v_empty[st], ((jj >> 1) - 1) & 1, &sh.dead);
       convert(dyn + Smem::kV + st * Smem::kTileBytes, std::integral_constant<int, 1>(), e[1]);
       fence_async();
       mbar_arrive(&sh.v_full[st]);
@@ -647,13 +713,16 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       load_scales();
       load_slots(j + 3);
     }
+    if (!ok) break;
+    base += tiles;
+    }
   } else {
     // ================================================== products
     const uint32_t leader = elect_leader();
-    const uint32_t at = __shfl_sync(0xffffffffu, tmem, 0), base = __shfl_sync(0xffffffffu, smem_addr(dyn), 0);
+    const uint32_t at = __shfl_sync(0xffffffffu, tmem, 0), tiles_at = __shfl_sync(0xffffffffu, smem_addr(dyn), 0);
     auto scores = [&](int i, int j) {  // S_i = Q_i K(j)^T
-      const uint64_t q = smem_desc(base + Smem::kQ + i * Smem::kTileBytes, 16);
-      const uint64_t k = smem_desc(base + Smem::kK + (j & 1) * Smem::kTileBytes, 16);
+      const uint64_t q = smem_desc(tiles_at + Smem::kQ + i * Smem::kTileBytes, 16);
+      const uint64_t k = smem_desc(tiles_at + Smem::kK + (j & 1) * Smem::kTileBytes, 16);
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
         const uint64_t step = ((s / 4) * kBlockBytes + (s % 4) * 32) >> 4;
@@ -661,35 +730,40 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       }
       commit(&sh.s_full[i], leader);
     };
-    auto values = [&](int i, int j) {  // O_i += P_i(j) V(j)
-      const uint64_t v = smem_desc(base + Smem::kV + (j & 1) * Smem::kTileBytes, kBlockBytes);
+    auto values = [&](int i, int j, bool add) {  // O_i (+)= P_i(j) V(j)
+      const uint64_t v = smem_desc(tiles_at + Smem::kV + (j & 1) * Smem::kTileBytes, kBlockBytes);
 #pragma unroll
       for (int s = 0; s < kKeys / 16; ++s)
-        mma_tmem(at + 256 + i * D, at + i * 128 + s * 8, v + s * (2048 >> 4), instr_desc(D, true), j > 0 || s > 0, leader);
+        mma_tmem(at + 256 + i * D, at + i * 128 + s * 8, v + s * (2048 >> 4), instr_desc(D, true), add || s > 0, leader);
     };
-    bool ok = true;
-    for (int j = 0; j <= tiles && ok; ++j) {
+    for (int k = 0; ok && (k == 0 || find_work(p, cursor, work_number(k), lane, work)); ++k) {
+      const int tiles = work.tiles;
+      for (int j = 0; j <= tiles && ok; ++j) {
+        const int jj = base + j;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (j > 0) {
-          ok = ok && mbar_wait(&sh.v_full[(j - 1) & 1], ((j - 1) >> 1) & 1, &sh.dead) &&
-               mbar_wait(&sh.p_full[i], (j - 1) & 1, &sh.dead);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          fence_after();
-          values(i, j - 1);
-          if (i == 1) commit(&sh.v_empty[(j - 1) & 1], leader);
-        }
-        if (j < tiles) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh.k_full[j & 1], (j >> 1) & 1, &sh.dead));
-          if (!ok) break;
-          fence_after();
-          scores(i, j);
-          if (i == 1) commit(&sh.k_empty[j & 1], leader);
-        } else {
-          commit(&sh.s_full[i], leader);  // O_i is complete
+        for (int i = 0; i < 2; ++i) {
+          if (j > 0) {
+            ok = ok && mbar_wait(&sh.v_full[(jj - 1) & 1], ((jj - 1) >> 1) & 1, &sh.dead) &&
+                 mbar_wait(&sh.p_full[i], (jj - 1) & 1, &sh.dead);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            fence_after();
+            values(i, jj - 1, j > 1);
+            if (i == 1) commit(&sh.v_empty[(jj - 1) & 1], leader);
+          }
+          if (j < tiles) {
+            ok = (j > 0 || mbar_wait(&sh.q_full[i], k & 1, &sh.dead)) && mbar_wait(&sh.k_full[jj & 1], (jj >> 1) & 1, &sh.dead);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            fence_after();
+            scores(i, jj);
+            if (i == 1) commit(&sh.k_empty[jj & 1], leader);
+          } else {
+            commit(&sh.s_full[i], leader);  // O_i is complete
+          }
         }
       }
+      base += tiles;
     }
     __syncwarp();
   }
@@ -715,11 +789,9 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
   const cudaError_t e = kernel.resident(reinterpret_cast<const void*>(k_attend_tiles<D, GROUP, kScaleF16>), kThreadsTiles,
                                         TileSmem<D>::kAsk, &resident);
   if (e != cudaSuccess) return e;
-  const int64_t per_head = (static_cast<int64_t>(p.max_new) * p.G + kRowsTile - 1) / kRowsTile;
-  const int64_t grid = per_head * p.n_req * p.H;
-  if (grid >= (int64_t{1} << 31)) return cudaErrorInvalidConfiguration;
-  k_attend_tiles<D, GROUP, kScaleF16><<<static_cast<unsigned>(grid), kThreadsTiles, TileSmem<D>::kAsk, s>>>(
-      p, static_cast<int>(per_head));
+  const double works = static_cast<double>((static_cast<int64_t>(p.max_new) * p.G + kRowsTile - 1) / kRowsTile) * p.n_req * p.H;
+  const int grid = works < resident ? static_cast<int>(works) : resident;
+  k_attend_tiles<D, GROUP, kScaleF16><<<grid, kThreadsTiles, TileSmem<D>::kAsk, s>>>(p);
   return cudaGetLastError();
 }
 
