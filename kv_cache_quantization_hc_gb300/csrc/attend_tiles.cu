@@ -25,8 +25,9 @@
 //   its exponents are too: no barrier among those warps.
 // * Queries in fp16: each row times a power of two that brings its largest
 //   value near 2^14 (f holds the inverse).
-// * m moves only when the maximum exceeds it by 8, so that O (in tensor
-//   memory) is rarely rescaled; p_j stays below 2^15.
+// * m moves only when the maximum exceeds it by 8, and then to 4 above the
+//   maximum, so that O (in tensor memory) is rarely rescaled; p_j stays below
+//   2^15, and a row's largest is 2^3 or more.
 // * The channels of keys, queries and values are permuted within eights
 //   (0 4 1 5 2 6 3 7), the order in which a word of codes comes apart; the
 //   products over channels do not see it and the output is put back in order.
@@ -48,7 +49,9 @@ constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kThreadsTiles = (kSoftmaxWarps + kConvertWarps + 1) * 32;
 constexpr int kBlockBytes = kKeys * 128;  // 128 rows of 64 channels, swizzled in 128-byte rows
 constexpr int kKeyExp = -10;     // keys times 2^(kKeyExp - exponent of the run's largest scale)
-constexpr float kMoveAt = 8.f;   // the reference moves when the maximum is this far above it
+constexpr float kMoveAt = 8.f;   // the reference moves when the maximum is this far above it,
+constexpr float kAhead = 4.f;    // to this far above the maximum, or
+constexpr float kMostSum = 60000.f;  // when a tile's probabilities sum up to this: fp16 ends at 65504
 
 template <int D>
 struct TileSmem {
@@ -394,7 +397,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       fence_after();
       const int4 ek4 = sh.ek[jj & 3], ev4 = sh.ev[jj & 3];
       const int ek[4] = {ek4.x, ek4.y, ek4.z, ek4.w}, evs[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
-      const int ev_new = max(ev, max(max(evs[0], evs[1]), max(evs[2], evs[3])));
+      // one above the largest when it moves, so that it moves rarely
+      const int ev_tile = max(max(evs[0], evs[1]), max(evs[2], evs[3])), ev_new = ev_tile > ev ? ev_tile + 1 : ev;
       float f[4];  // the scores' factor, of each run of 32 keys
 #pragma unroll
       for (int c = 0; c < 4; ++c) f[c] = factor * pow2(ek[c] - kKeyExp);
@@ -403,10 +407,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       // Most tiles: all of it seen, and no score more than 8 above the reference.  One pass then, with P kept
       // in registers until the maximum is known, since it goes over the scores.
       float sum = 0.f;
-      bool done = false;
+      bool done = false, crowded = false;  // crowded: the sum was too large
       if (!masked && j > 0 && ev_new == ev) {
         uint32_t x[2][16], h[2][32];
-        float top = kNegInf;
+        float all = 0.f;
         tmem_load16(x[0], s_at);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -414,7 +418,6 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
           const float off = m == kNegInf ? 0.f : 7.f - m + static_cast<float>(d);
           const float2 f2 = make_float2(f[c], f[c]), off2 = make_float2(off, off);
           float2 part = make_float2(0.f, 0.f);
-          float most = kNegInf;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             uint32_t(&y)[16] = x[u];
@@ -422,19 +425,18 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
             if (c < 3 || u < 1) tmem_load16(x[u ^ 1], s_at + c * 32 + (u + 1) * 16);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              float2 v = make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1]));
-              most = fmaxf(most, fmaxf(v.x, v.y));
-              v = __ffma2_rn(v, f2, off2);
+              float2 v = __ffma2_rn(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), f2, off2);
               v.x = ex2(v.x);
               v.y = ex2(v.y);
               part = __fadd2_rn(part, v);
               h[c / 2][(c % 2) * 16 + u * 8 + k / 2] = pack_f16(v.x, v.y);
             }
           }
-          top = fmaxf(top, most * f[c]);
+          all += part.x + part.y;
           sum = fmaf(part.x + part.y, pow2(-d), sum);
         }
-        done = __all_sync(0xffffffffu, top <= m + kMoveAt);
+        done = __all_sync(0xffffffffu, all < kMostSum);
+        crowded = !done;
         if (done) {
           tmem_store32(s_at, h[0]);
           tmem_store32(s_at + 32, h[1]);
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
         }
         if (masked) wait_store();
         // the reference of the row, and O with it
-        const float m_new = top > m + kMoveAt || m == kNegInf ? fmaxf(m, top) : m;
+        const float m_new = top > m + (crowded ? 0.f : kMoveAt) || (m == kNegInf && top > m) ? top + kAhead : m;
         if (__any_sync(0xffffffffu, m_new != m || ev_new != ev)) {
           const float by = m == kNegInf ? 0.f : ex2(m - m_new);
           l *= by;
