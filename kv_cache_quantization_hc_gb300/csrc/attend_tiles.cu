@@ -17,8 +17,8 @@
 //
 // Mathematics, per row, with a reference m near the running maximum:
 //   x_j = f * 2^(ek + 10) * (q . k_j),  p_j = 2^(x_j - m + 7),  l = sum p_j,
-//   O = sum (p_j * 2^(ev_j - ev)) v_j,  out = O / l * 2^(ev - 12)
-// * k_j = code * scale * 2^(-10 - ek) and v_j = code * scale * 2^(12 - ev_j) in
+//   O = sum (p_j * 2^(ev_j - ev)) v_j,  out = O / l * 2^(ev + 10)
+// * k_j = code * scale * 2^(-10 - ek) and v_j = code * scale * 2^(-10 - ev_j) in
 //   fp16, 2^ek and 2^ev_j the largest scales of the run of 32 keys that j is
 //   in, 2^ev the largest so far.  Powers of two, so that scales of any size
 //   fit, and each element is rounded once.  A run is one warp's to convert, so
@@ -26,8 +26,8 @@
 // * Queries in fp16: each row times a power of two that brings its largest
 //   value near 2^14 (f holds the inverse).
 // * m moves only when the maximum exceeds it by 8, and then to 4 above the
-//   maximum, so that O (in tensor memory) is rarely rescaled; p_j stays below
-//   2^15, and a row's largest is 2^3 or more.
+//   maximum, so that O (in tensor memory) is rarely rescaled.  Between, a tile
+//   whose probabilities sum up to 60000 (fp16 ends at 65504) moves it too.
 // * The channels of keys, queries and values are permuted within eights
 //   (0 4 1 5 2 6 3 7), the order in which a word of codes comes apart; the
 //   products over channels do not see it and the output is put back in order.
@@ -48,7 +48,7 @@ constexpr int kRowsTile = 2 * kHalf;
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kThreadsTiles = (kSoftmaxWarps + kConvertWarps + 1) * 32;
 constexpr int kBlockBytes = kKeys * 128;  // 128 rows of 64 channels, swizzled in 128-byte rows
-constexpr int kKeyExp = -10;     // keys times 2^(kKeyExp - exponent of the run's largest scale)
+constexpr int kExp = -10;        // elements times 2^(kExp - exponent of the run's largest scale)
 constexpr float kMoveAt = 8.f;   // the reference moves when the maximum is this far above it,
 constexpr float kAhead = 4.f;    // to this far above the maximum, or
 constexpr float kMostSum = 60000.f;  // when a tile's probabilities sum up to this: fp16 ends at 65504
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       const int ev_tile = max(max(evs[0], evs[1]), max(evs[2], evs[3])), ev_new = ev_tile > ev ? ev_tile + 1 : ev;
       float f[4];  // the scores' factor, of each run of 32 keys
 #pragma unroll
-      for (int c = 0; c < 4; ++c) f[c] = factor * pow2(ek[c] - kKeyExp);
+      for (int c = 0; c < 4; ++c) f[c] = factor * pow2(ek[c] - kExp);
       const int key0 = (vis.tile0 + j) * kKeys;
       const bool masked = __any_sync(0xffffffffu, key0 < first || key0 + kKeys > last);
       // Most tiles: all of it seen, and no score more than 8 above the reference.  One pass then, with P kept
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     fence_after();
-    const float by = l > 0.f ? pow2(ev - 12) / l : 0.f;
+    const float by = l > 0.f ? pow2(ev - kExp) / l : 0.f;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t x[32];
@@ -630,14 +630,13 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     auto scale_value = [&](uint32_t bits) {
       return kScaleF16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(bits))) : __uint_as_float(bits);
     };
-    // Values: code times scale, the code as fp16 by way of 1024 + u.
-    // Keys: u * 2^-24 is the fp16 subnormal that the nibble u = code + 8 already is (u * 2^-20 four bits up), so
-    // one fused multiply-add by scale * 2^24 takes off 8 scales and rounds once; the run's scales come to
-    // 2^-9 at most for that, and what is below 2^-25 then is lost: 2^-18 of the run's largest key.  An fp32
-    // scale's rest would need two more steps there, so those keys go the values' way.
+    // The nibble u = code + 8 in the low bits of an fp16 is the subnormal u * 2^-24 (u * 2^-20 four bits up), so one
+    // fused multiply-add by scale * 2^24 takes off 8 scales and rounds once.  For that the run's scales come to 2^-9
+    // at most, and what is below 2^-25 then is lost: 2^-18 of the run's largest element.  An fp32 scale has a rest
+    // to an fp16; its products take the codes as whole numbers, 1024 + u less 1032.
     auto convert = [&](unsigned char* tile, auto which, int e) {
       constexpr int kv = decltype(which)::value;
-      const float up = pow2((kv ? 12 : kKeyExp) - e);
+      const float up = pow2(kExp - e);
 #pragma unroll
       for (int it = 0; it < kIters; ++it) {
         const int key = place(it);
@@ -652,7 +651,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
         for (int i = 0; i < 4; ++i) {
           const uint32_t lo = words[i], hi = lo >> 8;
           uint4 v;
-          if (kv || !kScaleF16) {
+          if (!kScaleF16) {
             v.x = s.times(codes_04(lo));
             v.y = s.times(codes_15(lo));
             v.z = s.times(codes_04(hi));

@@ -140,6 +140,8 @@ def _avail(x):
 
 def _need(x, nbytes, name):
     """Refuse a tensor smaller than the bytes the call will address."""
+    if x is None or isinstance(x, int) or (x.is_contiguous() and x.nbytes >= nbytes):
+        return                  # a contiguous tensor's own bytes lie in its storage: no need to ask for that
     a = _avail(x)
     if a is not None and a < nbytes:
         raise ValueError(f"{name} holds {a} bytes; the call addresses {nbytes}")
