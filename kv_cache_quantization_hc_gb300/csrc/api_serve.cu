@@ -64,6 +64,9 @@ int check_rope(const hc_rope_axes_desc* r, int d_head, int64_t n_tokens, hc::Rop
   out->half = r->rot_dim / 2;
   out->inverse = r->inverse;
   std::memcpy(out->pair_axis, r->pair_axis, sizeof out->pair_axis);
+  out->axes = 0;
+  for (int i = 0; i < out->half; ++i) out->axes |= 1u << r->pair_axis[i];
+  out->pairs16 = aligned(r->table, 16) && out->half % 2 == 0;
   return HC_OK;
 }
 

@@ -2,56 +2,120 @@
 // quantized, values quantized, in one launch.  Memory-bound: q, k, v read
 // once, q_out and the 4-bit rows written once.
 //
-// A warp takes either some query heads of a token (as k_rope_axes) or two
-// cache heads of it: their rotated keys go to shared memory in fp32, because
-// the rotation's lanes hold channels i and i + half while a quantization
-// group is a run of 32 to 128 channels; each lane then quantizes 8 adjacent
-// channels, the group's maximum found by shuffles.
+// A warp takes either some query heads of a token (as k_rope_axes) or some of
+// its cache heads.  Where all channels rotate (or none), a lane has whole
+// pieces of 16 bytes of a row before and after the rotation (channels i.. and
+// i + half..): it quantizes them where they are, the group's maximum found by
+// shuffles.  A partial rotation shifts pieces against groups; such keys go
+// through shared memory in fp32 first.
+//
+// A code is fp32(x / s) rounded: the quotient as x * r corrected by its exact
+// residual, r = fp32(1 / s) correctly rounded (Markstein, IBM J. Res. Dev.
+// 34(1), 1990), which gives the IEEE quotient where nothing under- or overflows;
+// scales outside 2^-100..2^100 are divided by.
 #include <algorithm>
+#include <type_traits>
 
 #include "rope.cuh"
 
 namespace hc {
 namespace {
 
-// Cache heads per warp: as many rows as its lanes hold at 8 channels each.
+// Cache heads per warp: a row of values takes 8 to 32 lanes, a row of keys as
+// many or half of that.
 template <int D>
-constexpr int kKvHeads = 256 / D;
+constexpr int kKvHeads = 512 / D;
 
-// One row of 8 channels per lane (D / 8 lanes): scale and codes.
-template <int D, bool kScaleF16>
-__device__ __forceinline__ void quantize_row(const float (&x)[8], int lane, int group_log2, uint8_t* codes,
-                                             void* scales) {
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-  for (int o = 1; o < (1 << (group_log2 - 3)); o <<= 1)
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  float s = __fmul_rn(amax, 0x1.24924ap-3f);  // fp32(1/7)
-  if (kScaleF16) s = __half2float(__float2half_rn(s));
+// The codes of N values, a nibble each from the lowest on.
+template <int N>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[N], float s) {
   uint32_t packed = 0;
+  float q[N];
+  if (s >= 0x1p-100f && s <= 0x1p100f) {
+    const float r = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = s != 0.f ? __fdiv_rn(x[i], s) : 0.f;
-    const int n = static_cast<int>(fminf(fmaxf(rintf(q), -7.f), 7.f));
-    packed |= (static_cast<uint32_t>(n) & 0xfu) << (4 * i);
+    for (int i = 0; i < N; ++i) {
+      q[i] = x[i] * r;
+      q[i] = fmaf(fmaf(-q[i], s, x[i]), r, q[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = s != 0.f ? __fdiv_rn(x[i], s) : 0.f;
   }
-  const int piece = lane & (D / 8 - 1);
-  reinterpret_cast<uint32_t*>(codes)[piece] = packed;
-  if ((piece & ((1 << (group_log2 - 3)) - 1)) == 0) {
-    const int g = piece >> (group_log2 - 3);
-    if (kScaleF16)
-      static_cast<__half*>(scales)[g] = __float2half_rn(s);
-    else
-      static_cast<float*>(scales)[g] = s;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    // 1.5 * 2^23 more: rounded to even, the two's complement in the low bits
+    const uint32_t n = __float_as_uint(fminf(fmaxf(q[i], -7.f), 7.f) + 12582912.f);
+    packed |= (n & 0xfu) << (4 * i);
   }
+  return packed;
 }
 
-template <typename T, int D, int kPairing, bool kScaleF16>
+template <bool kScaleF16>
+__device__ __forceinline__ float scale_of(float amax) {
+  const float s = __fmul_rn(amax, 0x1.24924ap-3f);  // fp32(1/7)
+  return kScaleF16 ? __half2float(__float2half_rn(s)) : s;
+}
+template <bool kScaleF16>
+__device__ __forceinline__ void store_scale(void* scales, int64_t i, float s) {
+  if (kScaleF16)
+    static_cast<__half*>(scales)[i] = __float2half_rn(s);
+  else
+    static_cast<float*>(scales)[i] = s;
+}
+template <int N>
+__device__ __forceinline__ float amax_of(const float (&x)[N]) {
+  float m = fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, fabsf(x[i]));
+  return m;
+}
+// The largest over runs of `lanes` lanes (a power of two).
+__device__ __forceinline__ float amax_over(float m, int lanes) {
+  for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* codes, int channel, uint32_t packed) {
+  if (N == 8)
+    *reinterpret_cast<uint32_t*>(codes + channel / 2) = packed;
+  else
+    *reinterpret_cast<uint16_t*>(codes + channel / 2) = static_cast<uint16_t>(packed);
+}
+
+// A row's codes and scales in the cache.
+struct CacheRow {
+  uint8_t* codes;
+  int64_t scale;  // index of its first scale
+};
+template <int D>
+__device__ __forceinline__ CacheRow cache_row(const AppendParams& p, int64_t row, int kv, int h) {
+  const int64_t at = ((((row >> p.B_log2) * 2 + kv) * p.H + h) << p.B_log2) + (row & ((1 << p.B_log2) - 1));
+  return {p.codes + at * (D / 2), at * (D >> p.group_log2)};
+}
+
+// One piece of V channels per lane, D / V lanes to a row; `live`: the lane's row is there.
+template <int D, bool kScaleF16, int V>
+__device__ __forceinline__ void quantize_pieces(const AppendParams& p, const float (&x)[V], int channel, CacheRow to,
+                                                bool live) {
+  const float s = scale_of<kScaleF16>(amax_over(amax_of(x), (1 << p.group_log2) / V));
+  const uint32_t packed = codes_of(x, s);
+  if (!live) return;
+  store_codes<V>(to.codes, channel, packed);
+  if ((channel & ((1 << p.group_log2) - 1)) == 0) store_scale<kScaleF16>(p.scales, to.scale + (channel >> p.group_log2), s);
+}
+
+template <typename T, int D>
+struct AppendShared {
+  float2 cs[kRopeWarps][D / 2];
+  alignas(16) float rows[kRopeWarps][512];
+};
+struct NoShared {};
+
+template <typename T, int D, int kPairing, bool kScaleF16, bool kInLanes>
 __global__ void __launch_bounds__(kRopeWarps * 32) k_append_int4(const __grid_constant__ AppendParams p) {
   constexpr int V = 16 / sizeof(T);
-  __shared__ float2 cs[kRopeWarps][D / 2];
-  __shared__ __align__(16) float rows[kRopeWarps][256];
+  __shared__ std::conditional_t<kInLanes, NoShared, AppendShared<T, D>> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
   const int parts = p.q_parts + p.kv_parts;
@@ -59,83 +123,162 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_append_int4(const __grid_co
   if (t >= p.n_tokens) return;
   const int part = static_cast<int>(w - t * parts);
   const int64_t row = __ldg(p.token_rows + t);
-  int bad = row < -1 || row >= p.n_rows ? HC_DEVERR_SLOT : 0;
-  if (p.rope.table != nullptr && !stage_cos_sin(p.rope, static_cast<int>(t), lane, cs[warp]))
-    bad |= HC_DEVERR_POS;
-  if (bad) {
-    if (lane == 0) flag_error(p.err, bad);
+  if (row < -1 || row >= p.n_rows) {
+    if (lane == 0) flag_error(p.err, HC_DEVERR_SLOT);
     return;
   }
   if (part < p.q_parts) {
-    const int h0 = part * p.q_heads_per_warp;
-    rotate_rows<T, kPairing, V, 4>(static_cast<const T*>(p.q) + t * p.q_token, p.q_head,
-                                   static_cast<T*>(p.q_out) + t * p.o_token, p.o_head, h0,
-                                   min(h0 + p.q_heads_per_warp, p.n_q_heads), p.rope.half, cs[warp],
-                                   p.items_per_row, lane);
+    const int h0 = part * p.q_heads_per_warp, h1 = min(h0 + p.q_heads_per_warp, p.n_q_heads);
+    const T* q = static_cast<const T*>(p.q) + t * p.q_token;
+    T* q_out = static_cast<T*>(p.q_out) + t * p.o_token;
+    bool ok;
+    if constexpr (kInLanes) {
+      ok = rotate_rows_in_lanes<T, kPairing, V, 4>(p.rope, static_cast<int>(t), q, p.q_head, q_out, p.o_head, h0, h1,
+                                                   static_cast<int>(p.items_per_row.d), lane);
+    } else {
+      ok = stage_cos_sin(p.rope, static_cast<int>(t), lane, sh.cs[warp]);
+      if (ok)
+        rotate_rows<T, kPairing, V, 4>(q, p.q_head, q_out, p.o_head, h0, h1, p.rope.half, sh.cs[warp], p.items_per_row, lane);
+    }
+    if (!ok && lane == 0) flag_error(p.err, HC_DEVERR_POS);
     return;
   }
   if (row < 0) return;
   const int h0 = (part - p.q_parts) * kKvHeads<D>, nh = min(kKvHeads<D>, p.H - h0);
-  const int64_t slot = row >> p.B_log2;
-  const int64_t in_block = row & ((1 << p.B_log2) - 1);
-  constexpr int kLanes = D / 8;
-  const int groups = D >> p.group_log2;
-
-  // keys: rotated in fp32 into shared memory, converted on the way
   const T* k = static_cast<const T*>(p.k) + t * p.k_token + h0 * p.k_head;
-  const int total = nh * static_cast<int>(p.items_per_row.d);
-  const int half = p.rope.half;
-  const int turned = kPairing == HC_PAIR_HALF_SPLIT ? half / V : 2 * half / V;
-  for (int idx = lane; idx < total; idx += 32) {
-    uint32_t h, it;
-    p.items_per_row.divmod(static_cast<uint32_t>(idx), h, it);
-    const int item = static_cast<int>(it);
-    const int c = item < turned || kPairing != HC_PAIR_HALF_SPLIT ? item * V : 2 * half + (item - turned) * V;
-    const T* src = k + h * p.k_head + c;
-    float* dst = rows[warp] + h * D + c;
-    const Piece<T, V> a = load_piece<T, V>(src);
-    float f[V];
+  const T* v = static_cast<const T*>(p.v) + t * p.v_token + h0 * p.v_head;
+  constexpr int kLanes = D / V, kAt = 32 / kLanes;  // lanes of a row of values, rows at a time
+  const int piece = lane % kLanes;
+  // values: on their way before the keys are worked on
+  Piece<T, V> vp[kKvHeads<D> / kAt];
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = to_f32(a.e[i]);
-    if (item < turned) {
-      if constexpr (kPairing == HC_PAIR_HALF_SPLIT) {
-        const Piece<T, V> b = load_piece<T, V>(src + half);
+  for (int u = 0; u < kKvHeads<D> / kAt; ++u)
+    if (u * kAt + lane / kLanes < nh) vp[u] = load_piece<T, V>(v + (u * kAt + lane / kLanes) * p.v_head + piece * V);
+
+  if constexpr (kInLanes) {
+    using Item = LaneItem<T, kPairing, V>;
+    const Item item(lane, static_cast<int>(p.items_per_row.d), p.rope.half);
+    constexpr int kItemLanes = kPairing == HC_PAIR_HALF_SPLIT ? D / 2 / V : D / V, kRowsAt = 32 / kItemLanes;
+    constexpr bool kSplit = kPairing == HC_PAIR_HALF_SPLIT;
+    if (p.rope.table != nullptr) {
+      Piece<T, V> a[(kKvHeads<D> + kRowsAt - 1) / kRowsAt], b[(kKvHeads<D> + kRowsAt - 1) / kRowsAt];
+#pragma unroll
+      for (int u = 0; u < (kKvHeads<D> + kRowsAt - 1) / kRowsAt; ++u)
+        if (u * kRowsAt + item.sub < nh) item.load(k + (u * kRowsAt + item.sub) * p.k_head, a[u], b[u]);
+      float2 cs[Item::kPairs];
+      if (!load_turns<Item::kPairs>(p.rope, static_cast<int>(t), item.first_pair(), true, lane, cs)) {
+        if (lane == 0) flag_error(p.err, HC_DEVERR_POS);
+        return;
+      }
+#pragma unroll
+      for (int u = 0; u < (kKvHeads<D> + kRowsAt - 1) / kRowsAt; ++u) {
+        const int r = u * kRowsAt + item.sub;
+        const bool live = r < nh;
+        const CacheRow to = cache_row<D>(p, row, 0, h0 + (live ? r : 0));
+        float x[V], x2[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          float x2 = to_f32(b.e[i]);
-          turn(f[i], x2, cs[warp][item * V + i]);
-          dst[half + i] = x2;
+          x[i] = live ? to_f32(a[u].e[i]) : 0.f;
+          if (kSplit) x2[i] = live ? to_f32(b[u].e[i]) : 0.f;
         }
-      } else {
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) turn(f[2 * i], f[2 * i + 1], cs[warp][item * (V / 2) + i]);
+        for (int i = 0; i < Item::kPairs; ++i) {
+          if (kSplit)
+            turn(x[i], x2[i], cs[i]);
+          else
+            turn(x[2 * i], x[2 * i + 1], cs[i]);
+        }
+        if (!kSplit) {
+          quantize_pieces<D, kScaleF16, V>(p, x, item.c, to, live);
+        } else {
+          // channels c.. and c + D/2..: in groups of their own, or the same one
+          const bool one = (1 << p.group_log2) > D / 2;
+          const int lanes = one ? kItemLanes : (1 << p.group_log2) / V;
+          float m1 = amax_of(x), m2 = amax_of(x2);
+          if (one) m1 = fmaxf(m1, m2);
+          m1 = amax_over(m1, lanes);
+          m2 = one ? m1 : amax_over(m2, lanes);
+          const float s1 = scale_of<kScaleF16>(m1), s2 = one ? s1 : scale_of<kScaleF16>(m2);
+          const uint32_t c1 = codes_of(x, s1), c2 = codes_of(x2, s2);
+          if (live) {
+            store_codes<V>(to.codes, item.c, c1);
+            store_codes<V>(to.codes, item.c + D / 2, c2);
+            if ((item.it & (lanes - 1)) == 0) {
+              store_scale<kScaleF16>(p.scales, to.scale + (item.c >> p.group_log2), s1);
+              if (!one) store_scale<kScaleF16>(p.scales, to.scale + ((item.c + D / 2) >> p.group_log2), s2);
+            }
+          }
+        }
       }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) dst[i] = f[i];
-  }
-  __syncwarp();
-
-  // every lane 8 channels of a row; lanes past the last row repeat it
-  const int h = min(lane / kLanes, nh - 1), c = (lane & (kLanes - 1)) * 8;
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    float x[8];
-    if (kv == 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = rows[warp][h * D + c + i];
     } else {
-      const T* src = static_cast<const T*>(p.v) + t * p.v_token + (h0 + h) * p.v_head + c;
 #pragma unroll
-      for (int j = 0; j < 8 / V; ++j) {
-        const Piece<T, V> a = load_piece<T, V>(src + j * V);
+      for (int u = 0; u < kKvHeads<D> / kAt; ++u) {
+        const int r = u * kAt + lane / kLanes;
+        const bool live = r < nh;
+        float x[V];
+        Piece<T, V> a;
+        if (live) a = load_piece<T, V>(k + r * p.k_head + piece * V);
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[j * V + i] = to_f32(a.e[i]);
+        for (int i = 0; i < V; ++i) x[i] = live ? to_f32(a.e[i]) : 0.f;
+        quantize_pieces<D, kScaleF16, V>(p, x, piece * V, cache_row<D>(p, row, 0, h0 + (live ? r : 0)), live);
       }
     }
-    const int64_t at = (((slot * 2 + kv) * p.H + h0 + h) << p.B_log2) + in_block;
-    quantize_row<D, kScaleF16>(x, lane, p.group_log2, p.codes + at * (D / 2),
-                               static_cast<uint8_t*>(p.scales) + at * groups * (kScaleF16 ? 2 : 4));
+  } else {
+    // rotated in fp32 into shared memory, converted on the way
+    if (!stage_cos_sin(p.rope, static_cast<int>(t), lane, sh.cs[warp])) {
+      if (lane == 0) flag_error(p.err, HC_DEVERR_POS);
+      return;
+    }
+    const int total = nh * static_cast<int>(p.items_per_row.d);
+    const int half = p.rope.half;
+    const int turned = kPairing == HC_PAIR_HALF_SPLIT ? half / V : 2 * half / V;
+    for (int idx = lane; idx < total; idx += 32) {
+      uint32_t h, it;
+      p.items_per_row.divmod(static_cast<uint32_t>(idx), h, it);
+      const int item = static_cast<int>(it);
+      const int c = item < turned || kPairing != HC_PAIR_HALF_SPLIT ? item * V : 2 * half + (item - turned) * V;
+      const T* src = k + h * p.k_head + c;
+      float* dst = sh.rows[warp] + h * D + c;
+      const Piece<T, V> a = load_piece<T, V>(src);
+      float f[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = to_f32(a.e[i]);
+      if (item < turned) {
+        if constexpr (kPairing == HC_PAIR_HALF_SPLIT) {
+          const Piece<T, V> b = load_piece<T, V>(src + half);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float x2 = to_f32(b.e[i]);
+            turn(f[i], x2, sh.cs[warp][item * V + i]);
+            dst[half + i] = x2;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) turn(f[2 * i], f[2 * i + 1], sh.cs[warp][item * (V / 2) + i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) dst[i] = f[i];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kKvHeads<D> / kAt; ++u) {
+      const int r = u * kAt + lane / kLanes;
+      const bool live = r < nh;
+      float x[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = live ? sh.rows[warp][r * D + piece * V + i] : 0.f;
+      quantize_pieces<D, kScaleF16, V>(p, x, piece * V, cache_row<D>(p, row, 0, h0 + (live ? r : 0)), live);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kKvHeads<D> / kAt; ++u) {
+    const int r = u * kAt + lane / kLanes;
+    const bool live = r < nh;
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = live ? to_f32(vp[u].e[i]) : 0.f;
+    quantize_pieces<D, kScaleF16, V>(p, x, piece * V, cache_row<D>(p, row, 1, h0 + (live ? r : 0)), live);
   }
 }
 
@@ -154,10 +297,15 @@ cudaError_t launch(AppendParams p, cudaStream_t s) {
   p.q_parts = (p.n_q_heads + p.q_heads_per_warp - 1) / p.q_heads_per_warp;
   const int64_t warps = static_cast<int64_t>(p.n_tokens) * (p.q_parts + p.kv_parts);
   const unsigned grid = static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps);
-  if (p.scale_f16)
-    k_append_int4<T, D, kPairing, true><<<grid, kRopeWarps * 32, 0, s>>>(p);
+  const bool in_lanes = p.rope.half == 0 || 2 * p.rope.half == D;
+  if (in_lanes && p.scale_f16)
+    k_append_int4<T, D, kPairing, true, true><<<grid, kRopeWarps * 32, 0, s>>>(p);
+  else if (in_lanes)
+    k_append_int4<T, D, kPairing, false, true><<<grid, kRopeWarps * 32, 0, s>>>(p);
+  else if (p.scale_f16)
+    k_append_int4<T, D, kPairing, true, false><<<grid, kRopeWarps * 32, 0, s>>>(p);
   else
-    k_append_int4<T, D, kPairing, false><<<grid, kRopeWarps * 32, 0, s>>>(p);
+    k_append_int4<T, D, kPairing, false, false><<<grid, kRopeWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 

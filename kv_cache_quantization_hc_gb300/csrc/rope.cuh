@@ -81,6 +81,52 @@ __device__ __forceinline__ void store_piece(T* p, const Piece<T, V>& r) {
   }
 }
 
+// (cos, sin) of pairs first..first+N-1 for token t, in registers; false if a
+// position that some pair needs is outside the table (nothing is read for it).
+// Called by whole warps with N pairs for each lane.
+template <int N>
+__device__ __forceinline__ bool load_turns(const RopeParams& p, int t, int first, bool rotates, int lane,
+                                           float2 (&cs)[N]) {
+  int pos = 0;
+  bool ok = true;
+  if (p.axes >> lane & 1u) {  // a lane per axis
+    pos = __ldg(p.positions + lane * p.position_stride + t);
+    ok = pos >= 0 && pos < p.n_positions;
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) return false;
+  uint8_t axis[N];
+  bool same = true;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    axis[i] = rotates ? p.pair_axis[first + i] : 0;
+    same = same && axis[i] == axis[0];
+  }
+  if (N % 2 == 0 && p.pairs16 && __all_sync(0xffffffffu, same)) {
+    const int at = __shfl_sync(0xffffffffu, pos, axis[0]);
+    if (rotates) {
+      const float4* src = reinterpret_cast<const float4*>(p.table + static_cast<int64_t>(at) * p.half + first);
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const float4 v = __ldg(src + i);
+        cs[2 * i] = make_float2(v.x, v.y);
+        cs[2 * i + 1] = make_float2(v.z, v.w);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = __shfl_sync(0xffffffffu, pos, axis[i]);
+      if (rotates) cs[i] = __ldg(p.table + static_cast<int64_t>(at) * p.half + first + i);
+    }
+  }
+  if (p.inverse) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) cs[i].y = -cs[i].y;
+  }
+  return true;
+}
+
 // Items of one row: its rotated pieces (half split: the piece of V pairs at
 // channels V*i.. and half+V*i..; interleaved: V channels, V/2 pairs), then
 // the pieces that are copied.
@@ -143,6 +189,74 @@ __device__ __forceinline__ void rotate_rows(const T* x, int64_t x_head, T* y, in
       }
       store_piece<T, V>(y + yo[u], a[u]);
     }
+  }
+}
+
+// Rows whose items divide a warp's lanes: a lane has the same item of every
+// row it takes, so its (cos, sin) stay in registers.
+template <typename T, int kPairing, int V>
+struct LaneItem {
+  static constexpr bool kHalfSplit = kPairing == HC_PAIR_HALF_SPLIT;
+  static constexpr int kPairs = kHalfSplit ? V : V / 2;  // of an item
+  int it, sub, at_once;  // the item, the row among those of a pass, rows of a pass
+  bool rotates;
+  int c, half;           // the item's first channel; half-split: its second piece is `half` further on
+
+  __device__ __forceinline__ LaneItem(int lane, int items, int half_) {
+    it = lane & (items - 1);
+    at_once = 32 / items;
+    sub = lane / items;
+    half = half_;
+    const int turned = kHalfSplit ? half / V : 2 * half / V;
+    rotates = it < turned;
+    c = rotates || !kHalfSplit ? it * V : 2 * half + (it - turned) * V;
+  }
+  __device__ __forceinline__ int first_pair() const { return it * kPairs; }
+  __device__ __forceinline__ void load(const T* row, Piece<T, V>& a, Piece<T, V>& b) const {
+    a = load_piece<T, V>(row + c);
+    if (kHalfSplit && rotates) b = load_piece<T, V>(row + c + half);
+  }
+  __device__ __forceinline__ void turn_and_store(T* row, Piece<T, V>& a, Piece<T, V>& b, const float2 (&cs)[kPairs]) const {
+    if (rotates) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        T& e1 = kHalfSplit ? a.e[i] : a.e[2 * i];
+        T& e2 = kHalfSplit ? b.e[i] : a.e[2 * i + 1];
+        float x1 = to_f32(e1), x2 = to_f32(e2);
+        turn(x1, x2, cs[i]);
+        e1 = from_f32<T>(x1);
+        e2 = from_f32<T>(x2);
+      }
+      if (kHalfSplit) store_piece<T, V>(row + c + half, b);
+    }
+    store_piece<T, V>(row + c, a);
+  }
+};
+
+// The rows of heads [h0, h1) of token t.  The first rows are on their way
+// before the positions and the table are read.  False: a position outside.
+template <typename T, int kPairing, int V, int kUnroll>
+__device__ __forceinline__ bool rotate_rows_in_lanes(const RopeParams& rope, int t, const T* x, int64_t x_head, T* y,
+                                                     int64_t y_head, int h0, int h1, int items, int lane) {
+  using Item = LaneItem<T, kPairing, V>;
+  const Item item(lane, items, rope.half);
+  Piece<T, V> a[kUnroll], b[kUnroll];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (h + u * item.at_once < h1) item.load(x + (h + u * item.at_once) * x_head, a[u], b[u]);
+  };
+  int h = h0 + item.sub;
+  load(h);
+  float2 cs[Item::kPairs];
+  if (rope.table != nullptr && !load_turns<Item::kPairs>(rope, t, item.first_pair(), item.rotates, lane, cs)) return false;
+  for (;;) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (h + u * item.at_once < h1) item.turn_and_store(y + (h + u * item.at_once) * y_head, a[u], b[u], cs);
+    h += kUnroll * item.at_once;
+    if (h0 + (h - h0 - item.sub) >= h1) return true;  // the same for all lanes
+    load(h);
   }
 }
 

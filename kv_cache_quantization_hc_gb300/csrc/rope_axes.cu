@@ -1,29 +1,35 @@
 // Rotary positions with several axes: y = x with the pairs of its rows turned.
 // Memory-bound (each element read and written once).  A warp takes one
-// token's rows, or a part of its heads where there are few tokens: the
-// token's (cos, sin), gathered from as many rows of the table as there are
-// axes, goes to shared memory once and serves all of them.
+// token's rows, or a part of its heads where there are few tokens, and gathers
+// the token's (cos, sin) once, from as many rows of the table as there are
+// axes: into registers where a row's pieces divide the warp (whole rotations of
+// 64 or 128 channels among them), into shared memory where they do not.
 #include "rope.cuh"
 
 namespace hc {
 namespace {
 
-template <typename T, int kPairing, int V>
+template <typename T, int kPairing, int V, bool kInLanes>
 __global__ void __launch_bounds__(kRopeWarps * 32) k_rope_axes(const __grid_constant__ RopeAxesParams p) {
-  __shared__ float2 cs[kRopeWarps][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
   const int64_t t = w / p.parts;
   if (t >= p.n_tokens) return;
   const int h0 = static_cast<int>(w - t * p.parts) * p.heads_per_warp;
   const int h1 = min(h0 + p.heads_per_warp, p.n_heads);
-  if (!stage_cos_sin(p.rope, static_cast<int>(t), lane, cs[warp])) {
-    if (lane == 0) flag_error(p.err, HC_DEVERR_POS);
-    return;
+  const T* x = static_cast<const T*>(p.x) + t * p.x_token;
+  T* y = static_cast<T*>(p.y) + t * p.y_token;
+  bool ok;
+  if constexpr (kInLanes) {
+    ok = rotate_rows_in_lanes<T, kPairing, V, 4>(p.rope, static_cast<int>(t), x, p.x_head, y, p.y_head, h0, h1,
+                                                 static_cast<int>(p.items_per_row.d), lane);
+  } else {
+    __shared__ float2 cs[kRopeWarps][128];
+    ok = stage_cos_sin(p.rope, static_cast<int>(t), lane, cs[warp]);
+    if (ok)
+      rotate_rows<T, kPairing, V, 4>(x, p.x_head, y, p.y_head, h0, h1, p.rope.half, cs[warp], p.items_per_row, lane);
   }
-  rotate_rows<T, kPairing, V, 4>(static_cast<const T*>(p.x) + t * p.x_token, p.x_head,
-                                 static_cast<T*>(p.y) + t * p.y_token, p.y_head, h0, h1, p.rope.half,
-                                 cs[warp], p.items_per_row, lane);
+  if (!ok && lane == 0) flag_error(p.err, HC_DEVERR_POS);
 }
 
 template <typename T, int kPairing, int V>
@@ -39,7 +45,11 @@ cudaError_t launch(RopeAxesParams p, cudaStream_t s) {
     p.heads_per_warp = (p.heads_per_warp + 1) / 2;
   p.parts = (p.n_heads + p.heads_per_warp - 1) / p.heads_per_warp;
   const int64_t warps = static_cast<int64_t>(p.n_tokens) * p.parts;
-  k_rope_axes<T, kPairing, V><<<static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps), kRopeWarps * 32, 0, s>>>(p);
+  const unsigned grid = static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps);
+  if (V * sizeof(T) == 16 && items <= 32 && 32 % items == 0)
+    k_rope_axes<T, kPairing, V, V * sizeof(T) == 16><<<grid, kRopeWarps * 32, 0, s>>>(p);
+  else
+    k_rope_axes<T, kPairing, V, false><<<grid, kRopeWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 

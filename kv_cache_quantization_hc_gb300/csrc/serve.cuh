@@ -61,7 +61,9 @@ struct RopeParams {
   int64_t position_stride;
   const float2* table;  // null: no rotation
   int32_t n_positions, half, inverse;
-  uint8_t pair_axis[128];
+  uint32_t axes;        // bit a: some pair has axis a
+  int32_t pairs16;      // two pairs of the table make an aligned 16-byte word
+  alignas(16) uint8_t pair_axis[128];
 };
 
 struct RopeAxesParams {

@@ -205,9 +205,9 @@ def _stream(s):
     """cudaStream_t of a torch stream; None means torch's current stream."""
     if isinstance(s, int):
         return s
-    import torch
     if s is None:
-        s = torch.cuda.current_stream()
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return s.cuda_stream
 
 
