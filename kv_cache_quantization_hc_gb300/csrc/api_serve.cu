@@ -133,7 +133,7 @@ int hc_rope_axes(const hc_rows* x, const hc_rows* y, int32_t dtype, int32_t n_to
   const int st = check_rope(rope, d_head, n_tokens, &p.rope);
   if (st != HC_OK) return st;
   // the kernels index a token's pieces, and the grid's warps, in 32 bits
-  if (int64_t{n_heads} * d_head >= (int64_t{1} << 31) || int64_t{n_tokens} * n_heads >= (int64_t{1} << 31))
+  if (int64_t{n_heads} * d_head >= (int64_t{1} << 31) || int64_t{n_tokens} * n_heads >= (int64_t{1} << 31) - 8)
     return HC_ERR_INVALID_ARG;
   if (n_tokens == 0 || n_heads == 0) return HC_OK;
   const int piece = 16 / es, half = rope->rot_dim / 2;
@@ -181,7 +181,7 @@ int hc_append_int4(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t
       (n_q_heads > 0 && (!rows16(*q, es, n_tokens, n_q_heads) || !rows16(*q_out, es, n_tokens, n_q_heads))))
     return HC_ERR_INVALID_ARG;
   if ((int64_t{n_q_heads} + cache->n_kv_heads) * cache->d_head >= (int64_t{1} << 31) ||
-      int64_t{n_tokens} * (int64_t{n_q_heads} + cache->n_kv_heads) >= (int64_t{1} << 31))
+      int64_t{n_tokens} * (int64_t{n_q_heads} + cache->n_kv_heads) >= (int64_t{1} << 31) - 8)
     return HC_ERR_INVALID_ARG;
   if (n_tokens == 0) return HC_OK;
   p.q = n_q_heads ? q->ptr : nullptr;

@@ -112,48 +112,51 @@ struct AppendShared {
 };
 struct NoShared {};
 
+// Three CTAs an SM (80 registers) cover the latency of a chunk's loads better
+// than two with the 96 or more registers that some variants would take.
 template <typename T, int D, int kPairing, bool kScaleF16, bool kInLanes>
-__global__ void __launch_bounds__(kRopeWarps * 32) k_append_int4(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 3) k_append_int4(const __grid_constant__ AppendParams p) {
   constexpr int V = 16 / sizeof(T);
   __shared__ std::conditional_t<kInLanes, NoShared, AppendShared<T, D>> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
-  const int parts = p.q_parts + p.kv_parts;
-  const int64_t t = w / parts;
-  if (t >= p.n_tokens) return;
-  const int part = static_cast<int>(w - t * parts);
+  uint32_t tok, part_of;
+  p.parts.divmod(blockIdx.x * kRopeWarps + warp, tok, part_of);
+  if (tok >= static_cast<uint32_t>(p.n_tokens)) return;
+  const int64_t t = tok;
+  const int part = static_cast<int>(part_of);
+  // asked after the data is on its way: what is read is there whatever the row says
   const int64_t row = __ldg(p.token_rows + t);
-  if (row < -1 || row >= p.n_rows) {
-    if (lane == 0) flag_error(p.err, HC_DEVERR_SLOT);
-    return;
-  }
+  auto row_exists = [&] {
+    const bool ok = row >= -1 && row < p.n_rows;
+    if (!ok && lane == 0) flag_error(p.err, HC_DEVERR_SLOT);
+    return ok;
+  };
   if (part < p.q_parts) {
     const int h0 = part * p.q_heads_per_warp, h1 = min(h0 + p.q_heads_per_warp, p.n_q_heads);
     const T* q = static_cast<const T*>(p.q) + t * p.q_token;
     T* q_out = static_cast<T*>(p.q_out) + t * p.o_token;
     bool ok;
     if constexpr (kInLanes) {
-      ok = rotate_rows_in_lanes<T, kPairing, V, 4>(p.rope, static_cast<int>(t), q, p.q_head, q_out, p.o_head, h0, h1,
-                                                   static_cast<int>(p.items_per_row.d), lane);
+      ok = rotate_rows_in_lanes<T, kPairing, V>(p.rope, static_cast<int>(t), q, p.q_head, q_out, p.o_head, h0, h1,
+                                                static_cast<int>(p.items_per_row.d), lane, row_exists);
     } else {
       ok = stage_cos_sin(p.rope, static_cast<int>(t), lane, sh.cs[warp]);
-      if (ok)
+      if (ok && row_exists())
         rotate_rows<T, kPairing, V, 4>(q, p.q_head, q_out, p.o_head, h0, h1, p.rope.half, sh.cs[warp], p.items_per_row, lane);
     }
     if (!ok && lane == 0) flag_error(p.err, HC_DEVERR_POS);
     return;
   }
-  if (row < 0) return;
   const int h0 = (part - p.q_parts) * kKvHeads<D>, nh = min(kKvHeads<D>, p.H - h0);
   const T* k = static_cast<const T*>(p.k) + t * p.k_token + h0 * p.k_head;
   const T* v = static_cast<const T*>(p.v) + t * p.v_token + h0 * p.v_head;
   constexpr int kLanes = D / V, kAt = 32 / kLanes;  // lanes of a row of values, rows at a time
   const int piece = lane % kLanes;
-  // values: on their way before the keys are worked on
+  // values: on their way before the keys are worked on (rows past the last repeat it and are not stored)
   Piece<T, V> vp[kKvHeads<D> / kAt];
 #pragma unroll
   for (int u = 0; u < kKvHeads<D> / kAt; ++u)
-    if (u * kAt + lane / kLanes < nh) vp[u] = load_piece<T, V>(v + (u * kAt + lane / kLanes) * p.v_head + piece * V);
+    vp[u] = load_piece<T, V>(v + min(u * kAt + lane / kLanes, nh - 1) * p.v_head + piece * V);
 
   if constexpr (kInLanes) {
     using Item = LaneItem<T, kPairing, V>;
@@ -164,23 +167,21 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_append_int4(const __grid_co
       Piece<T, V> a[(kKvHeads<D> + kRowsAt - 1) / kRowsAt], b[(kKvHeads<D> + kRowsAt - 1) / kRowsAt];
 #pragma unroll
       for (int u = 0; u < (kKvHeads<D> + kRowsAt - 1) / kRowsAt; ++u)
-        if (u * kRowsAt + item.sub < nh) item.load(k + (u * kRowsAt + item.sub) * p.k_head, a[u], b[u]);
+        item.load(k + min(u * kRowsAt + item.sub, nh - 1) * p.k_head, a[u], b[u]);
       float2 cs[Item::kPairs];
       if (!load_turns<Item::kPairs>(p.rope, static_cast<int>(t), item.first_pair(), true, lane, cs)) {
         if (lane == 0) flag_error(p.err, HC_DEVERR_POS);
         return;
       }
+      if (!row_exists() || row < 0) return;
 #pragma unroll
       for (int u = 0; u < (kKvHeads<D> + kRowsAt - 1) / kRowsAt; ++u) {
         const int r = u * kRowsAt + item.sub;
         const bool live = r < nh;
         const CacheRow to = cache_row<D>(p, row, 0, h0 + (live ? r : 0));
         float x[V], x2[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          x[i] = live ? to_f32(a[u].e[i]) : 0.f;
-          if (kSplit) x2[i] = live ? to_f32(b[u].e[i]) : 0.f;
-        }
+        widen_piece(a[u], x);
+        if (kSplit) widen_piece(b[u], x2);
 #pragma unroll
         for (int i = 0; i < Item::kPairs; ++i) {
           if (kSplit)
@@ -211,15 +212,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_append_int4(const __grid_co
         }
       }
     } else {
+      if (!row_exists() || row < 0) return;
 #pragma unroll
       for (int u = 0; u < kKvHeads<D> / kAt; ++u) {
         const int r = u * kAt + lane / kLanes;
         const bool live = r < nh;
         float x[V];
-        Piece<T, V> a;
-        if (live) a = load_piece<T, V>(k + r * p.k_head + piece * V);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = live ? to_f32(a.e[i]) : 0.f;
+        widen_piece(load_piece<T, V>(k + min(r, nh - 1) * p.k_head + piece * V), x);
         quantize_pieces<D, kScaleF16, V>(p, x, piece * V, cache_row<D>(p, row, 0, h0 + (live ? r : 0)), live);
       }
     }
@@ -229,6 +228,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_append_int4(const __grid_co
       if (lane == 0) flag_error(p.err, HC_DEVERR_POS);
       return;
     }
+    if (!row_exists() || row < 0) return;
     const int total = nh * static_cast<int>(p.items_per_row.d);
     const int half = p.rope.half;
     const int turned = kPairing == HC_PAIR_HALF_SPLIT ? half / V : 2 * half / V;
@@ -276,8 +276,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_append_int4(const __grid_co
     const int r = u * kAt + lane / kLanes;
     const bool live = r < nh;
     float x[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = live ? to_f32(vp[u].e[i]) : 0.f;
+    widen_piece(vp[u], x);
     quantize_pieces<D, kScaleF16, V>(p, x, piece * V, cache_row<D>(p, row, 1, h0 + (live ? r : 0)), live);
   }
 }
@@ -288,16 +287,12 @@ cudaError_t launch(AppendParams p, cudaStream_t s) {
   const int items = rope_items<kPairing, V>(p.rope.half, D);
   p.items_per_row = FastDivmod(static_cast<uint32_t>(items));
   p.kv_parts = (p.H + kKvHeads<D> - 1) / kKvHeads<D>;
-  p.q_heads_per_warp = std::max(1, p.n_q_heads);
-  constexpr int64_t enough = 152 * 24;
-  while (p.q_heads_per_warp > 1 && static_cast<int64_t>(p.q_heads_per_warp) * items > 32 &&
-         static_cast<int64_t>(p.n_tokens) *
-                 (p.kv_parts + (p.n_q_heads + p.q_heads_per_warp - 1) / p.q_heads_per_warp) < enough)
-    p.q_heads_per_warp = (p.q_heads_per_warp + 1) / 2;
-  p.q_parts = (p.n_q_heads + p.q_heads_per_warp - 1) / p.q_heads_per_warp;
-  const int64_t warps = static_cast<int64_t>(p.n_tokens) * (p.q_parts + p.kv_parts);
-  const unsigned grid = static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps);
   const bool in_lanes = p.rope.half == 0 || 2 * p.rope.half == D;
+  p.q_heads_per_warp = heads_per_warp(p.n_tokens, p.n_q_heads, items, in_lanes);
+  p.q_parts = (p.n_q_heads + p.q_heads_per_warp - 1) / p.q_heads_per_warp;
+  p.parts = FastDivmod(static_cast<uint32_t>(p.q_parts + p.kv_parts));
+  const int64_t warps = static_cast<int64_t>(p.n_tokens) * p.parts.d;
+  const unsigned grid = static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps);
   if (in_lanes && p.scale_f16)
     k_append_int4<T, D, kPairing, true, true><<<grid, kRopeWarps * 32, 0, s>>>(p);
   else if (in_lanes)

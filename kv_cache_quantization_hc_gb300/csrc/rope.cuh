@@ -7,6 +7,8 @@
 // it bit by bit.
 #pragma once
 
+#include <algorithm>
+
 #include "serve.cuh"
 
 namespace hc {
@@ -95,12 +97,23 @@ __device__ __forceinline__ bool load_turns(const RopeParams& p, int t, int first
   }
   ok = __all_sync(0xffffffffu, ok);
   if (!ok) return false;
-  uint8_t axis[N];
+  // the pairs' axes, 4 bytes at a time (N and first are even, or N is 1)
+  uint32_t axis[N];
   bool same = true;
+  if constexpr (N % 4 == 0) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    axis[i] = rotates ? p.pair_axis[first + i] : 0;
-    same = same && axis[i] == axis[0];
+    for (int i = 0; i < N; i += 4) {
+      const uint32_t w = rotates ? *reinterpret_cast<const uint32_t*>(p.pair_axis + first + i) : 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) axis[i + j] = __byte_perm(w, 0, 0x4440 + j);
+      same = same && w == axis[0] * 0x01010101u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      axis[i] = rotates ? p.pair_axis[first + i] : 0u;
+      same = same && axis[i] == axis[0];
+    }
   }
   if (N % 2 == 0 && p.pairs16 && __all_sync(0xffffffffu, same)) {
     const int at = __shfl_sync(0xffffffffu, pos, axis[0]);
@@ -125,6 +138,48 @@ __device__ __forceinline__ bool load_turns(const RopeParams& p, int t, int first
     for (int i = 0; i < N; ++i) cs[i].y = -cs[i].y;
   }
   return true;
+}
+
+// A piece's elements as floats, and floats as a piece: 16-bit elements two at a time.
+template <typename T, int V>
+__device__ __forceinline__ void widen_piece(const Piece<T, V>& a, float (&x)[V]) {
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+    uint32_t w[V / 2];
+    memcpy(w, &a, sizeof w);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 f = u32_to_float2(w[i], static_cast<const T*>(nullptr));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = to_f32(a.e[i]);
+  }
+}
+__device__ __forceinline__ uint32_t narrow2(float a, float b, const __half*) {
+  const __half2 h = __floats2half2_rn(a, b);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+__device__ __forceinline__ uint32_t narrow2(float a, float b, const __nv_bfloat16*) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+template <typename T, int V>
+__device__ __forceinline__ void narrow_piece(const float (&x)[V], Piece<T, V>& a) {
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = narrow2(x[2 * i], x[2 * i + 1], static_cast<const T*>(nullptr));
+    memcpy(&a, w, sizeof w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) a.e[i] = from_f32<T>(x[i]);
+  }
 }
 
 // Items of one row: its rotated pieces (half split: the piece of V pairs at
@@ -192,6 +247,21 @@ __device__ __forceinline__ void rotate_rows(const T* x, int64_t x_head, T* y, in
   }
 }
 
+// Passes over rows that a warp loads at once, and heads for a warp to take: no
+// more than one such load where that leaves few, so that nothing waits twice.
+constexpr int kRowsAhead = 4;
+inline int heads_per_warp(int n_tokens, int heads, int items, bool in_lanes) {
+  if (heads < 1) return 1;
+  int most = heads;
+  if (in_lanes) most = std::min(heads, kRowsAhead * (32 / items));
+  // few tokens: shared out until the GPU has about 24 warps per SM, or a warp has no more than an item per lane
+  constexpr int64_t enough = 152 * 24;
+  while (most > 1 && static_cast<int64_t>(most) * items > 32 &&
+         static_cast<int64_t>(n_tokens) * ((heads + most - 1) / most) < enough)
+    most = (most + 1) / 2;
+  return most;
+}
+
 // Rows whose items divide a warp's lanes: a lane has the same item of every
 // row it takes, so its (cos, sin) stay in registers.
 template <typename T, int kPairing, int V>
@@ -218,26 +288,29 @@ struct LaneItem {
   }
   __device__ __forceinline__ void turn_and_store(T* row, Piece<T, V>& a, Piece<T, V>& b, const float2 (&cs)[kPairs]) const {
     if (rotates) {
+      float x[V], x2[V];
+      widen_piece(a, x);
+      if (kHalfSplit) widen_piece(b, x2);
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        T& e1 = kHalfSplit ? a.e[i] : a.e[2 * i];
-        T& e2 = kHalfSplit ? b.e[i] : a.e[2 * i + 1];
-        float x1 = to_f32(e1), x2 = to_f32(e2);
-        turn(x1, x2, cs[i]);
-        e1 = from_f32<T>(x1);
-        e2 = from_f32<T>(x2);
+      for (int i = 0; i < kPairs; ++i) turn(kHalfSplit ? x[i] : x[2 * i], kHalfSplit ? x2[i] : x[2 * i + 1], cs[i]);
+      narrow_piece(x, a);
+      if (kHalfSplit) {
+        narrow_piece(x2, b);
+        store_piece<T, V>(row + c + half, b);
       }
-      if (kHalfSplit) store_piece<T, V>(row + c + half, b);
     }
     store_piece<T, V>(row + c, a);
   }
 };
 
 // The rows of heads [h0, h1) of token t.  The first rows are on their way
-// before the positions and the table are read.  False: a position outside.
-template <typename T, int kPairing, int V, int kUnroll>
+// before the positions and the table are read, and before `allowed` is asked
+// whether to go on.  False: a position outside.
+template <typename T, int kPairing, int V, typename Allowed>
 __device__ __forceinline__ bool rotate_rows_in_lanes(const RopeParams& rope, int t, const T* x, int64_t x_head, T* y,
-                                                     int64_t y_head, int h0, int h1, int items, int lane) {
+                                                     int64_t y_head, int h0, int h1, int items, int lane,
+                                                     const Allowed& allowed) {
+  constexpr int kUnroll = kRowsAhead;
   using Item = LaneItem<T, kPairing, V>;
   const Item item(lane, items, rope.half);
   Piece<T, V> a[kUnroll], b[kUnroll];
@@ -250,6 +323,7 @@ __device__ __forceinline__ bool rotate_rows_in_lanes(const RopeParams& rope, int
   load(h);
   float2 cs[Item::kPairs];
   if (rope.table != nullptr && !load_turns<Item::kPairs>(rope, t, item.first_pair(), item.rotates, lane, cs)) return false;
+  if (!allowed()) return true;
   for (;;) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)

@@ -12,17 +12,18 @@ namespace {
 template <typename T, int kPairing, int V, bool kInLanes>
 __global__ void __launch_bounds__(kRopeWarps * 32) k_rope_axes(const __grid_constant__ RopeAxesParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
-  const int64_t t = w / p.parts;
-  if (t >= p.n_tokens) return;
-  const int h0 = static_cast<int>(w - t * p.parts) * p.heads_per_warp;
+  uint32_t tok, part;
+  p.parts.divmod(blockIdx.x * kRopeWarps + warp, tok, part);
+  if (tok >= static_cast<uint32_t>(p.n_tokens)) return;
+  const int64_t t = tok;
+  const int h0 = static_cast<int>(part) * p.heads_per_warp;
   const int h1 = min(h0 + p.heads_per_warp, p.n_heads);
   const T* x = static_cast<const T*>(p.x) + t * p.x_token;
   T* y = static_cast<T*>(p.y) + t * p.y_token;
   bool ok;
   if constexpr (kInLanes) {
-    ok = rotate_rows_in_lanes<T, kPairing, V, 4>(p.rope, static_cast<int>(t), x, p.x_head, y, p.y_head, h0, h1,
-                                                 static_cast<int>(p.items_per_row.d), lane);
+    ok = rotate_rows_in_lanes<T, kPairing, V>(p.rope, static_cast<int>(t), x, p.x_head, y, p.y_head, h0, h1,
+                                              static_cast<int>(p.items_per_row.d), lane, [] { return true; });
   } else {
     __shared__ float2 cs[kRopeWarps][128];
     ok = stage_cos_sin(p.rope, static_cast<int>(t), lane, cs[warp]);
@@ -36,17 +37,12 @@ template <typename T, int kPairing, int V>
 cudaError_t launch(RopeAxesParams p, cudaStream_t s) {
   const int items = rope_items<kPairing, V>(p.rope.half, p.d);
   p.items_per_row = FastDivmod(static_cast<uint32_t>(items));
-  // Heads of a token are shared out among warps until the GPU has about 24
-  // warps per SM, or a warp has no more than one item per lane.
-  p.heads_per_warp = p.n_heads;
-  constexpr int64_t enough = 152 * 24;
-  while (p.heads_per_warp > 1 && static_cast<int64_t>(p.heads_per_warp) * items > 32 &&
-         static_cast<int64_t>(p.n_tokens) * ((p.n_heads + p.heads_per_warp - 1) / p.heads_per_warp) < enough)
-    p.heads_per_warp = (p.heads_per_warp + 1) / 2;
-  p.parts = (p.n_heads + p.heads_per_warp - 1) / p.heads_per_warp;
-  const int64_t warps = static_cast<int64_t>(p.n_tokens) * p.parts;
+  const bool in_lanes = V * sizeof(T) == 16 && items <= 32 && 32 % items == 0;
+  p.heads_per_warp = heads_per_warp(p.n_tokens, p.n_heads, items, false);
+  p.parts = FastDivmod(static_cast<uint32_t>((p.n_heads + p.heads_per_warp - 1) / p.heads_per_warp));
+  const int64_t warps = static_cast<int64_t>(p.n_tokens) * p.parts.d;
   const unsigned grid = static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps);
-  if (V * sizeof(T) == 16 && items <= 32 && 32 % items == 0)
+  if (in_lanes)
     k_rope_axes<T, kPairing, V, V * sizeof(T) == 16><<<grid, kRopeWarps * 32, 0, s>>>(p);
   else
     k_rope_axes<T, kPairing, V, false><<<grid, kRopeWarps * 32, 0, s>>>(p);

@@ -71,8 +71,8 @@ struct RopeAxesParams {
   const void* x;
   void* y;
   int64_t x_token, x_head, y_token, y_head;
-  int32_t n_tokens, n_heads, d, heads_per_warp, parts;
-  FastDivmod items_per_row;
+  int32_t n_tokens, n_heads, d, heads_per_warp;
+  FastDivmod parts, items_per_row;  // warps of a token; pieces of a row
   int32_t* err;
 };
 
@@ -85,7 +85,7 @@ struct AppendParams {
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
   int32_t n_tokens, n_q_heads, H, B_log2, group_log2, scale_f16;
   int32_t q_heads_per_warp, q_parts, kv_parts;
-  FastDivmod items_per_row;
+  FastDivmod parts, items_per_row;  // warps of a token; pieces of a row
   const int64_t* token_rows;
   int64_t n_rows;  // num_slots * block_size
   uint8_t* codes;
@@ -109,6 +109,7 @@ struct AttendParams {
   FastDivmod by_group;  // division by G
   float scale_log2;     // softmax_scale * log2(e)
   int32_t rows_above;   // requests with more query rows than this go to k_attend_tiles
+  int32_t piece_cost;  // of the rows kernel: what a piece's start and end take, in tiles
   uint8_t* workspace;
   int32_t* err;
 };
