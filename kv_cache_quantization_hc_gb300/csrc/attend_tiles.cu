@@ -16,7 +16,7 @@
 // two S of 128 columns, over which P is written, and two O of d.
 //
 // Mathematics, per row, with a reference m near the running maximum:
-//   x_j = f * 2^(ek + 10) * (q . k_j),  p_j = 2^(x_j - m + 7),  l = sum p_j,
+//   x_j = f * 2^(ek + 10) * (q . k_j),  p_j = 2^(x_j - m + 11),  l = sum p_j,
 //   O = sum (p_j * 2^(ev_j - ev)) v_j,  out = O / l * 2^(ev + 10)
 // * k_j = code * scale * 2^(-10 - ek) and v_j = code * scale * 2^(-10 - ev_j) in
 //   fp16, 2^ek and 2^ev_j the largest scales of the run of 32 keys that j is
@@ -25,9 +25,13 @@
 //   its exponents are too: no barrier among those warps.
 // * Queries in fp16: each row times a power of two that brings its largest
 //   value near 2^14 (f holds the inverse).
-// * m moves only when the maximum exceeds it by 8, and then to 4 above the
+// * m moves only when the maximum exceeds it by 4, and then to 3 above the
 //   maximum, so that O (in tensor memory) is rarely rescaled.  Between, a tile
 //   whose probabilities sum up to 60000 (fp16 ends at 65504) moves it too.
+//   The largest probability is then 2^8: a tile of 128 equal scores sums up to
+//   half of what moves m, and a probability keeps fp16's 11 bits down to 2^-22
+//   of the largest and some of them down to 2^-33, which channels need where
+//   the larger keys' values are zero.
 // * The channels of keys, queries and values are permuted within eights
 //   (0 4 1 5 2 6 3 7), the order in which a word of codes comes apart; the
 //   products over channels do not see it and the output is put back in order.
@@ -49,8 +53,9 @@ constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kThreadsTiles = (kSoftmaxWarps + kConvertWarps + 1) * 32;
 constexpr int kBlockBytes = kKeys * 128;  // 128 rows of 64 channels, swizzled in 128-byte rows
 constexpr int kExp = -10;        // elements times 2^(kExp - exponent of the run's largest scale)
-constexpr float kMoveAt = 8.f;   // the reference moves when the maximum is this far above it,
-constexpr float kAhead = 4.f;    // to this far above the maximum, or
+constexpr float kTop = 11.f;     // log2 of the probability of a score that equals the reference
+constexpr float kMoveAt = 4.f;   // the reference moves when the maximum is this far above it,
+constexpr float kAhead = 3.f;    // to this far above the maximum, or
 constexpr float kMostSum = 60000.f;  // when a tile's probabilities sum up to this: fp16 ends at 65504
 
 template <int D>
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
       for (int c = 0; c < 4; ++c) f[c] = factor * pow2(ek[c] - kExp);
       const int key0 = (vis.tile0 + j) * kKeys;
       const bool masked = __any_sync(0xffffffffu, key0 < first || key0 + kKeys > last);
-      // Most tiles: all of it seen, and no score more than 8 above the reference.  One pass then, with P kept
+      // Most tiles: all of it seen, and no score far above the reference.  One pass then, with P kept
       // in registers until the maximum is known, since it goes over the scores.
       float sum = 0.f;
       bool done = false, crowded = false;  // crowded: the sum was too large
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int d = max(evs[c] - ev, -126);
-          const float off = m == kNegInf ? 0.f : 7.f - m + static_cast<float>(d);
+          const float off = m == kNegInf ? 0.f : kTop - m + static_cast<float>(d);
           const float2 f2 = make_float2(f[c], f[c]), off2 = make_float2(off, off);
           float2 part = make_float2(0.f, 0.f);
 #pragma unroll
@@ -466,7 +471,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
         }
         if (masked) wait_store();
         // the reference of the row, and O with it
-        const float m_new = top > m + (crowded ? 0.f : kMoveAt) || (m == kNegInf && top > m) ? top + kAhead : m;
+        const float m_new = top > m + (crowded ? -kAhead : kMoveAt) || (m == kNegInf && top > m) ? top + kAhead : m;
         if (__any_sync(0xffffffffu, m_new != m || ev_new != ev)) {
           const float by = m == kNegInf ? 0.f : ex2(m - m_new);
           l *= by;
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int d = max(evs[c] - ev, -126);
-          const float off = m == kNegInf ? 0.f : 7.f - m + static_cast<float>(d);
+          const float off = m == kNegInf ? 0.f : kTop - m + static_cast<float>(d);
           const float2 f2 = make_float2(f[c], f[c]), off2 = make_float2(off, off);
           float2 part = make_float2(0.f, 0.f);
           uint32_t h[16];
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
     }
     fence_before();
     if (p.lse && row < rows_all)
-      p.lse[row_offset(row, static_cast<int64_t>(p.H) * p.G, 1)] = l > 0.f ? (m - 7.f + log2f(l)) * 0.6931471805599453f : kNegInf;
+      p.lse[row_offset(row, static_cast<int64_t>(p.H) * p.G, 1)] = l > 0.f ? (m - kTop + log2f(l)) * 0.6931471805599453f : kNegInf;
     __syncwarp();
 #pragma unroll 4
     for (int r0 = 0; r0 < 32; r0 += kRowsAt) {
