@@ -1,5 +1,6 @@
 // C ABI of the serving operators over a 4-bit cache: host-side validation,
 // then the launch on the caller's stream.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -72,12 +73,27 @@ int check_rope(const hc_rope_axes_desc* r, int d_head, int64_t n_tokens, hc::Rop
 
 // A request with more query rows (new tokens times query heads per cache
 // head) than this is attended in tiles of 256 rows on the 5th-generation
-// tensor cores, one with fewer in pieces of 8 or 16 rows whose keys are split
-// over the SMs.
-#ifndef HC_ATTEND_TILE_ROWS
-#define HC_ATTEND_TILE_ROWS 192
-#endif
-constexpr int kTileRows = HC_ATTEND_TILE_ROWS;
+// tensor cores (one CTA walks all keys of a tile), one with fewer in pieces of
+// 16 rows whose keys are split over the SMs.  A piece costs the GPU as a whole
+// about 1/200 of what a tile costs its SM (64 channels: 1/340), so what counts
+// is how many tiles there are: below one per SM the rest of the GPU is idle.
+// Even lengths, bf16, groups of 32 and 8 heads of 128 channels, rows against
+// tiles: 16 requests of 4000 keys, 28 rows 71 us against 62, 80 rows 146
+// against 62, 160 rows 271 against 64; 4 requests, 80 rows 52 against 60, 160
+// rows 83 against 62; 1 request, 384 rows 43 against 39 (2000 keys), 164
+// against 191 (16000).  2 heads of 64 channels, 16 requests of 4000 keys, 140
+// rows 49 against 53, 280 rows 79 against 54.  Pieces share out ragged
+// lengths, tiles wait for the longest: the factors lean to the pieces by half.
+int rows_for_pieces(int64_t n_req, int64_t heads, int d_head) {
+  constexpr int64_t kSms = 152;
+  constexpr int kMost = 384;
+  const int64_t each = n_req * heads, factor = d_head == 128 ? 300 : 500;
+  for (int rows = 16; rows <= kMost; rows += 16) {
+    const int64_t tiles = each * ((rows + 255) / 256);
+    if (each * (rows / 16) > factor * ((tiles + kSms - 1) / kSms)) return std::max(16, rows - 16);
+  }
+  return kMost;
+}
 
 }  // namespace
 
@@ -270,7 +286,7 @@ int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dty
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.workspace = static_cast<uint8_t*>(workspace);
   p.err = err_flag;
-  p.rows_above = kTileRows;
+  p.rows_above = rows_for_pieces(n_req, p.H, cache->d_head);
   const bool scale_f16 = cache->scale_dtype == HC_F16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (int64_t{max_new} * G > p.rows_above) {
