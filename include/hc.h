@@ -498,7 +498,12 @@ int hc_append_int4(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t
  *               outside the cache: its block is taken as zeros
  * Keys and values enter the products as the codes they are, or as fp16 values
  * (code times scale, scaled by a power of two); scores, softmax and sums are
- * fp32; probabilities enter the second product in fp16. */
+ * fp32.  Probabilities (times value scales) enter the second product in 16
+ * bits of mantissa and fp32's range where a request has few query rows, in fp16
+ * where it has many (about 32 to 384, fewer in calls of many requests): there
+ * what is below 2^-33 of a row's largest probability is lost.
+ * Pieces of 8 query rows times tiles of 128 keys of a call, counted by
+ * table_width, stay below 2^31. */
 int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dtype,
                    int32_t n_tokens, int32_t n_q_heads, const hc_int4_cache* cache,
                    const uint8_t* codes, const void* scales, const int32_t* block_tables,

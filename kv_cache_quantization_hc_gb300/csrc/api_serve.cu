@@ -44,12 +44,13 @@ bool rows16(const hc_rows& r, int es, int64_t n_tokens, int64_t n_heads) {
   return aligned(r.ptr, 16) && (n_tokens <= 1 || (r.token_stride * es) % 16 == 0) &&
          (n_heads <= 1 || (r.head_stride * es) % 16 == 0);
 }
-bool rows_ok(const hc_rows* r, int es) {
-  return r && r->ptr && aligned(r->ptr, es) && r->token_stride >= 0 && r->head_stride >= 0;
+// Nothing is behind a pointer to no elements, which may be NULL.
+bool rows_ok(const hc_rows* r, int es, bool any) {
+  return r && (r->ptr || !any) && aligned(r->ptr, es) && r->token_stride >= 0 && r->head_stride >= 0;
 }
 
 int check_rope(const hc_rope_axes_desc* r, int d_head, int64_t n_tokens, hc::RopeParams* out) {
-  if (!r || !r->positions || !r->table) return HC_ERR_INVALID_ARG;
+  if (!r || (!r->positions && n_tokens > 0) || !r->table) return HC_ERR_INVALID_ARG;
   if (r->n_axes < 1 || r->n_axes > 8 || r->n_positions < 1) return HC_ERR_INVALID_ARG;
   if (r->rot_dim < 2 || r->rot_dim > 256 || (r->rot_dim & 1) || r->rot_dim > d_head) return HC_ERR_INVALID_ARG;
   if (r->pairing != HC_PAIR_INTERLEAVED && r->pairing != HC_PAIR_HALF_SPLIT) return HC_ERR_INVALID_ARG;
@@ -144,7 +145,8 @@ int hc_rope_axes(const hc_rows* x, const hc_rows* y, int32_t dtype, int32_t n_to
                  int32_t* err_flag, void* stream) {
   const int es = elem_size(dtype);
   if (es == 0 || n_tokens < 0 || n_heads < 0 || d_head < 2 || d_head > 256) return HC_ERR_INVALID_ARG;
-  if (!rows_ok(x, es) || !rows_ok(y, es) || !err_flag || !aligned(err_flag, 4)) return HC_ERR_INVALID_ARG;
+  const bool any = n_tokens > 0 && n_heads > 0;
+  if (!rows_ok(x, es, any) || !rows_ok(y, es, any) || !err_flag || !aligned(err_flag, 4)) return HC_ERR_INVALID_ARG;
   hc::RopeAxesParams p;
   const int st = check_rope(rope, d_head, n_tokens, &p.rope);
   if (st != HC_OK) return st;
@@ -180,8 +182,9 @@ int hc_append_int4(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t
   if (es == 0 || n_tokens < 0 || n_q_heads < 0) return HC_ERR_INVALID_ARG;
   int st = check_cache(cache, codes, scales);
   if (st != HC_OK) return st;
-  if (!rows_ok(k, es) || !rows_ok(v, es) || !token_rows || !err_flag) return HC_ERR_INVALID_ARG;
-  if (n_q_heads > 0 && (!rows_ok(q, es) || !rows_ok(q_out, es))) return HC_ERR_INVALID_ARG;
+  const bool any = n_tokens > 0;
+  if (!rows_ok(k, es, any) || !rows_ok(v, es, any) || (!token_rows && any) || !err_flag) return HC_ERR_INVALID_ARG;
+  if (n_q_heads > 0 && (!rows_ok(q, es, any) || !rows_ok(q_out, es, any))) return HC_ERR_INVALID_ARG;
   if (!aligned(token_rows, 8) || !aligned(err_flag, 4)) return HC_ERR_INVALID_ARG;
   hc::AppendParams p;
   std::memset(&p.rope, 0, sizeof p.rope);
@@ -242,7 +245,7 @@ int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dty
   if (st != HC_OK) return st;
   if (dtype == HC_F32) return HC_ERR_UNSUPPORTED;
   if (n_q_heads % cache->n_kv_heads) return HC_ERR_INVALID_ARG;
-  if (!rows_ok(q, es) || !rows_ok(out, es) || !err_flag || !aligned(err_flag, 4) || (lse && !aligned(lse, 4)))
+  if (!rows_ok(q, es, n_tokens > 0) || !rows_ok(out, es, n_tokens > 0) || !err_flag || !aligned(err_flag, 4) || (lse && !aligned(lse, 4)))
     return HC_ERR_INVALID_ARG;
   if (!rows16(*q, es, n_tokens, n_q_heads) || !rows16(*out, es, n_tokens, n_q_heads)) return HC_ERR_INVALID_ARG;
   if (!q_starts || !aligned(q_starts, 4) || (n_req > 0 && (!kv_lens || !aligned(kv_lens, 4))))
@@ -254,8 +257,13 @@ int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dty
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < hc::attend_workspace_bytes())
     return HC_ERR_INVALID_ARG;
   const int G = n_q_heads / cache->n_kv_heads;
-  // rows of a request and tiles of a call are counted in 32 bits
+  // rows of a request, and pieces of 8 rows times tiles of 128 keys of a call, are counted in 32 bits
   if (int64_t{max_new} * G >= (int64_t{1} << 30)) return HC_ERR_INVALID_ARG;
+  const int rows_above = n_req > 0 ? rows_for_pieces(n_req, cache->n_kv_heads, cache->d_head) : 0;
+  const int64_t pieces = (std::min<int64_t>(int64_t{max_new} * G, rows_above) + 7) / 8;
+  const int64_t tiles = ((int64_t{table_width} << log2) + 127) / 128 + 2;
+  if (static_cast<double>(n_req) * cache->n_kv_heads * static_cast<double>(pieces * tiles) >= 0x1p31)
+    return HC_ERR_INVALID_ARG;
   if (n_tokens == 0 || n_req == 0 || max_new == 0) return HC_OK;
   hc::AttendParams p;
   p.q = q->ptr;
@@ -286,7 +294,7 @@ int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dty
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.workspace = static_cast<uint8_t*>(workspace);
   p.err = err_flag;
-  p.rows_above = rows_for_pieces(n_req, p.H, cache->d_head);
+  p.rows_above = rows_above;
   const bool scale_f16 = cache->scale_dtype == HC_F16;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (int64_t{max_new} * G > p.rows_above) {
