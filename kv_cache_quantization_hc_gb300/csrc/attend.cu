@@ -55,10 +55,9 @@ constexpr int kTile = kWarpsA * kKeysWarp;         // keys of a tile
 // 117 us with 2, 120 us with 4.
 constexpr int kPieceCost = 2;
 constexpr int kStages = 3;
-#ifndef HC_ATTEND_CTAS
-#define HC_ATTEND_CTAS 3
-#endif
-constexpr int kCtasPerSm = HC_ATTEND_CTAS;
+// Per SM, up to 8 query rows: 64 ragged requests took 110 us with 3, 117 us
+// with 4, whose 128 registers do not hold the loop.  16 rows: 2.
+constexpr int kCtasPerSm = 3;
 constexpr int kMaxCtas = 1024;                     // counters in the workspace
 constexpr int kMaxRows = 16;                       // rows of a piece
 constexpr float kMostSum = 0x1p40f;                // of a lane's probabilities against a reference
@@ -646,7 +645,8 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
         w.y = p.bf16 ? pack_bf16(v.z * inv, v.w * inv) : pack_f16(v.z * inv, v.w * inv);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + tok * p.o_token + h * p.o_head + ch) = w;
         if (p.lse && ch == 0)
-          p.lse[tok * (static_cast<int64_t>(p.H) * p.G) + h] = sum > 0.f ? (mref + log2f(sum)) * 0.6931471805599453f : kNegInf;
+          p.lse[tok * (static_cast<int64_t>(p.H) * p.G) + h] =
+              sum > 0.f ? (mref + log2f(sum)) * 0.6931471805599453f : kNegInf;
       };
 
       for (int id = tid; id < rows * (D / 4); id += kWarpsA * 32) {
@@ -775,8 +775,8 @@ cudaError_t launch_rows(AttendParams p, cudaStream_t s) {
 
 template <int D, int GROUP, bool kScaleF16>
 cudaError_t launch_nt(const AttendParams& p, cudaStream_t s) {
-  return std::min<int64_t>(static_cast<int64_t>(p.max_new) * p.G, p.rows_above) <= 8 ? launch_rows<D, GROUP, kScaleF16, 1>(p, s)
-                                                    : launch_rows<D, GROUP, kScaleF16, 2>(p, s);
+  const int64_t rows = std::min<int64_t>(static_cast<int64_t>(p.max_new) * p.G, p.rows_above);
+  return rows <= 8 ? launch_rows<D, GROUP, kScaleF16, 1>(p, s) : launch_rows<D, GROUP, kScaleF16, 2>(p, s);
 }
 
 template <int D, int GROUP>
