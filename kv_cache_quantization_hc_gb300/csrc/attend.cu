@@ -106,9 +106,8 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
 __device__ __forceinline__ void split_bf16(float2 v, uint32_t& high, uint32_t& low) {
   const uint32_t ux = __float_as_uint(v.x), uy = __float_as_uint(v.y);
   high = __byte_perm(ux, uy, 0x7632);
-  const float2 less = make_float2(__uint_as_float(and_xor(ux, 0xffff0000u, 0x80000000u)),
-                                  __uint_as_float(and_xor(uy, 0xffff0000u, 0x80000000u)));
-  const __nv_bfloat162 rest = __float22bfloat162_rn(__fadd2_rn(v, less));
+  const float2 kept = make_float2(__uint_as_float(high * 65536u), __uint_as_float(high & 0xffff0000u));
+  const __nv_bfloat162 rest = __float22bfloat162_rn(__ffma2_rn(kept, make_float2(-1.f, -1.f), v));
   memcpy(&low, &rest, 4);
 }
 
@@ -500,6 +499,13 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
           }
         }
 
+        // the first values' codes on their way to registers
+        uint32_t vw[kChunks / 2][4];
+#pragma unroll
+        for (int cp = 0; cp < kChunks / 2; ++cp) {
+          const int key = ((lane >> 3) & 1) * 8 + (lane & 7);
+          ldmatrix4_trans(vw[cp], vs + key * L::kRowBytes + swizzled<D>(key, cp * 2 + (lane >> 4)) * 16);
+        }
         // -- probabilities against the reference that the rows have, kept while the sums stay small
         bool done = !(key0 < all_lo || key0 + kKeysWarp > all_hi);
         float2 e[NT][kKeysWarp / 8];
@@ -577,7 +583,12 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
 #pragma unroll
           for (int cp = 0; cp < kChunks / 2; ++cp) {  // two 16-byte pieces: 64 channels
             uint32_t w[4];
-            ldmatrix4_trans(w, vs + key * L::kRowBytes + swizzled<D>(key, cp * 2 + (lane >> 4)) * 16);
+            if (mt == 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[i] = vw[cp][i];
+            } else {
+              ldmatrix4_trans(w, vs + key * L::kRowBytes + swizzled<D>(key, cp * 2 + (lane >> 4)) * 16);
+            }
 #pragma unroll
             for (int h2 = 0; h2 < 2; ++h2) {
               const int c = cp * 2 + h2;
