@@ -6,6 +6,8 @@ status into an exception.  All work runs in the library's CUDA kernels.  If
 libhc.so is missing the first call raises; there is no other code path.
 """
 import ctypes
+import functools
+import math
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -112,22 +114,15 @@ def lib():
 
 
 # ------------------------------------------------------------- marshalling
-def _ptr(x):
-    """Device/host address of a tensor, an int address, or None (NULL)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
-
-
 def _dptr(x, name):
-    """Address of a device buffer: like _ptr, but a torch tensor must live on
+    """Device address of a tensor, an int address, or None (NULL).  A tensor must live on
     a CUDA device (the kernels dereference these pointers; a host tensor
     would make them fault)."""
-    if x is not None and not isinstance(x, int) and not getattr(x, "is_cuda", False):
+    if x is None or isinstance(x, int):
+        return x
+    if not getattr(x, "is_cuda", False):
         raise ValueError(f"{name} must be a CUDA tensor (or a device address)")
-    return _ptr(x)
+    return x.data_ptr()
 
 
 def _avail(x):
@@ -161,16 +156,10 @@ def _wire_bytes(desc, n_blocks, wire, group, scale_dtype):
     """(codes bytes, scales bytes) of the wire of a call on pools like `desc`."""
     cs, cdt, ss = wire_shapes(desc.n_layers, n_blocks, desc.n_kv_heads, desc.block_size,
                               desc.d_head, wire, group)
-    n = 1
-    for v in cs:
-        n *= v
-    codes = n * (_ES.get(desc.dtype, 1) if cdt == "paged" else 1)
+    codes = math.prod(cs) * (_ES.get(desc.dtype, 1) if cdt == "paged" else 1)
     if ss is None:
         return codes, 0
-    m = 1
-    for v in ss:
-        m *= v
-    return codes, m * (4 if wire == HC_WIRE_FP8 or scale_dtype == HC_F32 else 2)
+    return codes, math.prod(ss) * (4 if wire == HC_WIRE_FP8 or scale_dtype == HC_F32 else 2)
 
 
 def _sizes_apply(desc, n_blocks, wire, group=32):
@@ -225,20 +214,25 @@ def hc_version():
     return lib().hc_version()
 
 
+@functools.lru_cache(None)
+def _hc_dtype(dtype):
+    return {"torch.float32": HC_F32, "torch.float16": HC_F16, "torch.bfloat16": HC_BF16}[str(dtype)]
+
+
 def paged_desc(pool, dtype=None, n_layers=None, layer_stride=None, slot_stride=None):
     """Descriptor of a pool tensor shaped [L, num_slots, B, H, d] (or
     [num_slots, B, H, d] for one layer).  Strides are taken from the tensor."""
-    if pool.dim() == 4:
-        pool = pool.unsqueeze(0)
-    L, S, B, H, d = pool.shape
-    if pool.stride(4) != 1 or pool.stride(3) != d or pool.stride(2) != H * d:
+    shape, strides = tuple(pool.shape), pool.stride()
+    if len(shape) == 4:
+        shape, strides = (1,) + shape, (0,) + strides
+    L, S, B, H, d = shape
+    if strides[2:] != (H * d, d, 1):
         raise ValueError("each slot must be a contiguous [B, H, d] block")
     if dtype is None:
-        dtype = {"torch.float32": HC_F32, "torch.float16": HC_F16,
-                 "torch.bfloat16": HC_BF16}[str(pool.dtype)]
+        dtype = _hc_dtype(pool.dtype)
     return hc_paged_desc(n_layers if n_layers is not None else L, H, d, B, S, dtype,
-                         slot_stride if slot_stride is not None else pool.stride(1),
-                         layer_stride if layer_stride is not None else (pool.stride(0) if L > 1 else 0))
+                         slot_stride if slot_stride is not None else strides[1],
+                         layer_stride if layer_stride is not None else (strides[0] if L > 1 else 0))
 
 
 # ------------------------------------------------------------- the C-ABI calls
