@@ -39,7 +39,12 @@
 //   sum passes 2^40 (fp32 and bf16 hold 2^-126 to 2^127), so most tiles need
 //   no maximum, and no lanes' agreement but one vote.
 //
-// Bound: the cache's bytes when rows are few (decoding).
+// Bound: the cache's bytes when rows are few; in fact the issue of about 740
+// instructions per 32 keys of 128 channels, half of them the codes' conversion.
+// 64 requests of 200 to 25000 keys, 8 cache heads of 128 channels, groups of
+// 32: 107 us, 3.6 TB/s; 8 of 131000 keys, one group per head: 250 us, 4.4 TB/s.
+// Splitting the keys into equal runs rather than per request keeps every SM
+// busy whatever the lengths; copies run two tiles ahead (three: the same).
 #include <algorithm>
 
 #include "attend_common.cuh"
