@@ -789,6 +789,8 @@ cudaError_t launch_rows(AttendParams p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Pieces of 8 rows where no request has more: 64 ragged requests of 4 rows took
+// 106 us, 144 us in pieces of 16, which need twice the products.
 template <int D, int GROUP, bool kScaleF16>
 cudaError_t launch_nt(const AttendParams& p, cudaStream_t s) {
   const int64_t rows = std::min<int64_t>(static_cast<int64_t>(p.max_new) * p.G, p.rows_above);
