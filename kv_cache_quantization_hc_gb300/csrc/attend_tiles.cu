@@ -17,7 +17,7 @@
 // two S of 128 columns, over which P is written, and two O of d.
 //
 // Mathematics, per row, with a reference m near the running maximum:
-//   x_j = f * 2^(ek + 10) * (q . k_j),  p_j = 2^(x_j - m + 11),  l = sum p_j,
+//   x_j = f * 2^(ek + 10) * (q . k_j),  p_j = 2^(x_j - m + 11.5),  l = sum p_j,
 //   O = sum (p_j * 2^(ev_j - ev)) v_j,  out = O / l * 2^(ev + 10)
 // * k_j = code * scale * 2^(-10 - ek) and v_j = code * scale * 2^(-10 - ev_j) in
 //   fp16, 2^ek and 2^ev_j the largest scales of the run of 32 keys that j is
@@ -26,13 +26,14 @@
 //   its exponents are too: no barrier among those warps.
 // * Queries in fp16: each row times a power of two that brings its largest
 //   value near 2^14 (f holds the inverse).
-// * m moves only when the maximum exceeds it by 4, and then to 3 above the
+// * m moves only when the maximum exceeds it by 3.5, and then to 3 above the
 //   maximum, so that O (in tensor memory) is rarely rescaled.  Between, a tile
 //   whose probabilities sum up to 60000 (fp16 ends at 65504) moves it too.
-//   The largest probability is then 2^8: a tile of 128 equal scores sums up to
-//   half of what moves m, and a probability keeps fp16's 11 bits down to 2^-22
-//   of the largest and some of them down to 2^-33, which channels need where
-//   the larger keys' values are zero.
+//   The largest probability is then 2^8.5: a tile of 128 equal scores sums up to
+//   three quarters of what moves m, and a probability keeps fp16's 11 bits down
+//   to 2^-22 of the largest and some of them down to 2^-33, which channels need
+//   where the larger keys' values are zero.  That takes rows of few keys, mostly,
+//   so where a row sees n keys of its first tile m starts 128 / n times lower.
 // * The channels of keys, queries and values are permuted within eights
 //   (0 4 1 5 2 6 3 7), the order in which a word of codes comes apart; the
 //   products over channels do not see it and the output is put back in order.
@@ -62,8 +63,8 @@ constexpr int kThreadsTiles = (kWorkWarp + 1) * 32;
 constexpr int kWorksAhead = 4;   // found before they are begun
 constexpr int kBlockBytes = kKeys * 128;  // 128 rows of 64 channels, swizzled in 128-byte rows
 constexpr int kExp = -10;        // elements times 2^(kExp - exponent of the run's largest scale)
-constexpr float kTop = 11.f;     // log2 of the probability of a score that equals the reference
-constexpr float kMoveAt = 4.f;   // the reference moves when the maximum is this far above it,
+constexpr float kTop = 11.5f;    // log2 of the probability of a score that equals the reference
+constexpr float kMoveAt = 3.5f;  // the reference moves when the maximum is this far above it,
 constexpr float kAhead = 3.f;    // to this far above the maximum, or
 constexpr float kMostSum = 60000.f;  // when a tile's probabilities sum up to this: fp16 ends at 65504
 
@@ -521,7 +522,14 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
           }
           if (masked) wait_store();
           // the reference of the row, and O with it
-          const float m_new = top > m + (crowded ? -kAhead : kMoveAt) || (m == kNegInf && top > m) ? top + kAhead : m;
+          // where the row sees n keys of the tile, 128 / n times closer: n of them do not pass kMostSum either
+          float ahead = kAhead;
+          if (masked) {  // n keys seen: 128 / n times closer, as n of them do not pass kMostSum either
+            const int n = min(hi, kKeys) - max(lo, 0);
+            if (n < kKeys) ahead -= static_cast<float>(__clz(max(n - 1, 0)) - __clz(kKeys - 1));
+          }
+          const float m_new =
+              top > m + (crowded ? -kAhead : kMoveAt) || (m == kNegInf && top > m) ? top + ahead : m;
           if (__any_sync(0xffffffffu, m_new != m || ev_new != ev)) {
             const float by = m == kNegInf ? 0.f : ex2(m - m_new);
             l *= by;

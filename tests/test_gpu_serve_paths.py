@@ -41,3 +41,19 @@ def test_scores_that_fall_along_the_keys(serve, workspace, new):  # noqa: F811
         for j in range(n):
             c.scales[c.table[i, j // 16], 0, :, j % 16] *= 2.0 ** (14 - j // 16 / 4)
     _check_attend(serve, workspace, c)
+
+
+def test_more_requests_than_are_ordered(serve, workspace):  # noqa: F811
+    """Above 256 requests the tiles' works are taken in the requests' order."""
+    r = np.random.default_rng(3)
+    kv = [int(v) for v in r.integers(0, 120, 300)]
+    new = [int(v) for v in r.integers(0, 25, 300)]
+    _check_attend(serve, workspace, Cache(34, kv, new, Hq=10, H=2, d=64, B=16, group=32))
+
+
+@pytest.mark.parametrize("mask", [dict(), dict(window=600), dict(causal=False)], ids=str)
+def test_prompts_over_caches_of_different_lengths(serve, workspace, mask):  # noqa: F811
+    """Works of 1 to 21 tiles of keys, taken by the powers of two of what they see."""
+    new = [300, 120, 64, 200, 1, 90]
+    kv = [300, 2620, 764, 240, 1500, 50]
+    _check_attend(serve, workspace, Cache(35, kv, new, Hq=8, H=1, d=64, B=32, group=64, dtype="f16", **mask))
