@@ -459,8 +459,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
 #pragma unroll
         for (int c = 0; c < 4; ++c) f[c] = factor * pow2(ek[c] - kExp);
         const int key0 = (work.vis.tile0 + j) * kKeys;
-        const bool masked = __any_sync(0xffffffffu, key0 < first || key0 + kKeys > last);
-        // Most tiles: all of it seen, and no score far above the reference.  One pass then, with P kept
+        // A row may see all of this tile and nothing before it (its window starts here): no reference yet, so not
+        // for the one pass either.  In the vote that is taken anyway it costs nothing (chunks 133.4 us with and without).
+        const bool masked = __any_sync(0xffffffffu, key0 < first || key0 + kKeys > last || (j > 0 && m == kNegInf));
+        // Most tiles: all of it seen, by rows that have a reference, and no score far above that.  One pass then, with P kept
         // in registers until the maximum is known, since it goes over the scores.
         float sum = 0.f;
         bool done = false, crowded = false;  // crowded: the sum was too large
