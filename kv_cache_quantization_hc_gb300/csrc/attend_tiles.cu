@@ -455,9 +455,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
         const int ek[4] = {ek4.x, ek4.y, ek4.z, ek4.w}, evs[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
         // one above the largest when it moves, so that it moves rarely
         const int ev_tile = max(max(evs[0], evs[1]), max(evs[2], evs[3])), ev_new = ev_tile > ev ? ev_tile + 1 : ev;
-        float f[4];  // the scores' factor, of each run of 32 keys
+        // The scores' factor, of each run of 32 keys: never 0 (queries and keys of zeros, softmax_scale 0), as hidden
+        // scores are -inf and go through the same product; 2^-126 times a sum of 2^34 at most is as good as 0.
+        float f[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) f[c] = factor * pow2(ek[c] - kExp);
+        for (int c = 0; c < 4; ++c) f[c] = fmaxf(factor * pow2(ek[c] - kExp), 0x1p-126f);
         const int key0 = (work.vis.tile0 + j) * kKeys;
         // A row may see all of this tile and nothing before it (its window starts here): no reference yet, so not
         // for the one pass either.  In the vote that is taken anyway it costs nothing (chunks 133.4 us with and without).
