@@ -442,6 +442,18 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
         l[nt] = make_float2(0.f, 0.f);
       }
 
+      // Rows before the window came along with their run of 16 and may hold anything.  Their probabilities are 0, but
+      // 0 times a value scale that is infinite or NaN is not (scores are replaced, whatever they are).  Only the first
+      // tile has such rows; inside the loop this took 250 us to 253 (8 requests of 131000 keys, no window).
+      if (key_first < vis.lo) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        if (key_first + lane < vis.lo) {
+          uint16_t* hidden = reinterpret_cast<uint16_t*>(stages + 2 * L::kCodeBytes + L::kScaleStage + lane * L::kScaleBytes);
+#pragma unroll
+          for (int i = 0; i < L::kScaleBytes / 2; ++i) hidden[i] = 0;
+        }
+      }
       for (int i = 0; i < seg; ++i) {
         cp_async_wait<kStages - 2>();
         __syncwarp();

@@ -1,4 +1,4 @@
-"""Prompts with a sliding window whose first key is the first of a tile of 128 keys."""
+"""Attention with a sliding window: windows that start with a tile of 128 keys, and what lies before a window."""
 import numpy as np
 import pytest
 
@@ -42,3 +42,17 @@ def test_a_key_before_the_window_dominates(serve, workspace, Hq, H, scale, at, w
     assert int(err) == 0 and off[kept].max() <= 1, off[kept].max()
     off = np.abs(lse.double().cpu().numpy() - want_lse) / lse_bar(want_lse, reach)
     assert off.max() <= 1, off.max()
+
+
+@pytest.mark.parametrize("scale", ["f16", "f32"])
+@pytest.mark.parametrize("d,group", [(64, 64), (128, 32), (128, 128)])
+@pytest.mark.parametrize("new,Hq", [(1, 4), (3, 8), (30, 2), (300, 4)])
+def test_rows_before_the_window_hold_anything(serve, workspace, new, Hq, d, group, scale):  # noqa: F811
+    """Infinite and NaN scales in the rows that have left the window, in blocks that still hold visible ones."""
+    c = Cache(43, [new + 461, 77 + new, new + 5], [new] * 3, Hq=Hq, H=2, d=d, B=32, group=group, scale=scale, window=70)
+    r = np.random.default_rng(1)
+    for i, n in enumerate(c.kv):
+        first = max(0, n - c.new[i] - c.window + 1)
+        for j in range(first // 32 * 32, first):
+            c.scales[c.table[i, j // 32], :, :, j % 32] = r.choice([np.nan, np.inf, -np.inf, 6e4])
+    _check_attend(serve, workspace, c)
