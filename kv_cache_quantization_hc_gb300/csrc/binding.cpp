@@ -96,10 +96,13 @@ bool truth(PyObject* o) {
 bool none(PyObject* o) { return o == Py_None; }
 
 // The tensors' device made current for the call, and the stream: None for
-// torch's current one, an integer cudaStream_t, or a torch.cuda.Stream.
+// torch's current one, an integer cudaStream_t, or a torch.cuda.Stream.  What
+// the call allocates, it allocates on that stream: a block of another stream
+// may still be in use by work queued there.
 struct Where {
   c10::cuda::CUDAGuard guard;
   cudaStream_t stream;
+  c10::cuda::OptionalCUDAStreamGuard on_stream;
   Where(const at::Tensor& t, PyObject* s) : guard(t.device()) {
     if (none(s)) {
       stream = c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
@@ -110,10 +113,16 @@ struct Where {
     stream = static_cast<cudaStream_t>(PyLong_AsVoidPtr(handle));
     Py_DECREF(handle);
     if (PyErr_Occurred()) throw PythonError{};
+    if (stream == cudaStreamPerThread) return;  // see empty
+    // cudaStreamLegacy is another name of the default stream
+    on_stream.reset_stream(c10::cuda::getStreamFromExternal(stream == cudaStreamLegacy ? nullptr : stream,
+                                                            t.device().index()));
   }
 };
 
-at::Tensor empty(at::IntArrayRef size, at::ScalarType dtype, const at::Tensor& like) {
+at::Tensor empty(at::IntArrayRef size, at::ScalarType dtype, const at::Tensor& like, const Where& w) {
+  // one handle for as many streams as there are host threads: the allocator cannot tell them apart
+  if (w.stream == cudaStreamPerThread) throw BadArgument("on cudaStreamPerThread the output tensors have to be given");
   return at::Tensor(at::detail::empty_cuda(size, dtype, like.device(), std::nullopt));
 }
 
@@ -210,17 +219,16 @@ PyObject* build_block_tables(PyObject* const* a) {
   const int64_t sizes[6] = {n_req + 1, n_req, n_tokens, n_tokens, n_tokens, 1};
   static const char* const names[6] = {"q_starts", "kv_lens", "token_req", "token_pos", "token_rows", "n_taken"};
   const Where w(cached, a[8]);
-  PyObject* result;
-  if (none(a[7])) {
-    result = PyStructSequence_New(step_tables_type);
-    if (!result) throw PythonError{};
-    for (int i = 0; i < 6; ++i)
-      PyStructSequence_SetItem(result, i, THPVariable_Wrap(empty({sizes[i]}, i == 4 ? at::kLong : at::kInt, cached)));
-  } else {
-    if (Py_TYPE(a[7]) != step_tables_type) throw BadArgument("out must be a StepTables");
-    result = Py_NewRef(a[7]);
-  }
+  const bool makes = none(a[7]);
+  if (!makes && Py_TYPE(a[7]) != step_tables_type) throw BadArgument("out must be a StepTables");
+  PyObject* result = makes ? PyStructSequence_New(step_tables_type) : Py_NewRef(a[7]);
+  if (!result) throw PythonError{};
   try {
+    for (int i = 0; makes && i < 6; ++i) {
+      PyObject* t = THPVariable_Wrap(empty({sizes[i]}, i == 4 ? at::kLong : at::kInt, cached, w));
+      if (!t) throw PythonError{};
+      PyStructSequence_SetItem(result, i, t);
+    }
     void* p[6];
     for (int i = 0; i < 6; ++i)
       p[i] = buffer(PyStructSequence_GetItem(result, i), names[i], i == 4 ? at::kLong : at::kInt, sizes[i]).data_ptr();
@@ -248,7 +256,7 @@ PyObject* rope_axes(PyObject* const* a) {
   const hc_rope_axes_desc rope = rope_desc(a[1], a[2], a[3], a[5], truth(a[6]), n);
   const at::Tensor& err = buffer(a[4], "err", at::kInt, 1);
   const Where w(x, a[8]);
-  const at::Tensor y = none(a[7]) ? empty({n, heads, d}, x.scalar_type(), x) : tensor(a[7], "out");
+  const at::Tensor y = none(a[7]) ? empty({n, heads, d}, x.scalar_type(), x, w) : tensor(a[7], "out");
   const hc_rows yr = rows(y, "out", n, heads, d, x.scalar_type());
   check("hc_rope_axes", hc_rope_axes(&xr, &yr, dtype, i32(n, "n_tokens"), i32(heads, "n_heads"), i32(d, "d"), &rope,
                                      data<int32_t>(err), w.stream));
@@ -277,7 +285,7 @@ PyObject* append_int4(PyObject* const* a) {
     const at::Tensor& q = tensor(a[0], "q");
     qr = rows(q, "q", n, -1, cache.d_head, st);
     heads = q.size(1);
-    out = none(a[11]) ? empty({n, heads, cache.d_head}, st, k) : tensor(a[11], "q_out");
+    out = none(a[11]) ? empty({n, heads, cache.d_head}, st, k, w) : tensor(a[11], "q_out");
     qo = rows(out, "q_out", n, heads, cache.d_head, st);
   }
   hc_rope_axes_desc rope;
@@ -314,14 +322,14 @@ PyObject* attend_int4(PyObject* const* a) {
     if (scale == -1.0 && PyErr_Occurred()) throw PythonError{};
   }
   const Where w(q, a[15]);
-  const at::Tensor y = none(a[12]) ? empty({n, heads, cache.d_head}, q.scalar_type(), q) : tensor(a[12], "out");
+  const at::Tensor y = none(a[12]) ? empty({n, heads, cache.d_head}, q.scalar_type(), q, w) : tensor(a[12], "out");
   const hc_rows yr = rows(y, "out", n, heads, cache.d_head, q.scalar_type());
   const bool with_lse = truth(a[14]);
   at::Tensor lse;
   if (!none(a[13]))
     lse = buffer(a[13], "lse", at::kFloat, n * heads);
   else if (with_lse)
-    lse = empty({n, heads}, at::kFloat, q);
+    lse = empty({n, heads}, at::kFloat, q, w);
   check("hc_attend_int4",
         hc_attend_int4(&qr, &yr, lse.defined() ? data<float>(lse) : nullptr, dtype, i32(n, "n_tokens"),
                        i32(heads, "heads"), &cache, data<uint8_t>(codes), scales.data_ptr(), data<int32_t>(table),

@@ -11,8 +11,9 @@ a decoder:
     o = attend_int4(q, codes, scales, tables, step.q_starts, step.kv_lens, max_new, workspace, err)
 
 Every call takes its tensors on the GPU, enqueues its kernel on `stream`
-(default: torch's current stream) and returns without synchronising; an
-argument it cannot take raises.  What only the device sees (a slot, length or
+(default: torch's current stream; else a torch.cuda.Stream or a cudaStream_t as
+an integer) and returns without synchronising; tensors that it makes are
+allocated on that stream.  An argument it cannot take raises.  What only the device sees (a slot, length or
 position out of range) sets bits HC_DEVERR_* in `err`, an int32 tensor that
 the caller zeroes and reads.  Tensors used on another stream than the one
 they were allocated on are the caller's to record (`Tensor.record_stream`).
