@@ -396,11 +396,11 @@ typedef struct hc_rope_axes_desc {
  * get token_req = -1, token_pos = 0, token_rows = -1.
  *
  *   cached_lens, new_lens : device int32 [n_req], read-only; n_req >= 0
- *   free_slots   : device int32 [n_free], slots not in use, taken from the front
+ *   free_slots   : device int32 [n_free], slots not in use, taken from the front; n_free < 2^31 - 1
  *   block_tables : device int32, entry j of request r at r * table_stride + j; the
  *                  entries of held blocks are read, those of new blocks written
  *   table_width  : entries per request; table_stride >= table_width
- *   n_tokens     : entries of the token arrays (>= 0)
+ *   n_tokens     : entries of the token arrays (0 to 2^31 - 2)
  *   q_starts     : device int32 [n_req + 1];  kv_lens : device int32 [n_req]
  *   token_req, token_pos : device int32 [n_tokens];  token_rows : device int64 [n_tokens]
  *   n_taken      : device int32, free slots that were taken
@@ -412,7 +412,9 @@ typedef struct hc_rope_axes_desc {
  *                  few (the blocks without a slot get -1, their tokens row -1,
  *                  and n_taken is n_free)
  *   block_size   : 16, 32, 64 or 128
- * All sums stay below 2^31 (precondition, not checked). */
+ * Lengths may hold anything: a sum of new tokens or of new blocks past 2^31 - 1
+ * is taken as 2^31 - 1, which is more than the call holds and flagged as such,
+ * and nothing is written outside the arrays. */
 int hc_build_block_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t n_req,
                           int32_t block_size, const int32_t* free_slots, int32_t n_free,
                           int32_t* block_tables, int64_t table_stride, int32_t table_width,

@@ -106,7 +106,9 @@ int hc_build_block_tables(const int32_t* cached_lens, const int32_t* new_lens, i
                           int32_t n_tokens, int32_t* q_starts, int32_t* kv_lens,
                           int32_t* token_req, int32_t* token_pos, int64_t* token_rows,
                           int32_t* n_taken, int32_t* err_flag, void* stream) {
-  if (n_req < 0 || n_free < 0 || n_tokens < 0 || block_size < 1) return HC_ERR_INVALID_ARG;
+  // a sum that stops at 2^31 - 1 is then more than the call holds, and flagged
+  if (n_req < 0 || n_free < 0 || n_tokens < 0 || n_free == INT32_MAX || n_tokens == INT32_MAX || block_size < 1)
+    return HC_ERR_INVALID_ARG;
   const int log2 = block_log2(block_size);
   if (log2 < 0) return HC_ERR_UNSUPPORTED;
   if (!q_starts || !n_taken || !err_flag) return HC_ERR_INVALID_ARG;

@@ -11,8 +11,12 @@
 // after the first CTA, which costs less than a second launch or a chain of
 // CTAs waiting on one another.  A thread then takes 4 consecutive tokens and
 // finds the first one's request by bisection.
+//
+// Lengths come from the device and may be anything: the sums stop at 2^31 - 1
+// (counts.h), more than the arrays hold, and indexes near that are unsigned.
 #include <algorithm>
 
+#include "counts.h"
 #include "serve.cuh"
 
 namespace hc {
@@ -46,10 +50,10 @@ __global__ void __launch_bounds__(kTableThreads) k_block_tables(BlockTableParams
   extern __shared__ __align__(16) unsigned char smem_raw[];
   ChunkSmem& s = *reinterpret_cast<ChunkSmem*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gthread = blockIdx.x * kTableThreads + tid;
-  const int gthreads = gridDim.x * kTableThreads;
+  const uint32_t gthread = blockIdx.x * kTableThreads + tid;
+  const uint32_t gthreads = gridDim.x * kTableThreads;
   const int B = 1 << p.block_log2;
-  uint64_t carry = 0;  // (blocks << 32) + tokens of the requests before this chunk
+  uint64_t carry = 0;  // counts of the requests before this chunk
   int bad = 0;
 
   for (int r0 = 0; r0 < p.n_req; r0 += kChunk) {
@@ -69,74 +73,76 @@ __global__ void __launch_bounds__(kTableThreads) k_block_tables(BlockTableParams
         const int need = ok ? static_cast<int>(((cr + n + B - 1) >> p.block_log2) - ((cr + B - 1) >> p.block_log2)) : 0;
         c[i] = ok ? static_cast<int>(cr) : -1;
         kv[i] = ok ? static_cast<int>(cr + n) : 0;
-        v[i] = (static_cast<uint64_t>(need) << 32) + static_cast<uint64_t>(n > 0 ? n : 0);
-        sum += v[i];
+        v[i] = counts(static_cast<uint32_t>(n > 0 ? n : 0), static_cast<uint32_t>(need));
+        sum = add_counts(sum, v[i]);
       }
     }
     uint64_t inc = sum;  // inclusive scan over the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
+      if (lane >= o) inc = add_counts(inc, t);
     }
     if (lane == 31) s.warp[warp] = inc;
+    uint64_t before = __shfl_up_sync(0xffffffffu, inc, 1);  // the lanes before: a sum that stopped has no difference
+    if (lane == 0) before = 0;
     __syncthreads();
     if (warp == 0) {
-      const uint64_t w = s.warp[lane];
-      uint64_t wi = w;
+      uint64_t wi = s.warp[lane];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint64_t t = __shfl_up_sync(0xffffffffu, wi, o);
-        if (lane >= o) wi += t;
+        if (lane >= o) wi = add_counts(wi, t);
       }
-      s.warp[lane] = wi - w;
+      const uint64_t w = __shfl_up_sync(0xffffffffu, wi, 1);
+      s.warp[lane] = lane == 0 ? 0 : w;
       if (lane == 31) s.total = wi;
     }
     __syncthreads();
-    uint64_t at = carry + s.warp[warp] + inc - sum;
+    uint64_t at = add_counts(carry, add_counts(s.warp[warp], before));
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const int r = tid * kPerThread + i;
       if (r < nr) {
-        s.tok[r] = static_cast<int32_t>(at);
-        s.blk[r] = static_cast<int32_t>(at >> 32);
+        s.tok[r] = static_cast<int32_t>(tokens_of(at));
+        s.blk[r] = static_cast<int32_t>(blocks_of(at));
         s.cached[r] = c[i];
         if (writes_requests) {
-          p.q_starts[r0 + r] = static_cast<int32_t>(at);
+          p.q_starts[r0 + r] = static_cast<int32_t>(tokens_of(at));
           p.kv_lens[r0 + r] = kv[i];
         }
       }
-      at += v[i];
+      at = add_counts(at, v[i]);
     }
-    const uint64_t next = carry + s.total;
+    const uint64_t next = add_counts(carry, s.total);
     __syncthreads();
 
     // new blocks: their slots, from the front of the free list
-    const int b_end = static_cast<int>(next >> 32);
-    for (int b = static_cast<int>(carry >> 32) + gthread; b < b_end; b += gthreads) {
-      const int r = last_not_above(s.blk, nr, b);
-      const int j = ((s.cached[r] + B - 1) >> p.block_log2) + b - s.blk[r];
+    const uint32_t b_end = blocks_of(next), n_free = static_cast<uint32_t>(p.n_free);
+    for (uint32_t b = blocks_of(carry) + gthread; b < b_end; b += gthreads) {
+      const int r = last_not_above(s.blk, nr, static_cast<int>(b));
+      const int j = ((s.cached[r] + B - 1) >> p.block_log2) + static_cast<int>(b) - s.blk[r];
       int slot = -1;
-      if (b < p.n_free) slot = __ldg(p.free_slots + b); else bad |= HC_DEVERR_FREE;
+      if (b < n_free) slot = __ldg(p.free_slots + b); else bad |= HC_DEVERR_FREE;
       p.tables[(r0 + r) * p.table_stride + j] = slot;
     }
 
     // new tokens, 4 to a thread
-    const int t0 = static_cast<int>(carry), t_end = static_cast<int>(next);
+    const int t0 = static_cast<int>(tokens_of(carry)), t_end = static_cast<int>(tokens_of(next));
     if (t_end > p.n_tokens) bad |= HC_DEVERR_LENGTH;
     const int t1 = min(t_end, p.n_tokens);
-    for (int item = t0 / kTokensPerItem + gthread; item * kTokensPerItem < t1; item += gthreads) {
-      const int t = item * kTokensPerItem;
+    for (uint32_t item = t0 / kTokensPerItem + gthread; item * kTokensPerItem < static_cast<uint32_t>(t1); item += gthreads) {
+      const int t = static_cast<int>(item * kTokensPerItem);
       int req[4], pos[4];
       int64_t row[4];
       int r = last_not_above(s.tok, nr, max(t, t0));
-      const bool whole = t >= t0 && t + 4 <= t1;
+      const bool whole = t >= t0 && t <= t1 - 4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int ti = t + i;
         req[i] = pos[i] = 0;
         row[i] = -1;
-        if (ti < t0 || ti >= t1) continue;
+        if (t < t0 - i || t >= t1 - i) continue;
+        const int ti = t + i;
         while (r + 1 < nr && s.tok[r + 1] <= ti) ++r;
         const int cr = s.cached[r];
         req[i] = r0 + r;
@@ -147,8 +153,8 @@ __global__ void __launch_bounds__(kTableThreads) k_block_tables(BlockTableParams
           if (j < held) {
             slot = p.tables[(r0 + r) * p.table_stride + j];
           } else {
-            const int b = s.blk[r] + j - held;
-            slot = b < p.n_free ? __ldg(p.free_slots + b) : -1;
+            const uint32_t b = static_cast<uint32_t>(s.blk[r]) + static_cast<uint32_t>(j - held);
+            slot = b < n_free ? __ldg(p.free_slots + b) : -1;
           }
           if (slot >= 0) row[i] = (static_cast<int64_t>(slot) << p.block_log2) + (pos[i] & (B - 1));
         }
@@ -169,16 +175,15 @@ __global__ void __launch_bounds__(kTableThreads) k_block_tables(BlockTableParams
     __syncthreads();
   }
 
-  const int total = static_cast<int>(carry);
-  for (int t = total + gthread; t < p.n_tokens; t += gthreads) {  // a step padded to n_tokens
+  const uint32_t total = tokens_of(carry);
+  for (uint32_t t = total + gthread; t < static_cast<uint32_t>(p.n_tokens); t += gthreads) {  // a step padded to n_tokens
     p.token_req[t] = -1;
     p.token_pos[t] = 0;
     p.token_rows[t] = -1;
   }
   if (blockIdx.x == 0 && tid == 0) {
-    p.q_starts[p.n_req] = total;
-    const int need = static_cast<int>(carry >> 32);
-    *p.n_taken = min(need, p.n_free);
+    p.q_starts[p.n_req] = static_cast<int32_t>(total);
+    *p.n_taken = min(static_cast<int32_t>(blocks_of(carry)), p.n_free);
   }
   flag_error(p.err, bad);
 }
@@ -193,7 +198,7 @@ cudaError_t launch_block_tables(const BlockTableParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // one thread per 4 tokens or per new block (at most one per request and block of tokens)
   const int64_t blocks = (static_cast<int64_t>(p.n_tokens) >> p.block_log2) + p.n_req;
-  const int64_t items = std::max<int64_t>((p.n_tokens + 3) / 4, blocks);
+  const int64_t items = std::max<int64_t>((static_cast<int64_t>(p.n_tokens) + 3) / 4, blocks);
   const int64_t ctas = (items + kTableThreads - 1) / kTableThreads;
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ctas, resident)));
   k_block_tables<<<grid, kTableThreads, sizeof(ChunkSmem), s>>>(p);
