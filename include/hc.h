@@ -448,8 +448,10 @@ int hc_rope_axes(const hc_rows* x, const hc_rows* y, int32_t dtype, int32_t n_to
  *   s32 = fp32(amax * fp32(1/7));  s = fp16_rne(s32) if scale_dtype == HC_F16, else s32;
  *   code = clamp(round_half_even(fp32(x / s)), -7, 7) with the stored s, 0 if s == 0.
  * hc_encode_int4 divides amax by 7: its fp32 scales may differ from these in
- * the last bit, its fp16 scales of fp16 or bf16 elements do not for
- * amax >= 1e-5.  A token with row -1 (a padded step) gets its q_out but no
+ * the last bit (and a code beside a half with them), its fp16 scales of fp16 or
+ * bf16 elements do not for amax >= 1e-5.  Where appended blocks have to be the
+ * bytes that the encoder writes (content digests), use hc_append_int4_wire.  A
+ * token with row -1 (a padded step) gets its q_out but no
  * cache row.
  *
  *   q, q_out : [n_tokens][n_q_heads][d_head], or NULL with n_q_heads = 0
@@ -468,6 +470,14 @@ int hc_append_int4(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t
                    int32_t n_tokens, int32_t n_q_heads, const hc_rope_axes_desc* rope,
                    const int64_t* token_rows, const hc_int4_cache* cache, uint8_t* codes,
                    void* scales, const hc_rows* q_out, int32_t* err_flag, void* stream);
+
+/* hc_append_int4_wire: as hc_append_int4, with the scales of hc_encode_int4,
+ * s32 = fp32(amax / 7): the same rows give the same bytes, for any dtype and
+ * scale_dtype. */
+int hc_append_int4_wire(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t dtype,
+                        int32_t n_tokens, int32_t n_q_heads, const hc_rope_axes_desc* rope,
+                        const int64_t* token_rows, const hc_int4_cache* cache, uint8_t* codes,
+                        void* scales, const hc_rows* q_out, int32_t* err_flag, void* stream);
 
 /* hc_attend_int4: attention of the new tokens over the 4-bit cache.  Request r
  * has queries t in [q_starts[r], q_starts[r+1]), the last of its kv_lens[r]

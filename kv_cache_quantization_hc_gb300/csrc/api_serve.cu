@@ -96,6 +96,63 @@ int rows_for_pieces(int64_t n_req, int64_t heads, int d_head) {
   return kMost;
 }
 
+int append_int4(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t dtype, int32_t n_tokens,
+                int32_t n_q_heads, const hc_rope_axes_desc* rope, const int64_t* token_rows,
+                const hc_int4_cache* cache, uint8_t* codes, void* scales, const hc_rows* q_out, int32_t* err_flag,
+                bool wire_scales, void* stream) {
+  const int es = elem_size(dtype);
+  if (es == 0 || n_tokens < 0 || n_q_heads < 0) return HC_ERR_INVALID_ARG;
+  int st = check_cache(cache, codes, scales);
+  if (st != HC_OK) return st;
+  const bool any = n_tokens > 0;
+  if (!rows_ok(k, es, any) || !rows_ok(v, es, any) || (!token_rows && any) || !err_flag) return HC_ERR_INVALID_ARG;
+  if (n_q_heads > 0 && (!rows_ok(q, es, any) || !rows_ok(q_out, es, any))) return HC_ERR_INVALID_ARG;
+  if (!aligned(token_rows, 8) || !aligned(err_flag, 4)) return HC_ERR_INVALID_ARG;
+  hc::AppendParams p;
+  std::memset(&p.rope, 0, sizeof p.rope);
+  int pairing = HC_PAIR_HALF_SPLIT;
+  if (rope) {
+    st = check_rope(rope, cache->d_head, n_tokens, &p.rope);
+    if (st != HC_OK) return st;
+    if (rope->inverse) return HC_ERR_INVALID_ARG;
+    if (rope->rot_dim % 16) return HC_ERR_UNSUPPORTED;
+    pairing = rope->pairing;
+  }
+  if (!rows16(*k, es, n_tokens, cache->n_kv_heads) || !rows16(*v, es, n_tokens, cache->n_kv_heads) ||
+      (n_q_heads > 0 && (!rows16(*q, es, n_tokens, n_q_heads) || !rows16(*q_out, es, n_tokens, n_q_heads))))
+    return HC_ERR_INVALID_ARG;
+  if ((int64_t{n_q_heads} + cache->n_kv_heads) * cache->d_head >= (int64_t{1} << 31) ||
+      int64_t{n_tokens} * (int64_t{n_q_heads} + cache->n_kv_heads) >= (int64_t{1} << 31) - 8)
+    return HC_ERR_INVALID_ARG;
+  if (n_tokens == 0) return HC_OK;
+  p.q = n_q_heads ? q->ptr : nullptr;
+  p.q_out = n_q_heads ? q_out->ptr : nullptr;
+  p.q_token = n_q_heads ? q->token_stride : 0;
+  p.q_head = n_q_heads ? q->head_stride : 0;
+  p.o_token = n_q_heads ? q_out->token_stride : 0;
+  p.o_head = n_q_heads ? q_out->head_stride : 0;
+  p.k = k->ptr;
+  p.k_token = k->token_stride;
+  p.k_head = k->head_stride;
+  p.v = v->ptr;
+  p.v_token = v->token_stride;
+  p.v_head = v->head_stride;
+  p.n_tokens = n_tokens;
+  p.n_q_heads = n_q_heads;
+  p.H = cache->n_kv_heads;
+  p.B_log2 = block_log2(cache->block_size);
+  p.group_log2 = cache->group == 128 ? 7 : cache->group == 64 ? 6 : 5;
+  p.scale_f16 = cache->scale_dtype == HC_F16;
+  p.wire_scales = wire_scales;
+  p.token_rows = token_rows;
+  p.n_rows = int64_t{cache->num_slots} * cache->block_size;
+  p.codes = codes;
+  p.scales = scales;
+  p.err = err_flag;
+  return hc::record_cuda(
+      hc::launch_append_int4(dtype, cache->d_head, pairing, p, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -180,56 +237,16 @@ int hc_append_int4(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t
                    int32_t n_tokens, int32_t n_q_heads, const hc_rope_axes_desc* rope,
                    const int64_t* token_rows, const hc_int4_cache* cache, uint8_t* codes,
                    void* scales, const hc_rows* q_out, int32_t* err_flag, void* stream) {
-  const int es = elem_size(dtype);
-  if (es == 0 || n_tokens < 0 || n_q_heads < 0) return HC_ERR_INVALID_ARG;
-  int st = check_cache(cache, codes, scales);
-  if (st != HC_OK) return st;
-  const bool any = n_tokens > 0;
-  if (!rows_ok(k, es, any) || !rows_ok(v, es, any) || (!token_rows && any) || !err_flag) return HC_ERR_INVALID_ARG;
-  if (n_q_heads > 0 && (!rows_ok(q, es, any) || !rows_ok(q_out, es, any))) return HC_ERR_INVALID_ARG;
-  if (!aligned(token_rows, 8) || !aligned(err_flag, 4)) return HC_ERR_INVALID_ARG;
-  hc::AppendParams p;
-  std::memset(&p.rope, 0, sizeof p.rope);
-  int pairing = HC_PAIR_HALF_SPLIT;
-  if (rope) {
-    st = check_rope(rope, cache->d_head, n_tokens, &p.rope);
-    if (st != HC_OK) return st;
-    if (rope->inverse) return HC_ERR_INVALID_ARG;
-    if (rope->rot_dim % 16) return HC_ERR_UNSUPPORTED;
-    pairing = rope->pairing;
-  }
-  if (!rows16(*k, es, n_tokens, cache->n_kv_heads) || !rows16(*v, es, n_tokens, cache->n_kv_heads) ||
-      (n_q_heads > 0 && (!rows16(*q, es, n_tokens, n_q_heads) || !rows16(*q_out, es, n_tokens, n_q_heads))))
-    return HC_ERR_INVALID_ARG;
-  if ((int64_t{n_q_heads} + cache->n_kv_heads) * cache->d_head >= (int64_t{1} << 31) ||
-      int64_t{n_tokens} * (int64_t{n_q_heads} + cache->n_kv_heads) >= (int64_t{1} << 31) - 8)
-    return HC_ERR_INVALID_ARG;
-  if (n_tokens == 0) return HC_OK;
-  p.q = n_q_heads ? q->ptr : nullptr;
-  p.q_out = n_q_heads ? q_out->ptr : nullptr;
-  p.q_token = n_q_heads ? q->token_stride : 0;
-  p.q_head = n_q_heads ? q->head_stride : 0;
-  p.o_token = n_q_heads ? q_out->token_stride : 0;
-  p.o_head = n_q_heads ? q_out->head_stride : 0;
-  p.k = k->ptr;
-  p.k_token = k->token_stride;
-  p.k_head = k->head_stride;
-  p.v = v->ptr;
-  p.v_token = v->token_stride;
-  p.v_head = v->head_stride;
-  p.n_tokens = n_tokens;
-  p.n_q_heads = n_q_heads;
-  p.H = cache->n_kv_heads;
-  p.B_log2 = block_log2(cache->block_size);
-  p.group_log2 = cache->group == 128 ? 7 : cache->group == 64 ? 6 : 5;
-  p.scale_f16 = cache->scale_dtype == HC_F16;
-  p.token_rows = token_rows;
-  p.n_rows = int64_t{cache->num_slots} * cache->block_size;
-  p.codes = codes;
-  p.scales = scales;
-  p.err = err_flag;
-  return hc::record_cuda(
-      hc::launch_append_int4(dtype, cache->d_head, pairing, p, static_cast<cudaStream_t>(stream)));
+  return append_int4(q, k, v, dtype, n_tokens, n_q_heads, rope, token_rows, cache, codes, scales, q_out, err_flag,
+                     false, stream);
+}
+
+int hc_append_int4_wire(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t dtype,
+                        int32_t n_tokens, int32_t n_q_heads, const hc_rope_axes_desc* rope,
+                        const int64_t* token_rows, const hc_int4_cache* cache, uint8_t* codes,
+                        void* scales, const hc_rows* q_out, int32_t* err_flag, void* stream) {
+  return append_int4(q, k, v, dtype, n_tokens, n_q_heads, rope, token_rows, cache, codes, scales, q_out, err_flag,
+                     true, stream);
 }
 
 int64_t hc_attend_int4_workspace(void) { return hc::attend_workspace_bytes(); }

@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "div7.cuh"
 #include "rope.cuh"
 
 namespace hc {
@@ -55,9 +56,10 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[N], float s) {
   return packed;
 }
 
+// `wire`: the encoders' amax / 7, which differs from the product in the last bit of some fp32 scales.
 template <bool kScaleF16>
-__device__ __forceinline__ float scale_of(float amax) {
-  const float s = __fmul_rn(amax, 0x1.24924ap-3f);  // fp32(1/7)
+__device__ __forceinline__ float scale_of(float amax, int wire) {
+  const float s = wire ? div7(amax) : __fmul_rn(amax, 0x1.24924ap-3f);  // fp32(1/7)
   return kScaleF16 ? __half2float(__float2half_rn(s)) : s;
 }
 template <bool kScaleF16>
@@ -102,7 +104,7 @@ __device__ __forceinline__ CacheRow cache_row(const AppendParams& p, int64_t row
 template <int D, bool kScaleF16, int V>
 __device__ __forceinline__ void quantize_pieces(const AppendParams& p, const float (&x)[V], int channel, CacheRow to,
                                                 bool live) {
-  const float s = scale_of<kScaleF16>(amax_over(amax_of(x), (1 << p.group_log2) / V));
+  const float s = scale_of<kScaleF16>(amax_over(amax_of(x), (1 << p.group_log2) / V), p.wire_scales);
   const uint32_t packed = codes_of(x, s);
   if (!live) return;
   store_codes<V>(to.codes, channel, packed);
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 3) k_append_int4(const __grid
           if (one) m1 = fmaxf(m1, m2);
           m1 = amax_over(m1, lanes);
           m2 = one ? m1 : amax_over(m2, lanes);
-          const float s1 = scale_of<kScaleF16>(m1), s2 = one ? s1 : scale_of<kScaleF16>(m2);
+          const float s1 = scale_of<kScaleF16>(m1, p.wire_scales), s2 = one ? s1 : scale_of<kScaleF16>(m2, p.wire_scales);
           const uint32_t c1 = codes_of(x, s1), c2 = codes_of(x2, s2);
           if (live) {
             store_codes<V>(to.codes, item.c, c1);

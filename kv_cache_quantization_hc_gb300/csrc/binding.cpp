@@ -264,7 +264,7 @@ PyObject* rope_axes(PyObject* const* a) {
 }
 
 PyObject* append_int4(PyObject* const* a) {
-  // q, k, v, token_rows, codes, scales, positions, table, pair_axis, err, pairing, q_out, stream
+  // q, k, v, token_rows, codes, scales, positions, table, pair_axis, err, pairing, q_out, stream, wire_scales
   const at::Tensor& codes = buffer(a[4], "codes", at::kByte);
   const at::Tensor& scales = tensor(a[5], "scales");
   const hc_int4_cache cache = cache_desc(codes, scales);
@@ -291,10 +291,12 @@ PyObject* append_int4(PyObject* const* a) {
   hc_rope_axes_desc rope;
   const bool turns = !none(a[7]);
   if (turns) rope = rope_desc(a[6], a[7], a[8], a[10], false, n);
-  check("hc_append_int4",
-        hc_append_int4(has_q ? &qr : nullptr, &kr, &vr, dtype, i32(n, "n_tokens"), i32(heads, "heads"),
-                       turns ? &rope : nullptr, data<int64_t>(token_rows), &cache, data<uint8_t>(codes),
-                       scales.data_ptr(), has_q ? &qo : nullptr, data<int32_t>(err), w.stream));
+  const bool wire = truth(a[13]);
+  const auto append = wire ? hc_append_int4_wire : hc_append_int4;
+  check(wire ? "hc_append_int4_wire" : "hc_append_int4",
+        append(has_q ? &qr : nullptr, &kr, &vr, dtype, i32(n, "n_tokens"), i32(heads, "heads"), turns ? &rope : nullptr,
+               data<int64_t>(token_rows), &cache, data<uint8_t>(codes), scales.data_ptr(), has_q ? &qo : nullptr,
+               data<int32_t>(err), w.stream));
   if (!has_q) Py_RETURN_NONE;
   return none(a[11]) ? THPVariable_Wrap(out) : Py_NewRef(a[11]);
 }
@@ -372,7 +374,7 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<build_block_tables, 9>("build_block_tables"), method<rope_axes, 9>("rope_axes"),
-                         method<append_int4, 13>("append_int4"), method<attend_int4, 16>("attend_int4"),
+                         method<append_int4, 14>("append_int4"), method<attend_int4, 16>("attend_int4"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve", "Native binding of the serving calls (see serve.py).", -1,

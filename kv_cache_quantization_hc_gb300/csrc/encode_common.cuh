@@ -1,8 +1,9 @@
 // Pieces shared by the encode kernels (encode.cu, encode_rows.cu): E4M3
-// conversion, the corrected-quotient FP8 codes for 16-bit sources, the
-// division-free amax / 7, and the source block-table lookups.
+// conversion, the corrected-quotient FP8 codes for 16-bit sources, and the
+// source block-table lookups.
 #pragma once
 
+#include "div7.cuh"
 #include "hc_internal.cuh"
 
 namespace hc {
@@ -51,16 +52,6 @@ __device__ __noinline__ uint2 fp8x8_divide(Raw8<SrcT> raw, float s) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) c[e] = fp8x2(make_float2(__fdiv_rn(x[e].x, s), __fdiv_rn(x[e].y, s)));
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-}
-
-// fp32(a / 7) for every non-negative finite fp32 a, without a division: the
-// product with fp32(1/7) is corrected by its exact residual (Markstein's
-// correction, as in int4x8_corrected).  Checked against the IEEE division on
-// the GPU for all 2^31 non-negative finite fp32 values: no mismatch.
-__device__ __forceinline__ float div7(float a) {
-  const float r7 = 0.142857149f;  // fp32(1/7)
-  const float q1 = a * r7;
-  return fmaf(fmaf(-q1, 7.0f, a), r7, q1);
 }
 
 // Block-table entries a warp needs for one unit.

@@ -83,7 +83,7 @@ struct AppendParams {
   const void* v;
   void* q_out;
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
-  int32_t n_tokens, n_q_heads, H, B_log2, group_log2, scale_f16;
+  int32_t n_tokens, n_q_heads, H, B_log2, group_log2, scale_f16, wire_scales;
   int32_t q_heads_per_warp, q_parts, kv_parts;
   FastDivmod parts, items_per_row;  // warps of a token; pieces of a row
   const int64_t* token_rows;

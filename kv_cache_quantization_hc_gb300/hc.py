@@ -89,10 +89,12 @@ def lib():
         L.hc_rope_axes.argtypes = [rows_p, rows_p, _I32, _I32, _I32, _I32, rope_p, _P, _P]
         L.hc_append_int4.argtypes = [rows_p, rows_p, rows_p, _I32, _I32, _I32, rope_p, _P, cache_p, _P,
                                      _P, rows_p, _P, _P]
+        L.hc_append_int4_wire.argtypes = L.hc_append_int4.argtypes
         L.hc_attend_int4.argtypes = [rows_p, rows_p, _P, _I32, _I32, _I32, cache_p, _P, _P, _P, _I64,
                                      _I32, _P, _P, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _I64, _P,
                                      _P]
-        for fn in ("hc_build_block_tables", "hc_rope_axes", "hc_append_int4", "hc_attend_int4"):
+        for fn in ("hc_build_block_tables", "hc_rope_axes", "hc_append_int4", "hc_append_int4_wire",
+                   "hc_attend_int4"):
             getattr(L, fn).restype = ctypes.c_int
         L.hc_attend_int4_workspace.argtypes = []
         L.hc_attend_int4_workspace.restype = _I64

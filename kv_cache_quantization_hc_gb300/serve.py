@@ -76,12 +76,13 @@ def rope_axes(x, positions, table, pair_axis, err, pairing="half_split", inverse
 
 
 def append_int4(q, k, v, token_rows, codes, scales, positions, table, pair_axis, err,
-                pairing="half_split", q_out=None, stream=None):
+                pairing="half_split", q_out=None, stream=None, wire_scales=False):
     """hc_append_int4: k, v [n_tokens, H, d] into the cache at token_rows
     (int64), keys rotated; returns the rotated q (None for q None).  table
-    None: no rotation (positions and pair_axis unused)."""
+    None: no rotation (positions and pair_axis unused).  wire_scales=True
+    (hc_append_int4_wire): the bytes that hc_encode_int4 gives for the same rows."""
     return _serve.append_int4(q, k, v, token_rows, codes, scales, positions, table, pair_axis, err, pairing, q_out,
-                              stream)
+                              stream, wire_scales)
 
 
 def attend_int4(q, codes, scales, block_tables, q_starts, kv_lens, max_new, workspace, err, causal=True,
