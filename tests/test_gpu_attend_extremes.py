@@ -40,3 +40,20 @@ def test_a_softmax_scale_of_zero(serve, workspace, kv, new, mask):  # noqa: F811
 @pytest.mark.parametrize("kv,new", [(450, 450), (130, 3)])
 def test_a_negative_softmax_scale(serve, workspace, kv, new):  # noqa: F811
     _check_attend(serve, workspace, Cache(54, [kv], [new], Hq=4, H=4, d=64, B=16, group=32), softmax_scale=-0.2)
+
+
+@pytest.mark.parametrize("large", [3e4, 1e8, 1e20])
+@pytest.mark.parametrize("kv,new", [(1000, 450), (1000, 2)])
+def test_keys_without_values_count(serve, workspace, kv, new, large):  # noqa: F811
+    """Most keys have values of zeros and a small weight each, which the sum must not lose beside a few large values."""
+    c = Cache(55, [kv], [new], Hq=1, H=1, d=64, B=16, group=32, scale="f32", outliers=False, hostile=False)
+    c.codes[:, 0] = 0
+    slot = c.table[0, 0]
+    c.codes[slot, 0, :, 5, 0] = 7
+    c.scales[:, 0] = oserve.round_like(0.943, "f32")            # key 5 scores 6.6, the others 0
+    c.q[:, :, 0] = 8.0
+    keep = c.scales[c.table[0, :2], 1].copy()
+    c.scales[:, 1] = 0
+    c.scales[c.table[0, :2], 1] = keep * large                    # keys 0 to 31
+    c.scales = oserve.round_like(c.scales, "f32")
+    _check_attend(serve, workspace, c)
