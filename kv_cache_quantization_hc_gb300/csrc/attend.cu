@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // 2^e <= amax < 2^(e+1); queries times 2^(14-e)
-        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100), 100);
+        const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);  // at most 127: finite
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
         float sum[kGroups];
 #pragma unroll
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kWarpsA * 32, NT == 1 ? kCtasPerSm : 2)
             sum[cc / kChunksPerGroup] += (v.x + v.y) * ((k & 1) ? 16.f : 1.f);
           }
         }
-        factor[nt] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 10 + e) << 23);  // 2^(24-14+e)
+        factor[nt] = p.scale_log2 * 1024.f * pow2(e);  // 2^(24-14+e), which fp32 does not hold by itself from e = 118 on
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
           sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);

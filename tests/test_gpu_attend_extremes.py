@@ -57,3 +57,12 @@ def test_keys_without_values_count(serve, workspace, kv, new, large):  # noqa: F
     c.scales[c.table[0, :2], 1] = keep * large                    # keys 0 to 31
     c.scales = oserve.round_like(c.scales, "f32")
     _check_attend(serve, workspace, c)
+
+
+@pytest.mark.parametrize("size", [1e30, 1e34, 3e37])
+@pytest.mark.parametrize("kv,new", [(450, 450), (130, 3)])
+def test_queries_near_the_largest_bf16(serve, workspace, kv, new, size):  # noqa: F811
+    c = Cache(56, [kv], [new], Hq=4, H=4, d=64, B=16, group=32, q_scale=size, outliers=False)
+    # scores up to 220; up to 7.4 where probabilities are fp16, which keep their bits down to 2^-22 of the largest
+    for x in (3.0 if new == 3 else 0.1, 0.01):
+        _check_attend(serve, workspace, c, softmax_scale=x / size)
