@@ -508,12 +508,17 @@ int hc_append_int4_wire(const hc_rows* q, const hc_rows* k, const hc_rows* v, in
  *               than n_tokens holds, or a length outside its table: its rows of
  *               out and lse are left as they were; HC_DEVERR_SLOT: a slot
  *               outside the cache: its block is taken as zeros
- * Keys and values enter the products as the codes they are, or as fp16 values
- * (code times scale, scaled by a power of two); scores, softmax and sums are
- * fp32.  Probabilities (times value scales) enter the second product in 16
- * bits of mantissa and fp32's range where a request has few query rows, in fp16
- * where it has many (about 32 to 384, fewer in calls of many requests): there
- * what is below 2^-33 of a row's largest probability is lost.
+ * Scores, softmax and sums are fp32; queries enter the products as fp16, each
+ * row scaled by a power of two.  A request of few query rows (its new tokens
+ * times n_q_heads / n_kv_heads; hc_attend_int4_few_rows says how many) is
+ * attended with the keys' and values' codes as they are, and probabilities
+ * (times value scales) in 16 bits of mantissa and fp32's range.  One of more
+ * rows is attended with keys and values as fp16 (code times scale, scaled by a
+ * power of two; an element below 2^-18 of the largest of its 32 keys loses
+ * bits) and probabilities as fp16: what is below 2^-33 of a row's largest is
+ * lost.  So the last bits of a request's result depend on the number of
+ * requests in its call, which the limit depends on; for the same call they are
+ * the same every time.
  * Pieces of 8 query rows times tiles of 128 keys of a call, counted by
  * table_width, stay below 2^31. */
 int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dtype,
@@ -523,6 +528,11 @@ int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dty
                    const int32_t* kv_lens, int32_t n_req, int32_t max_new, int32_t causal,
                    int32_t window, float softmax_scale, void* workspace,
                    int64_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* hc_attend_int4_few_rows: the largest number of query rows of a request that
+ * an hc_attend_int4 call of n_req requests takes as few (a host function; see
+ * there), or a negative hc_status. */
+int32_t hc_attend_int4_few_rows(int32_t n_req, int32_t n_kv_heads, int32_t d_head);
 
 /* hc_attend_int4_workspace: bytes of workspace that any hc_attend_int4 call
  * needs (a host function; the same on every call). */

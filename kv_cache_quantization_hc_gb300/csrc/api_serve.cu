@@ -249,6 +249,12 @@ int hc_append_int4_wire(const hc_rows* q, const hc_rows* k, const hc_rows* v, in
                      true, stream);
 }
 
+int32_t hc_attend_int4_few_rows(int32_t n_req, int32_t n_kv_heads, int32_t d_head) {
+  if (n_req < 1 || n_kv_heads < 1 || d_head < 1) return HC_ERR_INVALID_ARG;
+  if (d_head != 64 && d_head != 128) return HC_ERR_UNSUPPORTED;
+  return rows_for_pieces(n_req, n_kv_heads, d_head);
+}
+
 int64_t hc_attend_int4_workspace(void) { return hc::attend_workspace_bytes(); }
 
 int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dtype,

@@ -96,6 +96,8 @@ def lib():
         for fn in ("hc_build_block_tables", "hc_rope_axes", "hc_append_int4", "hc_append_int4_wire",
                    "hc_attend_int4"):
             getattr(L, fn).restype = ctypes.c_int
+        L.hc_attend_int4_few_rows.argtypes = [_I32, _I32, _I32]
+        L.hc_attend_int4_few_rows.restype = _I32
         L.hc_attend_int4_workspace.argtypes = []
         L.hc_attend_int4_workspace.restype = _I64
         for fn in ("hc_encode_fp8", "hc_encode_fp8_crc", "hc_encode_int4", "hc_encode_fp8_rows",

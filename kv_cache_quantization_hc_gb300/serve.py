@@ -55,6 +55,16 @@ def attend_workspace(device="cuda"):
     return torch.zeros(hc.lib().hc_attend_int4_workspace(), dtype=torch.uint8, device=device)
 
 
+def attend_few_rows(n_req, n_kv_heads, d):
+    """hc_attend_int4_few_rows: the largest number of query rows of a request (new
+    tokens times query heads per cache head) that attend_int4 takes as few in a
+    call of n_req requests; others are attended in fp16 tiles."""
+    rows = hc.lib().hc_attend_int4_few_rows(n_req, n_kv_heads, d)
+    if rows < 0:
+        hc._check("hc_attend_int4_few_rows", rows)
+    return rows
+
+
 def build_block_tables(cached_lens, new_lens, free_slots, block_tables, block_size, n_tokens, err,
                        out=None, stream=None):
     """hc_build_block_tables: writes the new blocks' slots into block_tables
