@@ -86,12 +86,12 @@ int check_rope(const hc_rope_axes_desc* r, int d_head, int64_t n_tokens, hc::Rop
 // rows 49 against 53, 280 rows 79 against 54.  Pieces share out ragged
 // lengths, tiles wait for the longest: the factors lean to the pieces by half.
 int rows_for_pieces(int64_t n_req, int64_t heads, int d_head) {
-  constexpr int64_t kSms = 152;
+  const int64_t sms = hc::device_sm_count();
   constexpr int kMost = 384;
   const int64_t each = n_req * heads, factor = d_head == 128 ? 300 : 500;
   for (int rows = 16; rows <= kMost; rows += 16) {
     const int64_t tiles = each * ((rows + 255) / 256);
-    if (each * (rows / 16) > factor * ((tiles + kSms - 1) / kSms)) return std::max(16, rows - 16);
+    if (each * (rows / 16) > factor * ((tiles + sms - 1) / sms)) return std::max(16, rows - 16);
   }
   return kMost;
 }

@@ -259,7 +259,7 @@ inline int heads_per_warp(int n_tokens, int heads, int items, bool in_lanes) {
   if (in_lanes) most = std::min(heads, kRowsAhead * (32 / items));
   // few tokens: shared out until the GPU has the 16 warps per SM that k_rope_axes' registers let in (24: 8.8 us
   // instead of 8.1 for 1369 x 40 rows), or a warp has no more than an item per lane
-  constexpr int64_t enough = 152 * 16;
+  const int64_t enough = int64_t{device_sm_count()} * 16;
   while (most > 1 && static_cast<int64_t>(most) * items > 32 &&
          static_cast<int64_t>(n_tokens) * ((heads + most - 1) / most) < enough)
     most = (most + 1) / 2;
