@@ -1,6 +1,6 @@
-"""Build libhc.so (the C-ABI library) in-tree with nvcc for sm_103a, and
-_serve (the Python binding of the serving calls, over torch's C++ headers)
-with the host compiler.
+"""Build libhc.so (the C-ABI library) in-tree with nvcc for sm_103a, and,
+where torch is installed, _serve (the Python binding of the serving calls,
+over torch's C++ headers) with the host compiler.
 
 The translation units compile in parallel; the link uses nvcc's default
 static CUDA runtime, so the library depends on no libcudart at load time.
@@ -9,10 +9,12 @@ library built for this machine's architecture.
 """
 import fcntl
 import hashlib
+import importlib.util
 import os
 import platform
 import shutil
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -65,15 +67,37 @@ def _binding_flags():
                    "-L", PKG, "-l:libhc.so", f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"]
 
 
-def _stamp(extra_flags):
-    import torch
-    h = hashlib.sha256(torch.__version__.encode())
-    for p in [os.path.join(CSRC, s) for s in SOURCES + ["binding.cpp"]] + _headers():
+def _digest(paths, *words):
+    h = hashlib.sha256()
+    for p in paths:
         with open(p, "rb") as f:
             h.update(p.encode() + b"\0" + f.read())
-    h.update(" ".join(FLAGS + list(extra_flags)).encode())
-    h.update(platform.machine().encode())
+    for w in words + (platform.machine(),):
+        h.update(w.encode() + b"\0")
     return h.hexdigest()
+
+
+def _stamp(extra_flags):
+    return _digest([os.path.join(CSRC, s) for s in SOURCES] + _headers(), " ".join(FLAGS + list(extra_flags)))
+
+
+def _torch_home():
+    """Where torch is installed, found without importing it; None where it is not."""
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None or spec.origin is None else os.path.dirname(spec.origin)
+
+
+def _binding_stamp(torch_home):
+    return _digest([os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "hc.h"),
+                    os.path.join(torch_home, "version.py")], sys.version)
+
+
+def _current(path, stamp_path, stamp):
+    """True if the file at path was built here for this stamp."""
+    if not _lib_matches_host(path) or not os.path.exists(stamp_path):
+        return False
+    with open(stamp_path) as f:
+        return f.read().strip() == stamp
 
 
 def _lib_matches_host(path):
@@ -90,8 +114,9 @@ def _lib_matches_host(path):
 
 
 def build(force=False, verbose=False, extra_flags=(), out_dir=None):
-    """Compile and link libhc.so; returns its path.  ``out_dir`` places the
-    objects and the library elsewhere (a variant built with extra flags).
+    """Compile and link libhc.so, and where torch is installed the binding;
+    returns the library's path.  ``out_dir`` places the objects and the
+    library elsewhere (a variant built with extra flags, without a binding).
     Concurrent callers (the ranks of a torchrun job) take turns on a lock
     file in the build directory: the first builds, the others then find the
     stamp up to date."""
@@ -105,54 +130,59 @@ def build(force=False, verbose=False, extra_flags=(), out_dir=None):
             fcntl.flock(lock, fcntl.LOCK_UN)
 
 
-def _build_locked(build_dir, force, verbose, extra_flags, out_dir):
-    lib = LIB if out_dir is None else os.path.join(out_dir, "libhc.so")
-    stamp = _stamp(extra_flags)
-    stamp_path = os.path.join(build_dir, "stamp")
-    with_binding = out_dir is None
-    if not force and _lib_matches_host(lib) and os.path.exists(stamp_path) and \
-            (not with_binding or _lib_matches_host(BINDING)):
-        with open(stamp_path) as f:
-            if f.read().strip() == stamp:
-                return lib
+def _run(what, cmd, verbose=False):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout + r.stderr)
+
+
+def _build_library(lib, build_dir, verbose, extra_flags, ex):
     nvcc = _nvcc()
 
     def compile_one(src):
         obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
-        cmd = [nvcc, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout + r.stderr)
+        _run(f"nvcc on {src}", [nvcc, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
         return obj
 
-    def run(what, cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{what} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    objs = list(ex.map(compile_one, SOURCES))
+    _run("link", [nvcc, *ARCH, "-shared", "-o", lib + ".tmp", *objs])
+    os.replace(lib + ".tmp", lib)
 
-    def compile_binding():
-        obj = os.path.join(build_dir, "binding.o")
-        run("binding", [cxx, *binding_flags, "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj])
-        return obj
 
+def _compile_binding(build_dir):
+    """Compiles it; the command that links it, once libhc.so is there, without its output."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("a C++ compiler is required to build the Python binding")
+    flags, libs = _binding_flags()
+    obj = os.path.join(build_dir, "binding.o")
+    _run("binding", [cxx, *flags, "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj])
+    return [cxx, "-shared", obj, *libs]
+
+
+def _build_locked(build_dir, force, verbose, extra_flags, out_dir):
+    lib = LIB if out_dir is None else os.path.join(out_dir, "libhc.so")
+    stamp, stamp_path = _stamp(extra_flags), os.path.join(build_dir, "stamp")
+    binding_stamp_path = os.path.join(build_dir, "binding_stamp")
+    # the library needs nvcc alone; the binding is for torch's tensors
+    torch_home = _torch_home() if out_dir is None else None
+    with_binding = torch_home is not None
+    binding_stamp = _binding_stamp(torch_home) if with_binding else None
+    library_due = force or not _current(lib, stamp_path, stamp)
+    binding_due = with_binding and (force or not _current(BINDING, binding_stamp_path, binding_stamp))
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        if with_binding:
-            cxx = shutil.which("g++") or shutil.which("c++")
-            if cxx is None:
-                raise RuntimeError("a C++ compiler is required to build the Python binding")
-            binding_flags, binding_libs = _binding_flags()
-            binding = ex.submit(compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
-        tmp = lib + ".tmp"
-        run("link", [nvcc, *ARCH, "-shared", "-o", tmp, *objs])
-        os.replace(tmp, lib)
-        if with_binding:
-            run("binding's link", [cxx, "-shared", "-o", BINDING + ".tmp", binding.result(), *binding_libs])
+        binding = ex.submit(_compile_binding, build_dir) if binding_due else None
+        if library_due:
+            _build_library(lib, build_dir, verbose, extra_flags, ex)
+            with open(stamp_path, "w") as f:
+                f.write(stamp)
+        if binding_due:
+            _run("binding's link", binding.result() + ["-o", BINDING + ".tmp"])
             os.replace(BINDING + ".tmp", BINDING)
-    with open(stamp_path, "w") as f:
-        f.write(stamp)
+            with open(binding_stamp_path, "w") as f:
+                f.write(binding_stamp)
     return lib
 
 
