@@ -29,26 +29,38 @@ struct BadArgument : std::runtime_error {
   using std::runtime_error::runtime_error;
 };
 
-const at::Tensor& tensor(PyObject* o, const char* name) {
-  if (!THPVariable_Check(o)) throw BadArgument(std::string(name) + " must be a torch tensor");
-  const at::Tensor& t = THPVariable_Unpack(o);
-  if (!t.is_cuda()) throw BadArgument(std::string(name) + " must be a CUDA tensor");
-  return t;
-}
-
 const char* type_name(at::ScalarType s) { return c10::toString(s); }
 
-// A contiguous tensor of `dtype` with at least `numel` elements.
-const at::Tensor& buffer(PyObject* o, const char* name, at::ScalarType dtype, int64_t numel = 0) {
-  const at::Tensor& t = tensor(o, name);
-  if (t.scalar_type() != dtype)
-    throw BadArgument(std::string(name) + " must be " + type_name(dtype) + ", not " + type_name(t.scalar_type()));
-  if (!t.is_contiguous()) throw BadArgument(std::string(name) + " must be contiguous");
-  if (t.numel() < numel)
-    throw BadArgument(std::string(name) + " has " + std::to_string(t.numel()) + " elements; the call addresses " +
-                      std::to_string(numel));
-  return t;
-}
+// The tensors of a call, all on one GPU: the kernel that the call launches
+// there dereferences them all.
+struct Tensors {
+  const at::Tensor* first = nullptr;
+
+  const at::Tensor& tensor(PyObject* o, const char* name) {
+    if (!THPVariable_Check(o)) throw BadArgument(std::string(name) + " must be a torch tensor");
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda()) throw BadArgument(std::string(name) + " must be a CUDA tensor");
+    if (!first) first = &t;
+    if (t.device() != first->device())
+      throw BadArgument(std::string(name) + " is on " + t.device().str() + ", other tensors of the call on " +
+                        first->device().str());
+    return t;
+  }
+  // None: null
+  const at::Tensor* given(PyObject* o, const char* name) { return o == Py_None ? nullptr : &tensor(o, name); }
+
+  // A contiguous tensor of `dtype` with at least `numel` elements.
+  const at::Tensor& buffer(PyObject* o, const char* name, at::ScalarType dtype, int64_t numel = 0) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.scalar_type() != dtype)
+      throw BadArgument(std::string(name) + " must be " + type_name(dtype) + ", not " + type_name(t.scalar_type()));
+    if (!t.is_contiguous()) throw BadArgument(std::string(name) + " must be contiguous");
+    if (t.numel() < numel)
+      throw BadArgument(std::string(name) + " has " + std::to_string(t.numel()) + " elements; the call addresses " +
+                        std::to_string(numel));
+    return t;
+  }
+};
 
 template <typename T>
 T* data(const at::Tensor& t) {
@@ -148,11 +160,11 @@ int64_t table_stride(const at::Tensor& t, int64_t n_req) {
   return n_req > 1 ? t.stride(0) : t.size(1);
 }
 
-hc_rope_axes_desc rope_desc(PyObject* positions, PyObject* table, PyObject* pair_axis, PyObject* pairing,
+hc_rope_axes_desc rope_desc(Tensors& in, PyObject* positions, PyObject* table, PyObject* pair_axis, PyObject* pairing,
                             bool inverse, int64_t n) {
   hc_rope_axes_desc r;
   std::memset(&r, 0, sizeof r);
-  const at::Tensor& pos = tensor(positions, "positions");
+  const at::Tensor& pos = in.tensor(positions, "positions");
   const bool flat = pos.dim() == 1;
   if (pos.scalar_type() != at::kInt || (!flat && pos.dim() != 2) || pos.size(-1) != n || (n > 1 && pos.stride(-1) != 1))
     throw BadArgument("positions must be int32 [n_axes, " + std::to_string(n) + "], each axis adjacent");
@@ -171,7 +183,7 @@ hc_rope_axes_desc rope_desc(PyObject* positions, PyObject* table, PyObject* pair
   Py_DECREF(seq);
   if (PyErr_Occurred()) throw PythonError{};
   if (!ok) throw BadArgument("pair_axis holds the axis (below " + std::to_string(r.n_axes) + ") of each of 1 to 128 pairs");
-  const at::Tensor& tab = buffer(table, "table", at::kFloat);
+  const at::Tensor& tab = in.buffer(table, "table", at::kFloat);
   if (tab.dim() != 3 || tab.size(1) != half || tab.size(2) != 2)
     throw BadArgument("table must be [n_positions, " + std::to_string(half) + ", 2]");
   r.table = data<float>(tab);
@@ -206,21 +218,26 @@ PyTypeObject* step_tables_type = nullptr;
 
 PyObject* build_block_tables(PyObject* const* a) {
   // cached_lens, new_lens, free_slots, block_tables, block_size, n_tokens, err, out, stream
-  const at::Tensor& cached = buffer(a[0], "cached_lens", at::kInt);
+  Tensors in;
+  const at::Tensor& cached = in.buffer(a[0], "cached_lens", at::kInt);
   const int64_t n_req = cached.numel();
-  const at::Tensor& fresh = buffer(a[1], "new_lens", at::kInt);
+  const at::Tensor& fresh = in.buffer(a[1], "new_lens", at::kInt);
   if (fresh.numel() != n_req) throw BadArgument("new_lens must hold as many requests as cached_lens");
-  const at::Tensor& free_slots = buffer(a[2], "free_slots", at::kInt);
-  const at::Tensor& table = tensor(a[3], "block_tables");
+  const at::Tensor& free_slots = in.buffer(a[2], "free_slots", at::kInt);
+  const at::Tensor& table = in.tensor(a[3], "block_tables");
   const int64_t stride = table_stride(table, n_req);
   const int32_t n_tokens = integer(a[5], "n_tokens");
   if (n_tokens < 0) throw BadArgument("n_tokens must not be negative");
-  const at::Tensor& err = buffer(a[6], "err", at::kInt, 1);
+  const at::Tensor& err = in.buffer(a[6], "err", at::kInt, 1);
   const int64_t sizes[6] = {n_req + 1, n_req, n_tokens, n_tokens, n_tokens, 1};
   static const char* const names[6] = {"q_starts", "kv_lens", "token_req", "token_pos", "token_rows", "n_taken"};
-  const Where w(cached, a[8]);
   const bool makes = none(a[7]);
   if (!makes && Py_TYPE(a[7]) != step_tables_type) throw BadArgument("out must be a StepTables");
+  auto output = [&](PyObject* step, int i) {
+    return in.buffer(PyStructSequence_GetItem(step, i), names[i], i == 4 ? at::kLong : at::kInt, sizes[i]).data_ptr();
+  };
+  for (int i = 0; !makes && i < 6; ++i) output(a[7], i);
+  const Where w(cached, a[8]);
   PyObject* result = makes ? PyStructSequence_New(step_tables_type) : Py_NewRef(a[7]);
   if (!result) throw PythonError{};
   try {
@@ -230,8 +247,7 @@ PyObject* build_block_tables(PyObject* const* a) {
       PyStructSequence_SetItem(result, i, t);
     }
     void* p[6];
-    for (int i = 0; i < 6; ++i)
-      p[i] = buffer(PyStructSequence_GetItem(result, i), names[i], i == 4 ? at::kLong : at::kInt, sizes[i]).data_ptr();
+    for (int i = 0; i < 6; ++i) p[i] = output(result, i);
     check("hc_build_block_tables",
           hc_build_block_tables(data<int32_t>(cached), data<int32_t>(fresh), i32(n_req, "n_req"),
                                 integer(a[4], "block_size"), data<int32_t>(free_slots),
@@ -249,14 +265,16 @@ PyObject* build_block_tables(PyObject* const* a) {
 
 PyObject* rope_axes(PyObject* const* a) {
   // x, positions, table, pair_axis, err, pairing, inverse, out, stream
-  const at::Tensor& x = tensor(a[0], "x");
+  Tensors in;
+  const at::Tensor& x = in.tensor(a[0], "x");
   const int dtype = dtype_of(x, "x");
   const hc_rows xr = rows(x, "x", -1, -1, -1, x.scalar_type());
   const int64_t n = x.size(0), heads = x.size(1), d = x.size(2);
-  const hc_rope_axes_desc rope = rope_desc(a[1], a[2], a[3], a[5], truth(a[6]), n);
-  const at::Tensor& err = buffer(a[4], "err", at::kInt, 1);
+  const hc_rope_axes_desc rope = rope_desc(in, a[1], a[2], a[3], a[5], truth(a[6]), n);
+  const at::Tensor& err = in.buffer(a[4], "err", at::kInt, 1);
+  const at::Tensor* out = in.given(a[7], "out");
   const Where w(x, a[8]);
-  const at::Tensor y = none(a[7]) ? empty({n, heads, d}, x.scalar_type(), x, w) : tensor(a[7], "out");
+  const at::Tensor y = out ? *out : empty({n, heads, d}, x.scalar_type(), x, w);
   const hc_rows yr = rows(y, "out", n, heads, d, x.scalar_type());
   check("hc_rope_axes", hc_rope_axes(&xr, &yr, dtype, i32(n, "n_tokens"), i32(heads, "n_heads"), i32(d, "d"), &rope,
                                      data<int32_t>(err), w.stream));
@@ -265,32 +283,34 @@ PyObject* rope_axes(PyObject* const* a) {
 
 PyObject* append_int4(PyObject* const* a) {
   // q, k, v, token_rows, codes, scales, positions, table, pair_axis, err, pairing, q_out, stream, wire_scales
-  const at::Tensor& codes = buffer(a[4], "codes", at::kByte);
-  const at::Tensor& scales = tensor(a[5], "scales");
+  Tensors in;
+  const at::Tensor& codes = in.buffer(a[4], "codes", at::kByte);
+  const at::Tensor& scales = in.tensor(a[5], "scales");
   const hc_int4_cache cache = cache_desc(codes, scales);
-  const at::Tensor& k = tensor(a[1], "k");
+  const at::Tensor& k = in.tensor(a[1], "k");
   const int dtype = dtype_of(k, "k");
   const at::ScalarType st = k.scalar_type();
   const hc_rows kr = rows(k, "k", -1, cache.n_kv_heads, cache.d_head, st);
   const int64_t n = k.size(0);
-  const hc_rows vr = rows(tensor(a[2], "v"), "v", n, cache.n_kv_heads, cache.d_head, st);
-  const at::Tensor& token_rows = buffer(a[3], "token_rows", at::kLong, n);
-  const at::Tensor& err = buffer(a[9], "err", at::kInt, 1);
+  const hc_rows vr = rows(in.tensor(a[2], "v"), "v", n, cache.n_kv_heads, cache.d_head, st);
+  const at::Tensor& token_rows = in.buffer(a[3], "token_rows", at::kLong, n);
+  const at::Tensor& err = in.buffer(a[9], "err", at::kInt, 1);
+  hc_rope_axes_desc rope;
+  const bool turns = !none(a[7]);
+  if (turns) rope = rope_desc(in, a[6], a[7], a[8], a[10], false, n);
+  const at::Tensor* q = in.given(a[0], "q");
+  const at::Tensor* q_out = q ? in.given(a[11], "q_out") : nullptr;
   const Where w(k, a[12]);
   hc_rows qr{}, qo{};
   int64_t heads = 0;
   at::Tensor out;
-  const bool has_q = !none(a[0]);
+  const bool has_q = q != nullptr;
   if (has_q) {
-    const at::Tensor& q = tensor(a[0], "q");
-    qr = rows(q, "q", n, -1, cache.d_head, st);
-    heads = q.size(1);
-    out = none(a[11]) ? empty({n, heads, cache.d_head}, st, k, w) : tensor(a[11], "q_out");
+    qr = rows(*q, "q", n, -1, cache.d_head, st);
+    heads = q->size(1);
+    out = q_out ? *q_out : empty({n, heads, cache.d_head}, st, k, w);
     qo = rows(out, "q_out", n, heads, cache.d_head, st);
   }
-  hc_rope_axes_desc rope;
-  const bool turns = !none(a[7]);
-  if (turns) rope = rope_desc(a[6], a[7], a[8], a[10], false, n);
   const bool wire = truth(a[13]);
   const auto append = wire ? hc_append_int4_wire : hc_append_int4;
   check(wire ? "hc_append_int4_wire" : "hc_append_int4",
@@ -304,32 +324,35 @@ PyObject* append_int4(PyObject* const* a) {
 PyObject* attend_int4(PyObject* const* a) {
   // q, codes, scales, block_tables, q_starts, kv_lens, max_new, workspace, err, causal, window, softmax_scale,
   // out, lse, return_lse, stream
-  const at::Tensor& codes = buffer(a[1], "codes", at::kByte);
-  const at::Tensor& scales = tensor(a[2], "scales");
+  Tensors in;
+  const at::Tensor& codes = in.buffer(a[1], "codes", at::kByte);
+  const at::Tensor& scales = in.tensor(a[2], "scales");
   const hc_int4_cache cache = cache_desc(codes, scales);
-  const at::Tensor& q = tensor(a[0], "q");
+  const at::Tensor& q = in.tensor(a[0], "q");
   const int dtype = dtype_of(q, "q");
   const hc_rows qr = rows(q, "q", -1, -1, cache.d_head, q.scalar_type());
   const int64_t n = q.size(0), heads = q.size(1);
-  const at::Tensor& kv = buffer(a[5], "kv_lens", at::kInt);
+  const at::Tensor& kv = in.buffer(a[5], "kv_lens", at::kInt);
   const int64_t n_req = kv.numel();
-  const at::Tensor& table = tensor(a[3], "block_tables");
+  const at::Tensor& table = in.tensor(a[3], "block_tables");
   const int64_t stride = table_stride(table, n_req);
-  const at::Tensor& starts = buffer(a[4], "q_starts", at::kInt, n_req + 1);
-  const at::Tensor& workspace = buffer(a[7], "workspace", at::kByte);
-  const at::Tensor& err = buffer(a[8], "err", at::kInt, 1);
+  const at::Tensor& starts = in.buffer(a[4], "q_starts", at::kInt, n_req + 1);
+  const at::Tensor& workspace = in.buffer(a[7], "workspace", at::kByte);
+  const at::Tensor& err = in.buffer(a[8], "err", at::kInt, 1);
   double scale = 1.0 / std::sqrt(static_cast<double>(cache.d_head));
   if (!none(a[11])) {
     scale = PyFloat_AsDouble(a[11]);
     if (scale == -1.0 && PyErr_Occurred()) throw PythonError{};
   }
+  const at::Tensor* out_given = in.given(a[12], "out");
+  const at::Tensor* lse_given = none(a[13]) ? nullptr : &in.buffer(a[13], "lse", at::kFloat, n * heads);
   const Where w(q, a[15]);
-  const at::Tensor y = none(a[12]) ? empty({n, heads, cache.d_head}, q.scalar_type(), q, w) : tensor(a[12], "out");
+  const at::Tensor y = out_given ? *out_given : empty({n, heads, cache.d_head}, q.scalar_type(), q, w);
   const hc_rows yr = rows(y, "out", n, heads, cache.d_head, q.scalar_type());
   const bool with_lse = truth(a[14]);
   at::Tensor lse;
-  if (!none(a[13]))
-    lse = buffer(a[13], "lse", at::kFloat, n * heads);
+  if (lse_given)
+    lse = *lse_given;
   else if (with_lse)
     lse = empty({n, heads}, at::kFloat, q, w);
   check("hc_attend_int4",
