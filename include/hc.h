@@ -358,7 +358,8 @@ typedef struct hc_int4_cache {
 } hc_int4_cache;
 
 /* A tensor of rows x[token][head][0..d_head): strides in elements, the
- * channels of a row adjacent. */
+ * channels of a row adjacent.  Inputs may be broadcast (stride 0); the rows of
+ * an output do not overlap (a stride below d_head is refused). */
 typedef struct hc_rows {
   void* ptr; /* device */
   int64_t token_stride;

@@ -49,6 +49,12 @@ bool rows_ok(const hc_rows* r, int es, bool any) {
   return r && (r->ptr || !any) && aligned(r->ptr, es) && r->token_stride >= 0 && r->head_stride >= 0;
 }
 
+// Rows that are written: closer together than they are long (a broadcast tensor's), warps would write over each other.
+bool rows_apart(const hc_rows& r, int64_t n_tokens, int64_t n_heads, int64_t d) {
+  return n_tokens == 0 || n_heads == 0 ||
+         ((n_tokens == 1 || r.token_stride >= d) && (n_heads == 1 || r.head_stride >= d));
+}
+
 int check_rope(const hc_rope_axes_desc* r, int d_head, int64_t n_tokens, hc::RopeParams* out) {
   if (!r || (!r->positions && n_tokens > 0) || !r->table) return HC_ERR_INVALID_ARG;
   if (r->n_axes < 1 || r->n_axes > 8 || r->n_positions < 1) return HC_ERR_INVALID_ARG;
@@ -107,6 +113,7 @@ int append_int4(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t dt
   const bool any = n_tokens > 0;
   if (!rows_ok(k, es, any) || !rows_ok(v, es, any) || (!token_rows && any) || !err_flag) return HC_ERR_INVALID_ARG;
   if (n_q_heads > 0 && (!rows_ok(q, es, any) || !rows_ok(q_out, es, any))) return HC_ERR_INVALID_ARG;
+  if (n_q_heads > 0 && !rows_apart(*q_out, n_tokens, n_q_heads, cache->d_head)) return HC_ERR_INVALID_ARG;
   if (!aligned(token_rows, 8) || !aligned(err_flag, 4)) return HC_ERR_INVALID_ARG;
   hc::AppendParams p;
   std::memset(&p.rope, 0, sizeof p.rope);
@@ -206,6 +213,7 @@ int hc_rope_axes(const hc_rows* x, const hc_rows* y, int32_t dtype, int32_t n_to
   if (es == 0 || n_tokens < 0 || n_heads < 0 || d_head < 2 || d_head > 256) return HC_ERR_INVALID_ARG;
   const bool any = n_tokens > 0 && n_heads > 0;
   if (!rows_ok(x, es, any) || !rows_ok(y, es, any) || !err_flag || !aligned(err_flag, 4)) return HC_ERR_INVALID_ARG;
+  if (!rows_apart(*y, n_tokens, n_heads, d_head)) return HC_ERR_INVALID_ARG;
   hc::RopeAxesParams p;
   const int st = check_rope(rope, d_head, n_tokens, &p.rope);
   if (st != HC_OK) return st;
@@ -273,6 +281,7 @@ int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dty
   if (!rows_ok(q, es, n_tokens > 0) || !rows_ok(out, es, n_tokens > 0) || !err_flag || !aligned(err_flag, 4) || (lse && !aligned(lse, 4)))
     return HC_ERR_INVALID_ARG;
   if (!rows16(*q, es, n_tokens, n_q_heads) || !rows16(*out, es, n_tokens, n_q_heads)) return HC_ERR_INVALID_ARG;
+  if (!rows_apart(*out, n_tokens, n_q_heads, cache->d_head)) return HC_ERR_INVALID_ARG;
   if (!q_starts || !aligned(q_starts, 4) || (n_req > 0 && (!kv_lens || !aligned(kv_lens, 4))))
     return HC_ERR_INVALID_ARG;
   const int log2 = block_log2(cache->block_size);
