@@ -802,6 +802,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
         load_scales();
         load_slots(j + 3);
       }
+      // the last tile's waits may have run out for some lanes only: the warp leaves together, or not
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       base += tiles;
       leave_work(k);
