@@ -508,7 +508,10 @@ int hc_append_int4_wire(const hc_rows* q, const hc_rows* k, const hc_rows* v, in
  *   err_flag  : HC_DEVERR_LENGTH: a request with more queries than max_new, or
  *               than n_tokens holds, or a length outside its table: its rows of
  *               out and lse are left as they were; HC_DEVERR_SLOT: a slot
- *               outside the cache: its block is taken as zeros
+ *               outside the cache: its block is taken as zeros; HC_DEVERR_WAIT
+ *               (set by no other call): a kernel's wait for its own loads or
+ *               products ran out after two seconds, which only a defect can
+ *               cause: the results are unusable
  * Scores, softmax and sums are fp32; queries enter the products as fp16, each
  * row scaled by a power of two.  A request of few query rows (its new tokens
  * times n_q_heads / n_kv_heads; hc_attend_int4_few_rows says how many) is
