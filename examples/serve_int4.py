@@ -7,9 +7,10 @@ one encoder layer whose queries and keys turn on two axes (`rope_axes`), then
 image and text go through a two-layer decoder that keeps its keys and values
 in 4 bits: the prompt in chunks, then one token a step, all requests in one
 call per layer (`build_block_tables` once a step, `append_int4` and
-`attend_int4` in each layer).  Single-token steps replay one CUDA graph.  At
-the end each request's cache is read back (`hc_fetch_rotate_scatter`) and its
-last attention recomputed from that in float64.
+`attend_int4` in each layer).  Single-token steps replay one CUDA graph.  After
+each chunk and at the end, every request's cache is read back
+(`hc_fetch_rotate_scatter`) and the step's attention recomputed from that in
+float64.
 """
 import argparse
 import os
@@ -23,7 +24,7 @@ from kv_cache_quantization_hc_gb300 import hc, serve  # noqa: E402
 HIDDEN, HQ, H, D, B, GROUP, LAYERS, VOCAB = 256, 8, 2, 64, 16, 32, 2, 1000
 GRID = (6, 9)                              # patches of an image
 TEXT_AXES = (0,) * 16 + (1,) * 8 + (2,) * 8      # time, height and width sections of the 32 pairs
-CHUNK = 64                                 # prompt tokens of a request in one step
+CHUNK = 128                                # prompt tokens of a request in one step: 512 query rows per cache head, attended in tiles
 
 
 class Model:
@@ -105,6 +106,24 @@ def read_back(server, request, length, layer=-1):
     return k.view(-1, H, D)[:length].double(), v.view(-1, H, D)[:length].double()
 
 
+def deviation(server, lens, new):
+    """How far the last step's attention is from its cache read back, in the values' size: request r has `lens[r]`
+    tokens in the cache, `new[r]` of them from that step."""
+    q, o = server.last
+    worst, at = 0.0, 0
+    for r, (n, m) in enumerate(zip(lens, new)):
+        k, v = read_back(server, r, n)
+        hidden = torch.arange(n, device="cuda") > torch.arange(n - m, n, device="cuda")[:, None]
+        for h in range(HQ if m else 0):
+            kh, vh = k[:, h // (HQ // H)], v[:, h // (HQ // H)]
+            x = (q[at:at + m, h, None].double() * kh).sum(-1) * D ** -0.5          # [m, n]
+            p = torch.softmax(x.masked_fill(hidden, float("-inf")), -1)[..., None]
+            want, size = (p * vh).sum(1), (p * vh.abs()).sum(1)
+            worst = max(worst, float(((o[at:at + m, h].double() - want).abs() / size.clamp(min=1e-30)).max()))
+        at += m
+    return worst
+
+
 def main(n_req=5, steps=24, seed=0, say=print):
     torch.cuda.set_device(0)
     model = Model(seed)
@@ -123,10 +142,12 @@ def main(n_req=5, steps=24, seed=0, say=print):
 
     # prompts, a chunk of each at a time; a request whose prompt has ended brings nothing more
     token = torch.zeros(n_req, dtype=torch.long, device="cuda")
+    worst = 0.0
     for at in range(0, max(lens), CHUNK):
         parts = [p[at:at + CHUNK] for p in prompts]
         new = torch.tensor([len(p) for p in parts], dtype=torch.int32, device="cuda")
         token = torch.where(new > 0, server.step(torch.cat(parts), new, CHUNK), token)
+        worst = max(worst, deviation(server, [min(n, at + CHUNK) for n in lens], [len(p) for p in parts]))
 
     # one token per request and step: a graph over the same buffers
     one = torch.ones(n_req, dtype=torch.int32, device="cuda")
@@ -150,16 +171,7 @@ def main(n_req=5, steps=24, seed=0, say=print):
         tokens.append(feed.clone())
     assert int(server.err) == 0, f"device errors {int(server.err):#x}"
 
-    worst = 0.0
-    q, o = server.last
-    for r in range(n_req):
-        n = lens[r] + steps
-        k, v = read_back(server, r, n)
-        for h in range(HQ):
-            p = torch.softmax(k[:, h // (HQ // H)] @ q[r, h].double() * D ** -0.5, 0)
-            want = p @ v[:, h // (HQ // H)]
-            scale = p @ v[:, h // (HQ // H)].abs()
-            worst = max(worst, float(((o[r, h].double() - want).abs() / scale.clamp(min=1e-30)).max()))
+    worst = max(worst, deviation(server, [n + steps for n in lens], [1] * n_req))
     say(f"{n_req} requests of {min(lens)} to {max(lens)} prompt tokens, {steps} more each; "
         f"{server.caches[0][0].numel() * 2 * LAYERS} codes; attention against its cache: {worst:.2e} of the values' size")
     for r, row in enumerate(torch.stack(tokens, 1).tolist()):
