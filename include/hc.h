@@ -497,7 +497,9 @@ int hc_append_int4_wire(const hc_rows* q, const hc_rows* k, const hc_rows* v, in
  *   n_q_heads : a multiple of n_kv_heads
  *   block_tables, table_stride, table_width, q_starts, kv_lens : as
  *               hc_build_block_tables leaves them
- *   max_new   : at least every request's number of queries
+ *   max_new   : at least every request's number of queries; 0 launches nothing.
+ *               Queries of no request (a padded step: from q_starts[n_req] on)
+ *               have their rows of out and lse left as they were
  *   window    : 0 (none) or the number of positions a query sees, itself
  *               included; needs causal
  *   softmax_scale : finite
@@ -523,8 +525,9 @@ int hc_append_int4_wire(const hc_rows* q, const hc_rows* k, const hc_rows* v, in
  * lost.  So the last bits of a request's result depend on the number of
  * requests in its call, which the limit depends on; for the same call they are
  * the same every time.
- * Pieces of 8 query rows times tiles of 128 keys of a call, counted by
- * table_width, stay below 2^31. */
+ * Values are below 2^80 in magnitude (a probability may stand at 2^40 against
+ * a reference that has not moved yet).  Pieces of 8 query rows times tiles of
+ * 128 keys of a call, counted by table_width, stay below 2^31. */
 int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dtype,
                    int32_t n_tokens, int32_t n_q_heads, const hc_int4_cache* cache,
                    const uint8_t* codes, const void* scales, const int32_t* block_tables,

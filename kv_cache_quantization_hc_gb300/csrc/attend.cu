@@ -24,7 +24,8 @@
 //   by 16.
 // * Queries as fp16: each row times a power of two that brings its largest
 //   value near 2^14, so that bf16's range fits and only values below 2^-28
-//   of the row's largest lose bits.
+//   of the row's largest lose bits (2^-24 in the channels of nibbles 1 and 5,
+//   whose queries are divided by 16).
 // * Values as exact bf16 whole numbers.  Their scales go into the
 //   probabilities, and those into two bf16 (16 bits of mantissa, fp32's
 //   range) for two products: an fp16 would flush what is below 2^-39 of the
@@ -42,7 +43,7 @@
 // Bound: the cache's bytes when rows are few; in fact the issue of about 740
 // instructions per 32 keys of 128 channels, half of them the codes' conversion.
 // 64 requests of 200 to 25000 keys, 8 cache heads of 128 channels, groups of
-// 32: 107 us, 3.6 TB/s; 8 of 131000 keys, one group per head: 250 us, 4.4 TB/s.
+// 32: 107 us, 3.6 TB/s; 8 of 131000 keys, one group per head: 252 us, 4.4 TB/s.
 // Splitting the keys into equal runs rather than per request keeps every SM
 // busy whatever the lengths; copies run two tiles ahead (three: the same).
 #include <algorithm>

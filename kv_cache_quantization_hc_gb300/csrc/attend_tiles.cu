@@ -40,8 +40,9 @@
 //
 // Bound: the tensor cores (4 d flops per row and key), with the softmax's
 // exponentials and the conversion of the codes beside them.  A prompt of 8192
-// tokens, 32 query heads of 128 channels: 396 us, 1.39 PFLOP/s; the period of a
-// tile is about 2770 cycles, 1040 of them products.  Two halves of 128 rows take
+// tokens, 32 query heads of 128 channels: 400 us, 1.37 PFLOP/s, with the same
+// inputs again (415 us where they change from call to call); the period of a
+// tile is about 2800 cycles, 1040 of them products.  Two halves of 128 rows take
 // turns because a row's softmax has to stand between its two products; four
 // converting warps, as three are too slow for that (482 us against 387) and
 // seven take registers from the softmax (419).
@@ -510,9 +511,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) k_attend_tiles(const __grid_
           }
           if (masked) wait_store();
           // the reference of the row, and O with it
-          // where the row sees n keys of the tile, 128 / n times closer: n of them do not pass kMostSum either
           float ahead = kAhead;
-          if (masked) {  // n keys seen: 128 / n times closer, as n of them do not pass kMostSum either
+          if (masked) {  // n keys seen: 128 / n times lower, as n of them do not pass kMostSum either
             const int n = min(hi, kKeys) - max(lo, 0);
             if (n < kKeys) ahead -= static_cast<float>(__clz(max(n - 1, 0)) - __clz(kKeys - 1));
           }

@@ -119,7 +119,7 @@ struct AttendParams {
 int64_t attend_workspace_bytes();
 
 cudaError_t launch_block_tables(const BlockTableParams& p, cudaStream_t s);
-// `piece`: bytes moved at once (16, or the element's size).
+// `pieces16`: rows move in 16-byte pieces; element by element otherwise.
 cudaError_t launch_rope_axes(int dtype, int pairing, bool pieces16, const RopeAxesParams& p,
                              cudaStream_t s);
 cudaError_t launch_append_int4(int dtype, int d, int pairing, const AppendParams& p,

@@ -102,6 +102,8 @@ def attend_int4(q, codes, scales, block_tables, q_starts, kv_lens, max_new, work
 
     block_tables int32 [n_req, width], q_starts and kv_lens as
     build_block_tables gives them; max_new: at least the largest number of new
-    tokens of a request; softmax_scale: 1/sqrt(d) by default."""
+    tokens of a request; softmax_scale: 1/sqrt(d) by default.  Rows of tokens that
+    belong to no request (a padded step) are not written: in an `out` that the
+    call makes, they hold what the memory held."""
     return _serve.attend_int4(q, codes, scales, block_tables, q_starts, kv_lens, max_new, workspace, err, causal,
                               window, softmax_scale, out, lse, return_lse, stream)
