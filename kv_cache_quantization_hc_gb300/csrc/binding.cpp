@@ -87,6 +87,7 @@ hc_rows rows(const at::Tensor& t, const char* name, int64_t n, int64_t heads, in
                       (d >= 0 ? "=" + std::to_string(d) : "") + "], not " + c10::str(t.sizes()));
   if (t.scalar_type() != dtype)
     throw BadArgument(std::string(name) + " must be " + type_name(dtype) + ", not " + type_name(t.scalar_type()));
+  if (t.numel() == 0) return hc_rows{t.data_ptr(), 0, 0};  // whose strides may be anything
   if (t.stride(2) != 1 && t.size(2) != 1) throw BadArgument(std::string("the channels of ") + name + " must be adjacent");
   return hc_rows{t.data_ptr(), t.stride(0), t.stride(1)};
 }

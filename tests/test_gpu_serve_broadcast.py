@@ -6,6 +6,21 @@ from tests.test_gpu_serve import _err, serve, workspace  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 
+def test_no_tokens_with_any_strides(serve, workspace):  # noqa: F811
+    """A tensor without elements has strides that mean nothing."""
+    import torch
+    none = torch.empty(64, 4, 0, device="cuda").half().permute(2, 1, 0)          # [0, 4, 64]
+    assert none.shape == (0, 4, 64) and none.stride(2) != 1
+    codes, scales = serve.int4_cache(2, 2, 16, 64)
+    err, kv = _err(), none[:, :2]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    pos, table, axes = i32([]), serve.rotation_table(4, 32, 1e4), (0,) * 32
+    assert serve.rope_axes(none, pos, table, axes, err).shape == (0, 4, 64)
+    assert serve.append_int4(none, kv, kv, torch.zeros(0, dtype=torch.int64, device="cuda"), codes, scales, pos, table, axes,
+                             err).shape == (0, 4, 64)
+    assert serve.attend_int4(none, codes, scales, i32([[0]]), i32([0, 0]), i32([3]), 1, workspace, err).shape == (0, 4, 64)
+
+
 def test_broadcast_queries_and_outputs(serve, workspace):  # noqa: F811
     import torch
     n, Hq, H, d = 5, 4, 2, 64
