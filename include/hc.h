@@ -545,6 +545,122 @@ int32_t hc_attend_int4_few_rows(int32_t n_req, int32_t n_kv_heads, int32_t d_hea
  * needs (a host function; the same on every call). */
 int64_t hc_attend_int4_workspace(void);
 
+/* ------------------------------------------------------------------------
+ * Serving from the paged buffer
+ *
+ * The paged buffer that the encoders read and the fetch writes is also one to
+ * serve from: one layer's K and V pages (desc->n_layers = 1) in f16 or bf16
+ * (append: f32 too), with block tables and rows as hc_build_block_tables gives
+ * them.  Blocks fetched at a new offset, new tokens, and tokens that are
+ * computed again (hc_drift_select) lie side by side in it.
+ * ------------------------------------------------------------------------ */
+
+/* hc_append_paged: the new tokens into the pages.  Queries and keys are
+ * rotated as by hc_rope_axes (each rounded once to the pages' dtype); q goes to
+ * q_out, keys and values to row token_rows[t]: slot row / block_size, token
+ * row % block_size.  A token with row -1 (a padded step) gets its q_out but no
+ * row.
+ *
+ *   q, q_out : [n_tokens][n_q_heads][d_head], or NULL with n_q_heads = 0; q_out
+ *              may be q
+ *   k, v     : [n_tokens][n_kv_heads][d_head]; all of desc->dtype, 16-byte
+ *              aligned, strides multiples of 16 bytes
+ *   rope     : as for hc_rope_axes, inverse = 0 and rot_dim a multiple of 16;
+ *              NULL: no rotation (q and k are copied)
+ *   token_rows : device int64 [n_tokens], distinct where >= 0 (precondition)
+ *   desc     : host pointer, n_layers = 1; k_pages, v_pages: device, distinct,
+ *              written at the rows
+ *   err_flag : HC_DEVERR_SLOT: a row outside [-1, num_slots * block_size);
+ *              HC_DEVERR_POS: a position outside the table.  Such a token's
+ *              q_out and rows are left as they were. */
+int hc_append_paged(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_t n_tokens, int32_t n_q_heads,
+                    const hc_rope_axes_desc* rope, const int64_t* token_rows, const hc_paged_desc* desc, void* k_pages,
+                    void* v_pages, const hc_rows* q_out, int32_t* err_flag, void* stream);
+
+/* How hc_attend_paged scores keys and which it shows; 0 or NULL where unused. */
+typedef struct hc_attend_scores {
+  int32_t causal;             /* 1: a query sees no key behind its position */
+  int32_t window;             /* 0, or the number of positions a query sees, itself included; needs causal */
+  float softmax_scale;        /* finite */
+  float softcap;              /* 0, or the bound of |softcap * tanh(score / softcap)| */
+  const float* slopes;        /* device [n_q_heads] or NULL: the bias by distance, -slope * |position - key| */
+  const int32_t* positions;   /* device [n_tokens] or NULL: the queries' positions, not falling within a request */
+  const int32_t* prefix_lens; /* device [n_req] or NULL: keys that every query sees; needs causal */
+} hc_attend_scores;
+
+/* hc_attend_paged: attention of queries over the pages.  Request r has queries
+ * t in [q_starts[r], q_starts[r+1]) and kv_lens[r] keys.  Query i of n has
+ * position p = positions[t], or kv_lens[r] - n + i (the last ones) without
+ * positions.  It sees the keys j with 0 <= j < kv_lens[r], j <= p or
+ * j < prefix_lens[r] if causal, j > p - window if window > 0.  For query head h
+ * and cache head h / (n_q_heads / n_kv_heads):
+ *   s_j = softmax_scale * sum_c q[t][h][c] * K[j][c]
+ *   x_j = (softcap > 0 ? softcap * tanh(s_j / softcap) : s_j) - slopes[h] * |p - j|
+ *   lse = log sum_j exp(x_j),  out[t][h] = sum_j exp(x_j - lse) * V[j]
+ * A query that sees no key gets out = 0 and lse = -inf.  Rows that no query of
+ * the call's request sees are not read into the result, whatever they hold;
+ * keys and values that some query sees are finite.
+ *
+ *   q, out    : [n_tokens][n_q_heads][d_head] of desc->dtype (HC_F16 or HC_BF16),
+ *               16-byte aligned, strides multiples of 16 bytes; finite
+ *   lse       : device f32 [n_tokens][n_q_heads] or NULL
+ *   n_q_heads : a multiple of n_kv_heads
+ *   desc      : host pointer, n_layers = 1; k_pages, v_pages: device
+ *   block_tables, table_stride, table_width, q_starts, kv_lens : as
+ *               hc_build_block_tables leaves them
+ *   max_new   : at least every request's number of queries; 0 launches nothing.
+ *               Queries of no request (from q_starts[n_req] on) have their rows
+ *               of out and lse left as they were
+ *   scores    : host pointer, read during the call only.  A position below 0 sees
+ *               no key but the prefix's, one past the keys sees them all; any
+ *               negative one counts as -1 for the bias
+ *   workspace : device, 256-byte aligned, zero before its first use; every call
+ *               leaves it ready for the next, of hc_attend_int4 too.  Calls that
+ *               may run at the same time need workspaces of their own.
+ *   workspace_bytes : hc_attend_paged_workspace() at least
+ *   err_flag  : HC_DEVERR_LENGTH and HC_DEVERR_SLOT as for hc_attend_int4 (a block
+ *               whose slot does not exist is taken as zeros); HC_DEVERR_POS: a
+ *               request's positions fall: its results are unusable;
+ *               HC_DEVERR_WAIT as for hc_attend_int4
+ * Scores, softmax and sums are fp32.  A request of few query rows (its queries
+ * times n_q_heads / n_kv_heads; hc_attend_paged_few_rows says how many) has its
+ * keys split over the GPU and probabilities of 16 (bf16) or 22 bits (f16); one
+ * of more rows is attended in tiles of 256 rows with probabilities in the pages'
+ * dtype.  So the last bits of a request's result depend on the number of
+ * requests in its call, which the limit depends on; for the same call they are
+ * the same every time.  In f16 what is below 2^-33 of a row's largest
+ * probability is lost.  Values are below 2^80 in magnitude. */
+int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_tokens, int32_t n_q_heads,
+                    const hc_paged_desc* desc, const void* k_pages, const void* v_pages, const int32_t* block_tables,
+                    int64_t table_stride, int32_t table_width, const int32_t* q_starts, const int32_t* kv_lens,
+                    int32_t n_req, int32_t max_new, const hc_attend_scores* scores, void* workspace,
+                    int64_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* hc_attend_paged_few_rows: the largest number of query rows of a request that
+ * an hc_attend_paged call of n_req requests takes as few (a host function; see
+ * there), or a negative hc_status. */
+int32_t hc_attend_paged_few_rows(int32_t n_req, int32_t n_kv_heads, int32_t d_head);
+
+/* hc_attend_paged_workspace: bytes of workspace that any hc_attend_paged call
+ * needs (a host function; the same on every call). */
+int64_t hc_attend_paged_workspace(void);
+
+/* hc_merge_attention: two attention results of the same queries over different
+ * keys (a history in the 4-bit cache, recent tokens in the pages) joined:
+ *   top = max(lse_a, lse_b),  w = exp(lse - top),  lse = top + log(w_a + w_b),
+ *   out = (w_a * out_a + w_b * out_b) / (w_a + w_b)
+ * in fp32.  A side whose lse is -inf counts for nothing, whatever its row holds;
+ * both: out = 0 and lse = -inf.
+ *
+ *   out_a, out_b, out : [n_tokens][n_heads][d_head] of dtype (f32, f16, bf16),
+ *               16-byte aligned, strides multiples of 16 bytes, d_head 64 or 128;
+ *               out may be out_a or out_b, and overlaps neither otherwise
+ *   lse_a, lse_b : device f32 [n_tokens][n_heads], below +inf
+ *   lse       : device f32 [n_tokens][n_heads] or NULL; may be lse_a or lse_b */
+int hc_merge_attention(const hc_rows* out_a, const float* lse_a, const hc_rows* out_b, const float* lse_b,
+                       const hc_rows* out, float* lse, int32_t dtype, int32_t n_tokens, int32_t n_heads, int32_t d_head,
+                       void* stream);
+
 /* Human-readable name of an hc_status value (static string, never NULL). */
 const char* hc_status_string(int32_t status);
 

@@ -49,6 +49,7 @@
 #include <algorithm>
 
 #include "attend_common.cuh"
+#include "warp_mma.cuh"
 
 namespace hc {
 namespace {
@@ -69,32 +70,11 @@ constexpr int kMaxRows = 16;                       // rows of a piece
 constexpr float kMostSum = 0x1p40f;                // of a lane's probabilities against a reference
 constexpr int kPartialFloats = kMaxRows * (128 + 2);
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes));
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
                                         const float* c) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Signed codes of nibbles 0 and 4 of w as bf16: 128 + u in the mantissa,
 // u = code + 8, less 136.
@@ -107,16 +87,6 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
   memcpy(&u, &h, 4);
   return u;
 }
-// Two fp32 as pairs of bf16, high and low: the upper halves as they stand,
-// and what is left of them rounded to bf16: 16 bits in all.
-__device__ __forceinline__ void split_bf16(float2 v, uint32_t& high, uint32_t& low) {
-  const uint32_t ux = __float_as_uint(v.x), uy = __float_as_uint(v.y);
-  high = __byte_perm(ux, uy, 0x7632);
-  const float2 kept = make_float2(__uint_as_float(high * 65536u), __uint_as_float(high & 0xffff0000u));
-  const __nv_bfloat162 rest = __float22bfloat162_rn(__ffma2_rn(kept, make_float2(-1.f, -1.f), v));
-  memcpy(&low, &rest, 4);
-}
-
 template <int kRows>
 __device__ __forceinline__ int request_units(const AttendParams& p, const Request& q) {
   int units = 0;

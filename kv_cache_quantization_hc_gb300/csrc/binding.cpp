@@ -154,6 +154,26 @@ hc_int4_cache cache_desc(const at::Tensor& codes, const at::Tensor& scales) {
                        i32(d / groups, "group"),        dtype_of(scales, "scales")};
 }
 
+// One layer's pages [num_slots, B, H, d], each slot's rows adjacent.
+hc_paged_desc pages_desc(const at::Tensor& k, const at::Tensor& v) {
+  if (k.dim() != 4 || v.sizes() != k.sizes()) throw BadArgument("k_pages and v_pages must both be [num_slots, B, H, d]");
+  if (v.scalar_type() != k.scalar_type())
+    throw BadArgument(std::string("v_pages must be ") + type_name(k.scalar_type()) + ", not " + type_name(v.scalar_type()));
+  const int64_t S = k.size(0), B = k.size(1), H = k.size(2), d = k.size(3);
+  for (const at::Tensor* t : {&k, &v})
+    if ((d > 1 && t->stride(3) != 1) || (H > 1 && t->stride(2) != d) || (B > 1 && t->stride(1) != H * d))
+      throw BadArgument("each slot of k_pages and v_pages must be a contiguous [B, H, d] block");
+  if (S > 1 && v.stride(0) != k.stride(0)) throw BadArgument("k_pages and v_pages must have the same strides");
+  return hc_paged_desc{1, i32(H, "H"), i32(d, "d"), i32(B, "B"), i32(S, "num_slots"), dtype_of(k, "k_pages"),
+                       S > 1 ? k.stride(0) : B * H * d, 0};
+}
+
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw PythonError{};
+  return v;
+}
+
 // Block tables [n_req, width], each row adjacent.
 int64_t table_stride(const at::Tensor& t, int64_t n_req) {
   if (t.dim() != 2 || t.size(0) != n_req || t.scalar_type() != at::kInt || (t.size(1) > 1 && t.stride(1) != 1))
@@ -372,6 +392,121 @@ PyObject* attend_int4(PyObject* const* a) {
   return both;
 }
 
+PyObject* append_paged(PyObject* const* a) {
+  // q, k, v, token_rows, k_pages, v_pages, positions, table, pair_axis, err, pairing, q_out, stream
+  Tensors in;
+  const at::Tensor& k_pages = in.tensor(a[4], "k_pages");
+  const at::Tensor& v_pages = in.tensor(a[5], "v_pages");
+  const hc_paged_desc desc = pages_desc(k_pages, v_pages);
+  const at::ScalarType st = k_pages.scalar_type();
+  const at::Tensor& k = in.tensor(a[1], "k");
+  const hc_rows kr = rows(k, "k", -1, desc.n_kv_heads, desc.d_head, st);
+  const int64_t n = k.size(0);
+  const hc_rows vr = rows(in.tensor(a[2], "v"), "v", n, desc.n_kv_heads, desc.d_head, st);
+  const at::Tensor& token_rows = in.buffer(a[3], "token_rows", at::kLong, n);
+  const at::Tensor& err = in.buffer(a[9], "err", at::kInt, 1);
+  hc_rope_axes_desc rope;
+  const bool turns = !none(a[7]);
+  if (turns) rope = rope_desc(in, a[6], a[7], a[8], a[10], false, n);
+  const at::Tensor* q = in.given(a[0], "q");
+  const at::Tensor* q_out = q ? in.given(a[11], "q_out") : nullptr;
+  const Where w(k, a[12]);
+  hc_rows qr{}, qo{};
+  int64_t heads = 0;
+  at::Tensor out;
+  if (q) {
+    qr = rows(*q, "q", n, -1, desc.d_head, st);
+    heads = q->size(1);
+    out = q_out ? *q_out : empty({n, heads, desc.d_head}, st, k, w);
+    qo = rows(out, "q_out", n, heads, desc.d_head, st);
+  }
+  check("hc_append_paged",
+        hc_append_paged(q ? &qr : nullptr, &kr, &vr, i32(n, "n_tokens"), i32(heads, "heads"), turns ? &rope : nullptr,
+                        data<int64_t>(token_rows), &desc, k_pages.data_ptr(), v_pages.data_ptr(), q ? &qo : nullptr,
+                        data<int32_t>(err), w.stream));
+  if (!q) Py_RETURN_NONE;
+  return none(a[11]) ? THPVariable_Wrap(out) : Py_NewRef(a[11]);
+}
+
+PyObject* attend_paged(PyObject* const* a) {
+  // q, k_pages, v_pages, block_tables, q_starts, kv_lens, max_new, workspace, err, causal, window, softmax_scale,
+  // softcap, slopes, positions, prefix_lens, out, lse, return_lse, stream
+  Tensors in;
+  const at::Tensor& k_pages = in.tensor(a[1], "k_pages");
+  const at::Tensor& v_pages = in.tensor(a[2], "v_pages");
+  const hc_paged_desc desc = pages_desc(k_pages, v_pages);
+  const at::Tensor& q = in.tensor(a[0], "q");
+  const hc_rows qr = rows(q, "q", -1, -1, desc.d_head, k_pages.scalar_type());
+  const int64_t n = q.size(0), heads = q.size(1);
+  const at::Tensor& kv = in.buffer(a[5], "kv_lens", at::kInt);
+  const int64_t n_req = kv.numel();
+  const at::Tensor& table = in.tensor(a[3], "block_tables");
+  const int64_t stride = table_stride(table, n_req);
+  const at::Tensor& starts = in.buffer(a[4], "q_starts", at::kInt, n_req + 1);
+  const at::Tensor& workspace = in.buffer(a[7], "workspace", at::kByte);
+  const at::Tensor& err = in.buffer(a[8], "err", at::kInt, 1);
+  hc_attend_scores scores;
+  std::memset(&scores, 0, sizeof scores);
+  scores.causal = truth(a[9]);
+  scores.window = integer(a[10], "window");
+  scores.softmax_scale = static_cast<float>(none(a[11]) ? 1.0 / std::sqrt(static_cast<double>(desc.d_head)) : number(a[11]));
+  scores.softcap = static_cast<float>(number(a[12]));
+  if (!none(a[13])) scores.slopes = data<float>(in.buffer(a[13], "slopes", at::kFloat, heads));
+  if (!none(a[14])) scores.positions = data<int32_t>(in.buffer(a[14], "positions", at::kInt, n));
+  if (!none(a[15])) scores.prefix_lens = data<int32_t>(in.buffer(a[15], "prefix_lens", at::kInt, n_req));
+  const at::Tensor* out_given = in.given(a[16], "out");
+  const at::Tensor* lse_given = none(a[17]) ? nullptr : &in.buffer(a[17], "lse", at::kFloat, n * heads);
+  const Where w(q, a[19]);
+  const at::Tensor y = out_given ? *out_given : empty({n, heads, desc.d_head}, q.scalar_type(), q, w);
+  const hc_rows yr = rows(y, "out", n, heads, desc.d_head, q.scalar_type());
+  const bool with_lse = truth(a[18]);
+  at::Tensor lse;
+  if (lse_given)
+    lse = *lse_given;
+  else if (with_lse)
+    lse = empty({n, heads}, at::kFloat, q, w);
+  check("hc_attend_paged",
+        hc_attend_paged(&qr, &yr, lse.defined() ? data<float>(lse) : nullptr, i32(n, "n_tokens"), i32(heads, "heads"),
+                        &desc, k_pages.data_ptr(), v_pages.data_ptr(), data<int32_t>(table), stride,
+                        i32(table.size(1), "width"), data<int32_t>(starts), data<int32_t>(kv), i32(n_req, "n_req"),
+                        integer(a[6], "max_new"), &scores, workspace.data_ptr(), workspace.numel(), data<int32_t>(err),
+                        w.stream));
+  PyObject* out = none(a[16]) ? THPVariable_Wrap(y) : Py_NewRef(a[16]);
+  if (!with_lse) return out;
+  PyObject* l = none(a[17]) ? THPVariable_Wrap(lse) : Py_NewRef(a[17]);
+  PyObject* both = out && l ? PyTuple_Pack(2, out, l) : nullptr;
+  Py_XDECREF(out);
+  Py_XDECREF(l);
+  return both;
+}
+
+PyObject* merge_attention(PyObject* const* a) {
+  // out_a, lse_a, out_b, lse_b, out, lse, stream
+  Tensors in;
+  const at::Tensor& x = in.tensor(a[0], "out_a");
+  const int dtype = dtype_of(x, "out_a");
+  const hc_rows xr = rows(x, "out_a", -1, -1, -1, x.scalar_type());
+  const int64_t n = x.size(0), heads = x.size(1), d = x.size(2);
+  const at::Tensor& lse_a = in.buffer(a[1], "lse_a", at::kFloat, n * heads);
+  const hc_rows yr = rows(in.tensor(a[2], "out_b"), "out_b", n, heads, d, x.scalar_type());
+  const at::Tensor& lse_b = in.buffer(a[3], "lse_b", at::kFloat, n * heads);
+  const at::Tensor* out_given = in.given(a[4], "out");
+  const at::Tensor* lse_given = none(a[5]) ? nullptr : &in.buffer(a[5], "lse", at::kFloat, n * heads);
+  const Where w(x, a[6]);
+  const at::Tensor out = out_given ? *out_given : empty({n, heads, d}, x.scalar_type(), x, w);
+  const hc_rows zr = rows(out, "out", n, heads, d, x.scalar_type());
+  const at::Tensor lse = lse_given ? *lse_given : empty({n, heads}, at::kFloat, x, w);
+  check("hc_merge_attention",
+        hc_merge_attention(&xr, data<float>(lse_a), &yr, data<float>(lse_b), &zr, data<float>(lse), dtype,
+                           i32(n, "n_tokens"), i32(heads, "heads"), i32(d, "d"), w.stream));
+  PyObject* o = none(a[4]) ? THPVariable_Wrap(out) : Py_NewRef(a[4]);
+  PyObject* l = none(a[5]) ? THPVariable_Wrap(lse) : Py_NewRef(a[5]);
+  PyObject* both = o && l ? PyTuple_Pack(2, o, l) : nullptr;
+  Py_XDECREF(o);
+  Py_XDECREF(l);
+  return both;
+}
+
 // No C++ exception leaves a call.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -399,6 +534,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<build_block_tables, 9>("build_block_tables"), method<rope_axes, 9>("rope_axes"),
                          method<append_int4, 14>("append_int4"), method<attend_int4, 16>("attend_int4"),
+                         method<append_paged, 13>("append_paged"), method<attend_paged, 20>("attend_paged"),
+                         method<merge_attention, 7>("merge_attention"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve", "Native binding of the serving calls (see serve.py).", -1,

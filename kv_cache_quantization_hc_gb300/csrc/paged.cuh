@@ -1,0 +1,75 @@
+// Declarations of the serving operators over the 16-bit paged buffer (append,
+// attention, merge), shared by their kernels and the C ABI.
+#pragma once
+
+#include "serve.cuh"
+
+namespace hc {
+
+struct AppendPagedParams {
+  RopeParams rope;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_pages;
+  void* v_pages;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+  int64_t slot_stride;  // elements
+  int32_t n_tokens, n_q_heads, H, d, B_log2;
+  int32_t heads_per_warp, q_parts, kv_parts;
+  FastDivmod parts, items_per_row;  // warps of a token; pieces of a row
+  const int64_t* token_rows;
+  int64_t n_rows;  // num_slots * block_size
+  int32_t* err;
+};
+
+struct AttendPagedParams {
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_token, q_head, o_token, o_head;
+  const void* k_pages;
+  const void* v_pages;
+  int64_t slot_stride;  // elements
+  const int32_t* tables;
+  int64_t table_stride;
+  const int32_t* q_starts;
+  const int32_t* kv_lens;
+  const int32_t* positions;    // null: a request's queries are its last positions
+  const int32_t* prefix_lens;  // null: none
+  const float* slopes;         // null: none
+  int32_t n_req, n_tokens, max_new, table_width, num_slots;
+  int32_t H, G, B_log2, bf16, causal, window;
+  FastDivmod by_group, by_heads;  // division by G, by H
+  float scale_log2;     // softmax_scale * log2(e)
+  float cap_in, cap_log2;  // softmax_scale / cap and cap * log2(e); cap_log2 0: no cap
+  int32_t rows_above;   // requests with more query rows than this go to k_attend_paged_tiles
+  int32_t piece_cost;   // of the rows kernel: what a piece's start and end take, in tiles
+  uint8_t* workspace;
+  int32_t* err;
+};
+
+struct MergeParams {
+  const void* a;
+  const void* b;
+  void* out;
+  const float* lse_a;
+  const float* lse_b;
+  float* lse;
+  int64_t a_token, a_head, b_token, b_head, o_token, o_head;
+  int32_t n_tokens, n_heads, d;
+  FastDivmod by_heads;
+};
+
+// Bytes of the attention's workspace: one counter per CTA of the largest
+// grid, then two partial results per CTA.
+int64_t attend_paged_workspace_bytes();
+
+cudaError_t launch_append_paged(int dtype, int pairing, const AppendPagedParams& p, cudaStream_t s);
+// The requests with at most p.rows_above query rows, and those with more.
+cudaError_t launch_attend_paged_rows(int d, const AttendPagedParams& p, cudaStream_t s);
+cudaError_t launch_attend_paged_tiles(int d, const AttendPagedParams& p, cudaStream_t s);
+cudaError_t launch_merge(int dtype, const MergeParams& p, cudaStream_t s);
+
+}  // namespace hc

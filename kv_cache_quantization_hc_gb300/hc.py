@@ -56,6 +56,12 @@ class hc_rope_axes_desc(ctypes.Structure):
                 ("pair_axis", ctypes.c_uint8 * 128)]
 
 
+class hc_attend_scores(ctypes.Structure):
+    _fields_ = [("causal", ctypes.c_int32), ("window", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
+
+
 _LIB = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -93,8 +99,17 @@ def lib():
         L.hc_attend_int4.argtypes = [rows_p, rows_p, _P, _I32, _I32, _I32, cache_p, _P, _P, _P, _I64,
                                      _I32, _P, _P, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _I64, _P,
                                      _P]
+        desc_p, scores_p = ctypes.POINTER(hc_paged_desc), ctypes.POINTER(hc_attend_scores)
+        L.hc_append_paged.argtypes = [rows_p, rows_p, rows_p, _I32, _I32, rope_p, _P, desc_p, _P, _P, rows_p, _P, _P]
+        L.hc_attend_paged.argtypes = [rows_p, rows_p, _P, _I32, _I32, desc_p, _P, _P, _P, _I64, _I32, _P, _P, _I32,
+                                      _I32, scores_p, _P, _I64, _P, _P]
+        L.hc_merge_attention.argtypes = [rows_p, _P, rows_p, _P, rows_p, _P, _I32, _I32, _I32, _I32, _P]
+        L.hc_attend_paged_few_rows.argtypes = [_I32, _I32, _I32]
+        L.hc_attend_paged_few_rows.restype = _I32
+        L.hc_attend_paged_workspace.argtypes = []
+        L.hc_attend_paged_workspace.restype = _I64
         for fn in ("hc_build_block_tables", "hc_rope_axes", "hc_append_int4", "hc_append_int4_wire",
-                   "hc_attend_int4"):
+                   "hc_attend_int4", "hc_append_paged", "hc_attend_paged", "hc_merge_attention"):
             getattr(L, fn).restype = ctypes.c_int
         L.hc_attend_int4_few_rows.argtypes = [_I32, _I32, _I32]
         L.hc_attend_int4_few_rows.restype = _I32

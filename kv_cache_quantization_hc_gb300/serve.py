@@ -1,4 +1,4 @@
-"""Serving from the 4-bit cache: the calls of include/hc.h on torch tensors.
+"""Serving from the 4-bit cache and from the paged buffer: the calls of include/hc.h on torch tensors.
 
 A layer's cache is an INT4 wire over its slots, codes [num_slots, 2, H, B,
 d/2] and scales [num_slots, 2, H, B, d/group] (`int4_cache` makes one; the
@@ -9,6 +9,11 @@ a decoder:
   per layer:
     q = append_int4(q, k, v, step.token_rows, codes, scales, positions, table, pair_axis, err)
     o = attend_int4(q, codes, scales, tables, step.q_starts, step.kv_lens, max_new, workspace, err)
+
+The paged buffer that the fetch writes is one to serve from too: K and V pages
+[num_slots, B, H, d] in 16 bits (`paged_cache` makes them), with the same block
+tables, through append_paged and attend_paged.  Results over both are joined by
+merge_attention.
 
 Every call takes its tensors on the GPU, enqueues its kernel on `stream`
 (default: torch's current stream; else a torch.cuda.Stream or a cudaStream_t as
@@ -50,9 +55,10 @@ def rotation_table(n_positions, pairs, rope_base, device="cuda", stream=None):
 
 
 def attend_workspace(device="cuda"):
-    """A workspace for attend_int4 (zeroed; each call leaves it ready for the next).
-    Calls that may run at the same time need one each."""
-    return torch.zeros(hc.lib().hc_attend_int4_workspace(), dtype=torch.uint8, device=device)
+    """A workspace for attend_int4 and attend_paged (zeroed; each call leaves it
+    ready for the next).  Calls that may run at the same time need one each."""
+    size = max(hc.lib().hc_attend_int4_workspace(), hc.lib().hc_attend_paged_workspace())
+    return torch.zeros(size, dtype=torch.uint8, device=device)
 
 
 def attend_few_rows(n_req, n_kv_heads, d):
@@ -107,3 +113,50 @@ def attend_int4(q, codes, scales, block_tables, q_starts, kv_lens, max_new, work
     call makes, they hold what the memory held."""
     return _serve.attend_int4(q, codes, scales, block_tables, q_starts, kv_lens, max_new, workspace, err, causal,
                               window, softmax_scale, out, lse, return_lse, stream)
+
+
+def paged_cache(num_slots, H, B, d, dtype=torch.bfloat16, n_layers=None, device="cuda"):
+    """Empty K and V pages [num_slots, B, H, d]; with n_layers, one leading dimension more."""
+    lead = () if n_layers is None else (n_layers,)
+    return tuple(torch.zeros(lead + (num_slots, B, H, d), dtype=dtype, device=device) for _ in range(2))
+
+
+def attend_paged_few_rows(n_req, n_kv_heads, d):
+    """hc_attend_paged_few_rows: attend_few_rows for attend_paged."""
+    rows = hc.lib().hc_attend_paged_few_rows(n_req, n_kv_heads, d)
+    if rows < 0:
+        hc._check("hc_attend_paged_few_rows", rows)
+    return rows
+
+
+def append_paged(q, k, v, token_rows, k_pages, v_pages, positions, table, pair_axis, err, pairing="half_split",
+                 q_out=None, stream=None):
+    """hc_append_paged: k, v [n_tokens, H, d] into the pages [num_slots, B, H, d]
+    at token_rows (int64), keys rotated; returns the rotated q (None for q
+    None).  All of the pages' dtype.  table None: no rotation (positions and
+    pair_axis unused)."""
+    return _serve.append_paged(q, k, v, token_rows, k_pages, v_pages, positions, table, pair_axis, err, pairing, q_out,
+                               stream)
+
+
+def attend_paged(q, k_pages, v_pages, block_tables, q_starts, kv_lens, max_new, workspace, err, causal=True, window=0,
+                 softmax_scale=None, softcap=0.0, slopes=None, positions=None, prefix_lens=None, out=None, lse=None,
+                 return_lse=False, stream=None):
+    """hc_attend_paged: attention of q [n_tokens, Hq, d] over pages [num_slots,
+    B, H, d] of the same dtype (float16 or bfloat16); returns out, or (out, lse)
+    with return_lse.
+
+    block_tables, q_starts, kv_lens, max_new, softmax_scale and padded rows as
+    for attend_int4.  softcap > 0: scores softcap * tanh(score / softcap).
+    slopes (float32 [Hq]): less slope * distance.  positions (int32 [n_tokens],
+    not falling within a request): queries at these positions instead of the
+    last ones.  prefix_lens (int32 [n_req]): keys that every query sees."""
+    return _serve.attend_paged(q, k_pages, v_pages, block_tables, q_starts, kv_lens, max_new, workspace, err, causal,
+                               window, softmax_scale, softcap, slopes, positions, prefix_lens, out, lse, return_lse,
+                               stream)
+
+
+def merge_attention(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None):
+    """hc_merge_attention: (out, lse) of the keys of both results; out may be
+    out_a or out_b, and lse likewise."""
+    return _serve.merge_attention(out_a, lse_a, out_b, lse_b, out, lse, stream)
