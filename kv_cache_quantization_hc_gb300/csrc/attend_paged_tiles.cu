@@ -96,11 +96,14 @@ struct TileShared {
 __device__ __forceinline__ void mbar_expect(uint64_t* b, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mbar_addr(b)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint64_t* b, int channel, int head,
-                                         int token, int slot) {
+// Issued by one thread, like the products, while the whole warp goes along.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint64_t* b, int channel, int head, int slot,
+                                         uint32_t leader) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(map), "r"(mbar_addr(b)), "r"(channel), "r"(head), "r"(token), "r"(slot)
+      "{\n.reg .pred q;\nsetp.ne.u32 q, %7, 0;\n"
+      "@q cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];\n}" ::"r"(
+          dst),
+      "l"(map), "r"(mbar_addr(b)), "r"(channel), "r"(head), "r"(0), "r"(slot), "r"(leader)
       : "memory");
 }
 
@@ -443,11 +446,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
     }
   } else if (warp == kLoadWarp) {
     // ================================================== keys and values
-    // A lane per box: 64 channels of the tile's rows in one slot.  Rows of a slot that does not exist, or that no
-    // row sees, come from past the buffer's end, where the copy finds zeros.
-    const int block = min(1 << p.B_log2, kKeys), slots = kKeys / block;
-    const int at = lane / (D / 64), channels = lane % (D / 64);
-    const bool copies = lane < slots * (D / 64);
+    // A box is 64 channels of the tile's rows in one slot; lane i looks slot i up.  Rows of a slot that does not
+    // exist, or that no row sees, come from past the buffer's end, where the copy finds zeros.
+    const int block = 1 << p.B_log2, slots = kKeys >> p.B_log2;
+    const uint32_t leader = elect_leader(), tiles_at = __shfl_sync(0xffffffffu, smem_addr(dyn), 0);
     // bit st: the parity of v_edge[st]'s next use, and whether the last values into stage st went by it
     uint32_t edges = 0, by_edge = 0;
     int k_sent = 0, v_sent = 0;  // tiles on their way so far
@@ -458,8 +460,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
       const int32_t* const table = p.tables + static_cast<int64_t>(work.r) * p.table_stride;
       auto slot_of = [&](int j) {
         int slot = p.num_slots;
-        if (copies && j < tiles) {
-          const int key = tile_key(vis, j) + at * block;
+        if (lane < slots && j < tiles) {
+          const int key = tile_key(vis, j) + lane * block;
           if (key < vis.hi && key + block > vis.lo) {
             slot = __ldg(table + (key >> p.B_log2));
             if (static_cast<uint32_t>(slot) >= static_cast<uint32_t>(p.num_slots)) {
@@ -470,7 +472,16 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         }
         return slot;
       };
-      const uint32_t dst = smem_addr(dyn) + channels * kBlockBytes + at * block * 128;
+      auto load = [&](uint32_t dst, const CUtensorMap* map, uint64_t* full, int slot) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= slots) break;
+          const int s = __shfl_sync(0xffffffffu, slot, i);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load(dst + c * kBlockBytes + i * (block * 128), map, full, c * 64, head, s, leader);
+        }
+      };
       int slot = slot_of(0);
       for (int j = 0; j < tiles; ++j) {
         const int st = (base + j) & 1, round = (base + j) >> 1;
@@ -480,7 +491,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         if (lane == 0) mbar_expect(&sh.k_full[st], Smem::kTileBytes);
         __syncwarp();
         ++k_sent;
-        if (copies) tma_load(dst + Smem::kK + st * Smem::kTileBytes, &k_map, &sh.k_full[st], channels * 64, head, 0, slot);
+        load(tiles_at + Smem::kK + st * Smem::kTileBytes, &k_map, &sh.k_full[st], slot);
         if (base + j >= 2) ok = mbar_wait(&sh.v_empty[st], (round - 1) & 1, &sh.dead);
         if (!__all_sync(0xffffffffu, ok)) break;
         const bool edge = at_edge(vis, tile_key(vis, j));
@@ -490,7 +501,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         ++v_sent;
         by_edge = (by_edge & ~(1u << st)) | static_cast<uint32_t>(edge) << st;
         if (edge) edges ^= 1u << st;
-        if (copies) tma_load(dst + Smem::kV + st * Smem::kTileBytes, &v_map, full, channels * 64, head, 0, slot);
+        load(tiles_at + Smem::kV + st * Smem::kTileBytes, &v_map, full, slot);
         slot = next;
       }
       ok = __all_sync(0xffffffffu, ok);
