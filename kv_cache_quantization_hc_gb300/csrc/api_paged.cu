@@ -37,6 +37,8 @@ int rows_for_pieces(int64_t n_req, int64_t heads, int d_head) {
   return kMost;
 }
 
+int64_t workspace_bytes_needed() { return hc::attend_paged_rows_bytes() + 256; }
+
 }  // namespace
 
 extern "C" {
@@ -104,7 +106,7 @@ int32_t hc_attend_paged_few_rows(int32_t n_req, int32_t n_kv_heads, int32_t d_he
   return rows_for_pieces(n_req, n_kv_heads, d_head);
 }
 
-int64_t hc_attend_paged_workspace(void) { return hc::attend_paged_workspace_bytes(); }
+int64_t hc_attend_paged_workspace(void) { return workspace_bytes_needed(); }
 
 int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_tokens, int32_t n_q_heads,
                     const hc_paged_desc* desc, const void* k_pages, const void* v_pages, const int32_t* block_tables,
@@ -134,7 +136,7 @@ int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_
     return HC_ERR_INVALID_ARG;
   if (!aligned(scores->slopes, 4) || !aligned(scores->positions, 4) || !aligned(scores->prefix_lens, 4))
     return HC_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < hc::attend_paged_workspace_bytes())
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < workspace_bytes_needed())
     return HC_ERR_INVALID_ARG;
   const int G = n_q_heads / H;
   // rows of a request, pieces of 8 rows times tiles of 64 keys, and tiles of 256 rows are counted in 32 bits
@@ -181,7 +183,9 @@ int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_
   p.scale_log2 = scores->softmax_scale * 1.4426950408889634f;
   p.cap_in = cap_in;
   p.cap_log2 = cap_log2;
+  p.out32 = aligned(out->ptr, 32) && out->token_stride % 16 == 0 && out->head_stride % 16 == 0;
   p.workspace = static_cast<uint8_t*>(workspace);
+  p.tiles_taken = reinterpret_cast<int32_t*>(p.workspace + hc::attend_paged_rows_bytes());
   p.err = err_flag;
   p.rows_above = rows_above;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -578,7 +578,7 @@ cudaError_t launch_type(const AttendPagedParams& p, cudaStream_t s) {
 
 }  // namespace
 
-int64_t attend_paged_workspace_bytes() {
+int64_t attend_paged_rows_bytes() {
   return kMaxCtas * static_cast<int64_t>(sizeof(int32_t)) +
          static_cast<int64_t>(kMaxCtas) * 2 * kPartialFloats * static_cast<int64_t>(sizeof(float));
 }

@@ -37,10 +37,12 @@
 #include <algorithm>
 #include <climits>
 #include <cuda.h>
+#include <type_traits>
 
 #include "attend_paged_common.cuh"
 #include "mbarrier.cuh"
 #include "tcgen05.cuh"
+#include "warp_mma.cuh"
 
 namespace hc {
 namespace {
@@ -48,28 +50,42 @@ namespace {
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kHalf = 128;       // rows of a half
 constexpr int kRowsTile = 2 * kHalf;
-constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kProductWarp = 9, kWorkWarp = 10, kEdgeWarp = 11;
-constexpr int kThreadsTiles = 12 * 32;
-constexpr int kWorksAhead = 4;   // found before they are begun
+constexpr int kSoftmaxWarps = 8, kLoadWarp = 8, kProductWarp = 9, kWorkWarp = 10, kEdgeWarp = 11, kQueryWarp = 12;
+constexpr int kThreadsTiles = 16 * 32;
+// Registers of a thread: 128 at launch, shared out anew between the softmax's
+// 256 threads and the others (256 * 208 + 256 * 48 = 512 * 128).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 48;
+constexpr int kWorksAhead = 2;   // the one in hand and the next
+// The next work is taken when this many tiles of the one in hand are not loaded yet: late, as who is done first takes
+// the next, but not so late that it is waited for.
+constexpr int kDue = 4;
 constexpr int kBlockBytes = kKeys * 128;  // 128 rows of 64 channels, swizzled in 128-byte rows
+
+enum Scores { kPlain, kCapped, kBiased };  // kBiased: with or without a cap
 
 // p = 2^(x - m + kTop); see above.
 template <bool kBf16>
 struct Softmax;
 template <>
 struct Softmax<true> {
-  static constexpr float kTop = 0.f, kMoveAt = 0.f, kAhead = 0.f, kMostSum = 0x1p40f;
+  static constexpr float kTop = 0.f, kMoveAt = 30.f, kAhead = 0.f, kMostSum = 0x1p40f;
 };
 template <>
 struct Softmax<false> {
   static constexpr float kTop = 11.5f, kMoveAt = 3.5f, kAhead = 3.f, kMostSum = 60000.f;
 };
 
+// Tensor memory is full: scores (and over them probabilities) of 128 columns,
+// and two O of d.  A half's next scores wait for its probabilities' product
+// where there are two buffers; with 64 channels there is room for a third, and
+// they do not.
 template <int D>
-struct TileSmem {
+struct Tiles {
+  static constexpr int kBuffers = D == 64 ? 3 : 2, kStages = D == 64 ? 4 : 2;
+  static constexpr int kOut = kBuffers * 128;  // column of the first O
   static constexpr int kTileBytes = D / 64 * kBlockBytes;
-  static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + 2 * kTileBytes;
-  static constexpr int kBytes = kV + 2 * kTileBytes;
+  static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes;
+  static constexpr int kBytes = kV + kStages * kTileBytes;
   // with 1 KiB to align, and enough for one CTA per SM: each takes all of tensor memory
   static constexpr int kAsk = (kBytes > 120 * 1024 ? kBytes : 120 * 1024) + 1024;
 };
@@ -85,14 +101,22 @@ __device__ __forceinline__ int tile_key(const Range& v, int j) { return (v.tile0
 // Whether some key of the tile is seen by no row of the work.
 __device__ __forceinline__ bool at_edge(const Range& v, int key0) { return key0 < v.lo || key0 + kKeys > v.hi; }
 
+// Scores n = 2 * (tile, counted over all works) + half are in buffer n % kBuffers.
+template <int D>
 struct TileShared {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_edge[2], s_full[2], p_full[2], q_full[2],
-      work_full[kWorksAhead], work_empty[kWorksAhead], drain;
+  uint64_t k_full[Tiles<D>::kStages], k_empty[Tiles<D>::kStages], v_full[Tiles<D>::kStages], v_empty[Tiles<D>::kStages],
+      v_edge[Tiles<D>::kStages], s_full[Tiles<D>::kBuffers], p_full[Tiles<D>::kBuffers], q_full[2], q_empty[2], o_full[2][2],
+      work_full[kWorksAhead], work_empty[kWorksAhead], work_due, drain;
   uint32_t tmem;
   int32_t dead;               // some wait ran out
   Work work[kWorksAhead];     // work k at k % kWorksAhead
 };
 
+__device__ __forceinline__ __half2 half2_of(uint32_t u) {
+  __half2 h;
+  memcpy(&h, &u, 4);
+  return h;
+}
 __device__ __forceinline__ void mbar_expect(uint64_t* b, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mbar_addr(b)), "r"(bytes) : "memory");
 }
@@ -105,6 +129,11 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
           dst),
       "l"(map), "r"(mbar_addr(b)), "r"(channel), "r"(head), "r"(0), "r"(slot), "r"(leader)
       : "memory");
+}
+__device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // Number `idx` of the call's works, found by a warp (all lanes get it); false
@@ -178,39 +207,43 @@ __device__ __forceinline__ bool find_work(const AttendPagedParams& p, Cursor& c,
     c.r0 = 0;
   }
 }
-__device__ __forceinline__ int work_number(int k) {
-  const int g = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
-  return k * g + (k & 1 ? g - 1 - b : b);
-}
 
-// kMods: scores are capped or have a bias.
-template <bool kBf16, int D, bool kMods>
+template <bool kBf16, int D, Scores kScores>
 __global__ void __launch_bounds__(kThreadsTiles, 1)
     k_attend_paged_tiles(const __grid_constant__ AttendPagedParams p, const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map) {
-  using Smem = TileSmem<D>;
+  using L = Tiles<D>;
   using Soft = Softmax<kBf16>;
+  constexpr int kStages = L::kStages, kBuffers = L::kBuffers;
   extern __shared__ unsigned char dyn_raw[];
-  __shared__ TileShared sh;
+  __shared__ TileShared<D> sh;
   unsigned char* const dyn = dyn_raw + (1024 - (smem_addr(dyn_raw) & 1023)) % 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   int bad = 0;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.v_full[i], 1);
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.v_empty[i], 1);
       mbar_init(&sh.v_edge[i], 1);
+    }
+    for (int i = 0; i < kBuffers; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], kHalf);
-      mbar_init(&sh.q_full[i], kHalf);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 64);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.o_full[i][0], 1);
+      mbar_init(&sh.o_full[i][1], 1);
     }
     for (int i = 0; i < kWorksAhead; ++i) {
       mbar_init(&sh.work_full[i], 1);
       mbar_init(&sh.work_empty[i], kThreadsTiles / 32 - 1);
     }
+    mbar_init(&sh.work_due, 1);
     mbar_init(&sh.drain, 1);
     sh.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -229,7 +262,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
   int base = 0;  // tiles of the works so far
   // Work k is read where it is needed, which leaves the registers to the loops.
   auto take_work = [&](int k) {  // false: none left (or a wait ran out)
-    const bool there = mbar_wait(&sh.work_full[k % kWorksAhead], (k / kWorksAhead) & 1, &sh.dead);
+    const bool there = mbar_wait_inline(&sh.work_full[k % kWorksAhead], (k / kWorksAhead) & 1, &sh.dead);
     ok = __all_sync(0xffffffffu, ok && there);
     return ok && sh.work[k % kWorksAhead].tiles > 0;
   };
@@ -240,148 +273,144 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
 
   if (warp < kSoftmaxWarps) {
     // ================================================== softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes of tensor memory per warp
-    const uint32_t s_at = tmem + lanes + half * 128, o_at = tmem + lanes + 256 + half * D;
-    // A row's 16-byte pieces belong to D / 8 lanes where rows are read and written.
-    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
-    const int piece = lane % kLanes;
-    unsigned char* const rows_smem = dyn + Smem::kQ + half * Smem::kTileBytes + (warp & 3) * 32 * 128;
-    auto piece_at = [&](int at, int c) {  // piece c of the warp's row `at`: queries, then the result
-      return reinterpret_cast<uint4*>(rows_smem + (c / 8) * kBlockBytes + at * 128 + (((c % 8) ^ (at & 7)) << 4));
-    };
+    const uint32_t o_at = tmem + lanes + L::kOut + half * D;
     auto pack2 = [](float lo, float hi) { return kBf16 ? pack_bf16(lo, hi) : pack_f16(lo, hi); };
     for (int k = 0; take_work(k); ++k) {
       const Work& work = sh.work[k % kWorksAhead];
       const int tiles = work.tiles, row = work.row0 + tid;
-      auto row_offset = [&](int rr, int64_t token, int64_t head_stride) {  // of row rr in q or out
-        const int i = static_cast<int>(p.by_group.div(rr));
-        return static_cast<int64_t>(work.rq.q0 + i) * token +
-               static_cast<int64_t>(work.head * p.G + rr - i * p.G) * head_stride;
-      };
-      // ---- queries
-      const int row_first = work.row0 + warp * 32 + lane / kLanes;
-#pragma unroll 1
-      for (int r0 = 0; r0 < 32; r0 += 8 * kRowsAt) {
-        uint4 raw[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int rr = row_first + r0 + u * kRowsAt;
-          raw[u] = make_uint4(0, 0, 0, 0);
-          if (rr < work.rows_all)
-            raw[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                     row_offset(rr, p.q_token, p.q_head) + piece * 8);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) *piece_at(r0 + u * kRowsAt + lane / kLanes, piece) = raw[u];
-      }
-      fence_async();
-      mbar_arrive(&sh.q_full[half]);
+      const bool live = row < work.rows_all;
       // keys that the thread's row sees; rows past the last see what the work sees
-      int first = work.vis.lo, last = work.vis.hi;
-      float pos_f = 0.f, slope = 0.f;
-      if (row < work.rows_all) {
-        const int i = static_cast<int>(p.by_group.div(row));
-        const int pos = position(p, work.rq, i);
+      const int token = static_cast<int>(p.by_group.div(live ? row : 0)), head = work.head * p.G + row - token * p.G;
+      int first = work.vis.lo, last = work.vis.hi, pos = 0;
+      float slope = 0.f;
+      if (live) {
+        pos = position(p, work.rq, token);
         first = first_key(p, pos);
         last = last_key(p, work.rq, pos);
-        if (kMods) {
-          pos_f = static_cast<float>(pos);
-          if (p.slopes) slope = __ldg(p.slopes + work.head * p.G + row - i * p.G) * kLog2e;
-        }
+        if (kScores == kBiased) slope = p.slopes ? __ldg(p.slopes + head) * kLog2e : 0.f;
       }
-      __syncwarp();
 
       float m = kNegInf, l = 0.f;
-      for (int j = 0; j < tiles && ok; ++j) {
-        ok = mbar_wait(&sh.s_full[half], (base + j + k) & 1, &sh.dead);
+      int key0 = tile_key(work.vis, 0);
+      for (int j = 0; j < tiles && ok; ++j, key0 -= kKeys) {
+        const int n = 2 * (base + j) + half, buffer = n % kBuffers;
+        const uint32_t s_at = tmem + lanes + buffer * 128;
+        const int lo = first - key0, hi = last - key0;  // columns [lo, hi) count
+        // Most tiles: all of it seen, by rows that have a reference.
+        const bool partly = lo > 0 || hi < kKeys, fresh = m == kNegInf && max(lo, 0) < min(hi, kKeys);
+        const bool special = __any_sync(0xffffffffu, partly || fresh);
+        ok = mbar_wait_inline(&sh.s_full[buffer], (n / kBuffers) & 1, &sh.dead);
         if (!__all_sync(0xffffffffu, ok)) break;
         fence_after();
-        const int key0 = tile_key(work.vis, j);
-        // Most tiles: all of it seen, by rows that have a reference, and no score far above that.  One pass then,
-        // with P kept in registers until its sum is known, since it goes over the scores.
-        const bool masked = __any_sync(0xffffffffu, key0 < first || key0 + kKeys > last || m == kNegInf);
+        // A score in units of log2.
+        auto score = [&](float x, int c) {
+          if (kScores == kCapped || (kScores == kBiased && p.cap_log2 != 0.f))
+            x = tanh_of(x * p.cap_in) * p.cap_log2;
+          else
+            x *= p.scale_log2;
+          if (kScores == kBiased) x = fmaf(-slope, fabsf(static_cast<float>(pos - key0) - static_cast<float>(c)), x);
+          return x;
+        };
+        // P against the reference, and its sum.  It stays in registers until that is known, since it goes over S.
+        uint32_t h[64];
+        auto exponentials = [&](float2 (&v)[8], int c, float2& part) {  // of 16 columns from c on
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[i].x = ex2(v[i].x);
+            v[i].y = ex2(v[i].y);
+            part = __fadd2_rn(part, v[i]);
+            h[c / 2 + i] = pack2(v[i].x, v[i].y);
+          }
+        };
+        // Whether no sum is too large, nor a probability for fp16.
+        auto fits = [&](float sum) {
+          bool fit = __all_sync(0xffffffffu, sum < Soft::kMostSum);
+          if (!kBf16 && !fit) {
+            __half2 most = half2_of(h[0]);
+#pragma unroll
+            for (int i = 1; i < 64; ++i) most = __hmax2_nan(most, half2_of(h[i]));
+            fit = __all_sync(0xffffffffu, __hlt(__hmax_nan(__low2half(most), __high2half(most)), __ushort_as_half(0x7c00)));
+          }
+          return fit;
+        };
         float sum = 0.f;
-        bool done = false, crowded = false;  // crowded: the sum was too large
-        if (!kMods && !masked) {
-          uint32_t x[2][16], h[2][32];
-          const float2 f2 = make_float2(p.scale_log2, p.scale_log2), off2 = make_float2(Soft::kTop - m, Soft::kTop - m);
+        bool done = false, crowded = false;
+        if (!special) {
+          const float off = Soft::kTop - m;
           float2 part = make_float2(0.f, 0.f);
+          uint32_t x[2][16];
           tmem_load16(x[0], s_at);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint32_t(&y)[16] = x[c & 1];
             tmem_wait_load16(y);
             if (c < 7) tmem_load16(x[(c & 1) ^ 1], s_at + (c + 1) * 16);
+            float2 v[8];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float2 v = __ffma2_rn(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), f2, off2);
-              v.x = ex2(v.x);
-              v.y = ex2(v.y);
-              part = __fadd2_rn(part, v);
-              h[c / 4][(c % 4) * 8 + i / 2] = pack2(v.x, v.y);
+            for (int i = 0; i < 8; ++i) {
+              v[i] = make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+              if constexpr (kScores == kPlain)
+                v[i] = __ffma2_rn(v[i], make_float2(p.scale_log2, p.scale_log2), make_float2(off, off));
+              else
+                v[i] = make_float2(score(v[i].x, c * 16 + 2 * i) + off, score(v[i].y, c * 16 + 2 * i + 1) + off);
             }
+            exponentials(v, c * 16, part);
           }
           sum = part.x + part.y;
-          done = __all_sync(0xffffffffu, sum < Soft::kMostSum);
+          done = fits(sum);
           crowded = !done;
-          if (done) {
-            tmem_store32(s_at, h[0]);
-            tmem_store32(s_at + 32, h[1]);
-          }
         }
-        if (!done) {
-          const int lo = first - key0, hi = last - key0;  // columns [lo, hi) count
-          sum = 0.f;
-          uint32_t a[32];
+        // The first keys of a row, keys that some row does not see, or a reference to move: all scores in registers.
+        for (bool moves = crowded || __any_sync(0xffffffffu, fresh); !done; moves = crowded = true) {
+          uint32_t y[8][16];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) tmem_load16(y[c], s_at + c * 16);
+          uint32_t none = 0, some = 0;  // what 16 columns are to the warp: seen by no row, not seen by some
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            none |= __any_sync(0xffffffffu, lo < c * 16 + 16 && hi > c * 16) ? 0u : 1u << c;
+            some |= __all_sync(0xffffffffu, lo <= c * 16 && hi >= c * 16 + 16) ? 0u : 1u << c;
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) tmem_wait_load16(y[c]);
           float top = kNegInf;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_load32(a, s_at + c * 32);
-            tmem_wait_load(a);
-            // in units of log2, with what is hidden at -inf, where the scores are
-            const int n = min(max(hi - c * 32, 0), 32), skip = min(max(lo - c * 32, 0), 32);
-            const uint32_t seen = (n == 32 ? ~0u : (1u << n) - 1u) & (skip == 32 ? 0u : ~0u << skip);
-            if (kMods) {
-              const float away = pos_f - static_cast<float>(key0 + c * 32);
+          for (int c = 0; c < 8; ++c) {
+            if (none >> c & 1u) continue;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                float x = __uint_as_float(a[i]);
-                x = p.cap_log2 != 0.f ? tanh_of(x * p.cap_in) * p.cap_log2 : x * p.scale_log2;
-                x = fmaf(-slope, fabsf(away - static_cast<float>(i)), x);
-                a[i] = __float_as_uint(x);
-              }
-            } else {
+            for (int i = 0; i < 16; ++i) y[c][i] = __float_as_uint(score(__uint_as_float(y[c][i]), c * 16 + i));
+            if (some >> c & 1u) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * p.scale_log2);
+              for (int i = 0; i < 16; ++i)
+                if (c * 16 + i < lo || c * 16 + i >= hi) y[c][i] = __float_as_uint(kNegInf);
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (!(seen >> i & 1u)) a[i] = __float_as_uint(kNegInf);
-              top = fmaxf(top, __uint_as_float(a[i]));
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(y[c][i]));
+          }
+          if (moves) {  // the reference, and O with it
+            float ahead = Soft::kAhead;
+            if (!kBf16) {  // n keys in all, fewer than a tile: 128 / n times lower, as n of them do not pass kMostSum either
+              const int all = last - first;
+              if (all < kKeys) ahead -= static_cast<float>(__clz(max(all - 1, 0)) - __clz(kKeys - 1));
             }
-            tmem_store32(s_at + c * 32, a);
-          }
-          wait_store();
-          // the reference of the row, and O with it
-          float ahead = Soft::kAhead;
-          if (!kBf16) {  // n keys in all, fewer than a tile: 128 / n times lower, as n of them do not pass kMostSum either
-            const int n = last - first;
-            if (n < kKeys) ahead -= static_cast<float>(__clz(max(n - 1, 0)) - __clz(kKeys - 1));
-          }
-          const float m_new =
-              top > m + (crowded ? -Soft::kAhead : Soft::kMoveAt) || (m == kNegInf && top > m) ? top + ahead : m;
-          if (__any_sync(0xffffffffu, m_new != m)) {
-            const float by = m == kNegInf ? 0.f : ex2(m - m_new);
-            l *= by;
-            if (j > 0) {
+            const float m_new =
+                top > m + (crowded ? -Soft::kAhead : Soft::kMoveAt) || (m == kNegInf && top > m) ? top + ahead : m;
+            if (__any_sync(0xffffffffu, m_new != m && m != kNegInf)) {  // O of a row without one is 0
+              const float by = m == kNegInf ? 0.f : ex2(m - m_new);
+              l *= by;
+              ok = mbar_wait_inline(&sh.o_full[half][(base + j - 1) & 1], ((base + j - 1) >> 1) & 1, &sh.dead) && ok;
+              fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                tmem_load32(a, o_at + c * 32);
-                tmem_wait_load(a);
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_load16(o, o_at + c);
+                tmem_wait_load16(o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * by);
-                tmem_store32(o_at + c * 32, a);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+                tmem_store16(o_at + c, o);
               }
             }
             m = m_new;
@@ -389,239 +418,303 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           const float off = m == kNegInf ? 0.f : Soft::kTop - m;
           float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t h[16];
-            tmem_load32(a, s_at + c * 32);
-            tmem_wait_load(a);
+          for (int c = 0; c < 8; ++c) {
+            if (none >> c & 1u) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 v = make_float2(ex2(__uint_as_float(a[i]) + off), ex2(__uint_as_float(a[i + 1]) + off));
-              part = __fadd2_rn(part, v);
-              h[i / 2] = pack2(v.x, v.y);
+              for (int i = 0; i < 8; ++i) h[c * 8 + i] = 0;
+            } else {
+              float2 v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                v[i] = __fadd2_rn(make_float2(__uint_as_float(y[c][2 * i]), __uint_as_float(y[c][2 * i + 1])), make_float2(off, off));
+              exponentials(v, c * 16, part);
             }
-            tmem_store16(s_at + c * 16, h);  // over columns already read
           }
           sum = part.x + part.y;
+          done = moves || fits(sum);
         }
+        tmem_store32(s_at, reinterpret_cast<const uint32_t(&)[32]>(h[0]));
+        tmem_store32(s_at + 32, reinterpret_cast<const uint32_t(&)[32]>(h[32]));
         l += sum;
         wait_store();
         fence_before();
-        mbar_arrive(&sh.p_full[half]);
+        mbar_arrive(&sh.p_full[buffer]);
       }
       base += tiles;
-      // ---- the result, through the queries' place in shared memory, which no product reads any more
-      ok = ok && mbar_wait(&sh.s_full[half], (base + k) & 1, &sh.dead);
+      // ---- the result
+      ok = ok && mbar_wait_inline(&sh.o_full[half][(base - 1) & 1], ((base - 1) >> 1) & 1, &sh.dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       fence_after();
       const float by = l > 0.f ? 1.f / l : 0.f;
+      uint16_t* const out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(work.rq.q0 + token) * p.o_token +
+                            static_cast<int64_t>(head) * p.o_head;
+      uint32_t x[D / 32][32];
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t x[32];
-        tmem_load32(x, o_at + c * 32);
-        tmem_wait_load(x);
+      for (int c = 0; c < D / 32; ++c) tmem_load32(x[c], o_at + c * 32);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t w[4];
+      for (int c = 0; c < D / 32; ++c) tmem_wait_load(x[c]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = pack2(__uint_as_float(x[u * 8 + 2 * i]) * by, __uint_as_float(x[u * 8 + 2 * i + 1]) * by);
-          *piece_at(lane, c * 4 + u) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          w[i] = pack2(__uint_as_float(x[c / 2][c % 2 * 16 + 2 * i]) * by, __uint_as_float(x[c / 2][c % 2 * 16 + 2 * i + 1]) * by);
+        uint16_t* const to = out + c * 16;
+        if (live && p.out32) {
+          store32(to, w);
+        } else if (live) {
+          reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
       fence_before();
-      if (p.lse && row < work.rows_all)
-        p.lse[row_offset(row, static_cast<int64_t>(p.H) * p.G, 1)] =
+      if (p.lse && live)
+        p.lse[static_cast<int64_t>(work.rq.q0 + token) * (static_cast<int64_t>(p.H) * p.G) + head] =
             l > 0.f ? (m - Soft::kTop + log2f(l)) * kLn2 : kNegInf;
-      __syncwarp();
-#pragma unroll 4
-      for (int r0 = 0; r0 < 32; r0 += kRowsAt) {
-        const uint4 w = *piece_at(r0 + lane / kLanes, piece);
-        if (row_first + r0 < work.rows_all)
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row_offset(row_first + r0, p.o_token, p.o_head) +
-                                    piece * 8) = w;
-      }
-      __syncwarp();
       leave_work(k);
     }
-  } else if (warp == kLoadWarp) {
-    // ================================================== keys and values
-    // A box is 64 channels of the tile's rows in one slot; lane i looks slot i up.  Rows of a slot that does not
-    // exist, or that no row sees, come from past the buffer's end, where the copy finds zeros.
-    const int block = 1 << p.B_log2, slots = kKeys >> p.B_log2;
-    const uint32_t leader = elect_leader(), tiles_at = __shfl_sync(0xffffffffu, smem_addr(dyn), 0);
-    // bit st: the parity of v_edge[st]'s next use, and whether the last values into stage st went by it
-    uint32_t edges = 0, by_edge = 0;
-    int k_sent = 0, v_sent = 0;  // tiles on their way so far
-    for (int k = 0; take_work(k); ++k) {
-      const Work& work = sh.work[k % kWorksAhead];
-      const Range vis = work.vis;
-      const int head = work.head, tiles = work.tiles;
-      const int32_t* const table = p.tables + static_cast<int64_t>(work.r) * p.table_stride;
-      auto slot_of = [&](int j) {
-        int slot = p.num_slots;
-        if (lane < slots && j < tiles) {
-          const int key = tile_key(vis, j) + lane * block;
-          if (key < vis.hi && key + block > vis.lo) {
-            slot = __ldg(table + (key >> p.B_log2));
-            if (static_cast<uint32_t>(slot) >= static_cast<uint32_t>(p.num_slots)) {
-              bad |= HC_DEVERR_SLOT;
-              slot = p.num_slots;
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp) {
+      // ================================================== keys and values
+      // A box is 64 channels of the tile's rows in one slot; lane i looks slot i up.  Rows of a slot that does not
+      // exist, or that no row sees, come from past the buffer's end, where the copy finds zeros.
+      const int block = 1 << p.B_log2, slots = kKeys >> p.B_log2;
+      const uint32_t leader = elect_leader(), tiles_at = __shfl_sync(0xffffffffu, smem_addr(dyn), 0);
+      // bit st: the parity of v_edge[st]'s next use, and whether the last values into stage st went by it
+      uint32_t edges = 0, by_edge = 0;
+      int k_sent = 0, v_sent = 0;  // tiles on their way so far
+      for (int k = 0; take_work(k); ++k) {
+        const Work& work = sh.work[k % kWorksAhead];
+        const Range vis = work.vis;
+        const int head = work.head, tiles = work.tiles;
+        const int32_t* const table = p.tables + static_cast<int64_t>(work.r) * p.table_stride;
+        auto slot_of = [&](int j) {
+          int slot = p.num_slots;
+          if (lane < slots && j < tiles) {
+            const int key = tile_key(vis, j) + lane * block;
+            if (key < vis.hi && key + block > vis.lo) {
+              slot = __ldg(table + (key >> p.B_log2));
+              if (static_cast<uint32_t>(slot) >= static_cast<uint32_t>(p.num_slots)) {
+                bad |= HC_DEVERR_SLOT;
+                slot = p.num_slots;
+              }
             }
           }
-        }
-        return slot;
-      };
-      auto load = [&](uint32_t dst, const CUtensorMap* map, uint64_t* full, int slot) {
+          return slot;
+        };
+        auto load = [&](uint32_t dst, const CUtensorMap* map, uint64_t* full, int slot) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= slots) break;
-          const int s = __shfl_sync(0xffffffffu, slot, i);
+          for (int i = 0; i < 8; ++i) {
+            if (i >= slots) break;
+            const int s = __shfl_sync(0xffffffffu, slot, i);
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load(dst + c * kBlockBytes + i * (block * 128), map, full, c * 64, head, s, leader);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load(dst + c * kBlockBytes + i * (block * 128), map, full, c * 64, head, s, leader);
+          }
+        };
+        int slot = slot_of(0);
+        for (int j = 0; j < tiles; ++j) {
+          const int st = (base + j) % kStages, round = (base + j) / kStages;
+          const int next = slot_of(j + 1);
+          if (lane == 0 && j == max(tiles - kDue, 0)) mbar_arrive(&sh.work_due);
+          if (round > 0) ok = mbar_wait_inline(&sh.k_empty[st], (round - 1) & 1, &sh.dead);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          if (lane == 0) mbar_expect(&sh.k_full[st], L::kTileBytes);
+          __syncwarp();
+          ++k_sent;
+          load(tiles_at + L::kK + st * L::kTileBytes, &k_map, &sh.k_full[st], slot);
+          if (round > 0) ok = mbar_wait_inline(&sh.v_empty[st], (round - 1) & 1, &sh.dead);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          const bool edge = at_edge(vis, tile_key(vis, j));
+          uint64_t* const full = edge ? &sh.v_edge[st] : &sh.v_full[st];
+          if (lane == 0) mbar_expect(full, L::kTileBytes);
+          __syncwarp();
+          ++v_sent;
+          by_edge = (by_edge & ~(1u << st)) | static_cast<uint32_t>(edge) << st;
+          if (edge) edges ^= 1u << st;
+          load(tiles_at + L::kV + st * L::kTileBytes, &v_map, full, slot);
+          slot = next;
         }
-      };
-      int slot = slot_of(0);
-      for (int j = 0; j < tiles; ++j) {
-        const int st = (base + j) & 1, round = (base + j) >> 1;
-        const int next = slot_of(j + 1);
-        if (base + j >= 2) ok = mbar_wait(&sh.k_empty[st], (round - 1) & 1, &sh.dead);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        if (lane == 0) mbar_expect(&sh.k_full[st], Smem::kTileBytes);
-        __syncwarp();
-        ++k_sent;
-        load(tiles_at + Smem::kK + st * Smem::kTileBytes, &k_map, &sh.k_full[st], slot);
-        if (base + j >= 2) ok = mbar_wait(&sh.v_empty[st], (round - 1) & 1, &sh.dead);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const bool edge = at_edge(vis, tile_key(vis, j));
-        uint64_t* const full = edge ? &sh.v_edge[st] : &sh.v_full[st];
-        if (lane == 0) mbar_expect(full, Smem::kTileBytes);
-        __syncwarp();
-        ++v_sent;
-        by_edge = (by_edge & ~(1u << st)) | static_cast<uint32_t>(edge) << st;
-        if (edge) edges ^= 1u << st;
-        load(tiles_at + Smem::kV + st * Smem::kTileBytes, &v_map, full, slot);
-        slot = next;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        base += tiles;
+        leave_work(k);
       }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      base += tiles;
-      leave_work(k);
-    }
-    if (!ok) {  // a wait ran out: copies may still be on their way into shared memory
-      int32_t no = 0;
-      for (int n = max(k_sent - 2, 0); n < k_sent; ++n) mbar_wait(&sh.k_full[n & 1], (n >> 1) & 1, &no);
-      for (int n = max(v_sent - 2, 0); n < v_sent; ++n) {
-        const int st = n & 1;
-        if (by_edge >> st & 1u)
-          mbar_wait(&sh.v_edge[st], ~(edges >> st) & 1u, &no);
-        else
-          mbar_wait(&sh.v_full[st], (n >> 1) & 1, &no);
+      if (!ok) {  // a wait ran out: copies may still be on their way into shared memory
+        int32_t no = 0;
+        for (int n = max(k_sent - kStages, 0); n < k_sent; ++n) mbar_wait_inline(&sh.k_full[n % kStages], (n / kStages) & 1, &no);
+        for (int n = max(v_sent - kStages, 0); n < v_sent; ++n) {
+          const int st = n % kStages;
+          if (by_edge >> st & 1u)
+            mbar_wait_inline(&sh.v_edge[st], ~(edges >> st) & 1u, &no);
+          else
+            mbar_wait_inline(&sh.v_full[st], (n / kStages) & 1, &no);
+        }
+        __syncwarp();
+      }
+    } else if (warp == kEdgeWarp) {
+      // ================================================== values that no row sees: 0 times them must be 0
+      if (p.positions)  // of the requests r = blockIdx.x mod gridDim.x: whether positions fall
+        for (int r = blockIdx.x; r < p.n_req; r += gridDim.x) {
+          int dummy = 0;
+          const PagedRequest q = load_request(p, r, dummy);
+          for (int i = 1 + lane; i < q.n; i += 32)
+            if (position(p, q, i) < position(p, q, i - 1)) bad |= HC_DEVERR_POS;
+        }
+      uint32_t edges = 0;  // bit st: the parity of v_edge[st]'s next use
+      for (int k = 0; take_work(k); ++k) {
+        const Range vis = sh.work[k % kWorksAhead].vis;
+        leave_work(k);
+        for (int j = 0; j < vis.tiles && ok; ++j) {
+          const int key0 = tile_key(vis, j), st = (base + j) % kStages;
+          if (!at_edge(vis, key0)) continue;
+          ok = mbar_wait_inline(&sh.v_edge[st], edges >> st & 1u, &sh.dead);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          edges ^= 1u << st;
+          unsigned char* const tile = dyn + L::kV + st * L::kTileBytes;
+          for (int i = lane; i < kKeys * (D / 8); i += 32) {
+            const int key = (i / 8) % kKeys;
+            if (key0 + key < vis.lo || key0 + key >= vis.hi) *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.v_full[st]);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        base += vis.tiles;
+      }
+    } else if (warp == kWorkWarp) {
+      // ================================================== works, found ahead of the warps that do them
+      // The first is the CTA's number; the others are taken from a counter, each when the one before is nearly loaded.
+      Cursor cursor(p);
+      Work work;
+      int number = blockIdx.x;
+      for (int k = 0;; ++k) {
+        if (k >= kWorksAhead)
+          ok = mbar_wait_inline(&sh.work_empty[k % kWorksAhead], (k / kWorksAhead - 1) & 1, &sh.dead);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (k > 0) {
+          ok = mbar_wait_inline(&sh.work_due, (k - 1) & 1, &sh.dead);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          if (lane == 0) number = static_cast<int>(gridDim.x) + atomicAdd(p.tiles_taken, 1);
+          number = __shfl_sync(0xffffffffu, number, 0);
+        }
+        const bool more = find_work(p, cursor, number, lane, work);
+        if (!more) work.tiles = 0;
+        if (lane == 0) {
+          sh.work[k % kWorksAhead] = work;
+          mbar_arrive(&sh.work_full[k % kWorksAhead]);
+        }
+        if (!more) break;
+      }
+      // the last CTA to come here leaves the counters as it found them
+      if (lane == 0) {
+        __threadfence();
+        if (atomicAdd(p.tiles_taken + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+          p.tiles_taken[0] = 0;
+          p.tiles_taken[1] = 0;
+        }
+      }
+      __syncwarp();
+    } else if (warp == kProductWarp) {
+      // ================================================== products
+      // Buffers and stages go round by counting, a half is known where the code is written, and the numbers of tiles
+      // come by a shuffle: so all of it stays in uniform registers, and a product's issue takes 11 cycles instead of 33.
+      const uint32_t leader = elect_leader();
+      const uint32_t at = __shfl_sync(0xffffffffu, tmem, 0), tiles_at = __shfl_sync(0xffffffffu, smem_addr(dyn), 0);
+      uint32_t s_tile = 0, p_tile = 0;                          // tiles of keys and of values so far
+      uint32_t s_buffer = 0, p_buffer = 0, p_parity = 0;        // of the next scores, of the next probabilities
+      // Whether a wait ran out is asked once per tile: products on what is not there yet spoil results only.
+      auto wait = [&](uint64_t* b, uint32_t parity) { ok = mbar_wait_inline(b, parity, &sh.dead) && ok; };
+      auto scores = [&](int i) {  // S_i = Q_i K(j)^T
+        const uint32_t st = s_tile % kStages;
+        if (i == 0) wait(&sh.k_full[st], (s_tile / kStages) & 1);
+        fence_after();
+        const uint64_t q = smem_desc(tiles_at + L::kQ + i * L::kTileBytes, 16);
+        const uint64_t keys = smem_desc(tiles_at + L::kK + st * L::kTileBytes, 16);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint64_t step = ((s / 4) * kBlockBytes + (s % 4) * 32) >> 4;
+          mma_smem(at + s_buffer * 128, q + step, keys + step, instr_desc(kKeys, false, kBf16), s > 0, leader);
+        }
+        commit(&sh.s_full[s_buffer], leader);
+        s_buffer = s_buffer == kBuffers - 1 ? 0 : s_buffer + 1;
+        if (i == 1) {
+          commit(&sh.k_empty[st], leader);
+          ++s_tile;
+        }
+      };
+      auto values = [&](int i, bool add) {  // O_i (+)= P_i(j) V(j)
+        const uint32_t st = p_tile % kStages;
+        if (i == 0) wait(&sh.v_full[st], (p_tile / kStages) & 1);
+        wait(&sh.p_full[p_buffer], p_parity);
+        fence_after();
+        const uint64_t v = smem_desc(tiles_at + L::kV + st * L::kTileBytes, kBlockBytes);
+#pragma unroll
+        for (int s = 0; s < kKeys / 16; ++s)
+          mma_tmem(at + L::kOut + i * D, at + p_buffer * 128 + s * 8, v + s * (2048 >> 4), instr_desc(D, true, kBf16),
+                   add || s > 0, leader);
+        commit(&sh.o_full[i][p_tile & 1], leader);
+        if (i == 1) {
+          commit(&sh.v_empty[st], leader);
+          ++p_tile;
+        }
+        p_parity ^= p_buffer == kBuffers - 1 ? 1 : 0;
+        p_buffer = p_buffer == kBuffers - 1 ? 0 : p_buffer + 1;
+      };
+      for (int k = 0; take_work(k); ++k) {
+        const int count = 2 * __shfl_sync(0xffffffffu, sh.work[k % kWorksAhead].tiles, 0);  // tiles and halves
+        leave_work(k);
+#pragma unroll 1
+        for (int n = 0; n < count + kBuffers; n += 2) {  // scores n, and probabilities n - kBuffers whose place they take
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int nn = n + i - kBuffers;
+            if (nn >= 0 && nn < count) values((i + kBuffers) & 1, nn > 1);
+            if (n < count) {
+              if (n == 0) wait(&sh.q_full[i], k & 1);
+              scores(i);
+              if (n == count - 2) commit(&sh.q_empty[i], leader);
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+      }
+      __syncwarp();
+    } else {
+      // ================================================== queries: two warps a half, of the next work as soon as
+      // the last scores of this one are there
+      constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;  // 16-byte pieces of a row; rows at a time
+      const int half = (warp - kQueryWarp) >> 1, piece = lane % kLanes;
+      const int row_first = (warp - kQueryWarp) * 64 + lane / kLanes;  // of the 256
+      const uint32_t to = smem_addr(dyn) + L::kQ + half * L::kTileBytes + (piece / 8) * kBlockBytes;
+      for (int k = 0; take_work(k); ++k) {
+        const Work& work = sh.work[k % kWorksAhead];
+        const int row0 = work.row0, rows_all = work.rows_all, q0 = work.rq.q0, head = work.head * p.G;
+        leave_work(k);
+        if (k > 0) ok = mbar_wait_inline(&sh.q_empty[half], (k - 1) & 1, &sh.dead);
+        if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll 4
+        for (int r = 0; r < 64; r += kRowsAt) {
+          const int at = row_first + r, row = row0 + at;
+          const bool live = row < rows_all;
+          const int i = static_cast<int>(p.by_group.div(live ? row : 0));
+          const uint16_t* const from = static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(q0 + i) * p.q_token +
+                                       static_cast<int64_t>(head + (live ? row : 0) - i * p.G) * p.q_head + piece * 8;
+          cp_async16(to + (at % kHalf) * 128 + (((piece % 8) ^ (at & 7)) << 4), live ? from : static_cast<const uint16_t*>(p.q),
+                     live ? 16 : 0);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_async();
+        mbar_arrive(&sh.q_full[half]);
       }
       __syncwarp();
     }
-  } else if (warp == kEdgeWarp) {
-    // ================================================== values that no row sees: 0 times them must be 0
-    if (p.positions)  // of the requests r = blockIdx.x mod gridDim.x: whether positions fall
-      for (int r = blockIdx.x; r < p.n_req; r += gridDim.x) {
-        int dummy = 0;
-        const PagedRequest q = load_request(p, r, dummy);
-        for (int i = 1 + lane; i < q.n; i += 32)
-          if (position(p, q, i) < position(p, q, i - 1)) bad |= HC_DEVERR_POS;
-      }
-    uint32_t edges = 0;  // bit st: the parity of v_edge[st]'s next use
-    for (int k = 0; take_work(k); ++k) {
-      const Range vis = sh.work[k % kWorksAhead].vis;
-      leave_work(k);
-      for (int j = 0; j < vis.tiles && ok; ++j) {
-        const int key0 = tile_key(vis, j), st = (base + j) & 1;
-        if (!at_edge(vis, key0)) continue;
-        ok = mbar_wait(&sh.v_edge[st], edges >> st & 1u, &sh.dead);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        edges ^= 1u << st;
-        unsigned char* const tile = dyn + Smem::kV + st * Smem::kTileBytes;
-        for (int i = lane; i < kKeys * (D / 8); i += 32) {
-          const int key = (i / 8) % kKeys;
-          if (key0 + key < vis.lo || key0 + key >= vis.hi) *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.v_full[st]);
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      base += vis.tiles;
-    }
-  } else if (warp == kWorkWarp) {
-    // ================================================== works, found ahead of the warps that do them
-    Cursor cursor(p);
-    Work work;
-    for (int k = 0;; ++k) {
-      const bool more = find_work(p, cursor, work_number(k), lane, work);
-      if (!more) work.tiles = 0;
-      if (k >= kWorksAhead)
-        ok = mbar_wait(&sh.work_empty[k % kWorksAhead], (k / kWorksAhead - 1) & 1, &sh.dead);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0) {
-        sh.work[k % kWorksAhead] = work;
-        mbar_arrive(&sh.work_full[k % kWorksAhead]);
-      }
-      if (!more) break;
-    }
-    __syncwarp();
-  } else {
-    // ================================================== products
-    const uint32_t leader = elect_leader();
-    const uint32_t at = __shfl_sync(0xffffffffu, tmem, 0), tiles_at = __shfl_sync(0xffffffffu, smem_addr(dyn), 0);
-    auto scores = [&](int i, int j) {  // S_i = Q_i K(j)^T
-      const uint64_t q = smem_desc(tiles_at + Smem::kQ + i * Smem::kTileBytes, 16);
-      const uint64_t k = smem_desc(tiles_at + Smem::kK + (j & 1) * Smem::kTileBytes, 16);
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const uint64_t step = ((s / 4) * kBlockBytes + (s % 4) * 32) >> 4;
-        mma_smem(at + i * 128, q + step, k + step, instr_desc(kKeys, false, kBf16), s > 0, leader);
-      }
-      commit(&sh.s_full[i], leader);
-    };
-    auto values = [&](int i, int j, bool add) {  // O_i (+)= P_i(j) V(j)
-      const uint64_t v = smem_desc(tiles_at + Smem::kV + (j & 1) * Smem::kTileBytes, kBlockBytes);
-#pragma unroll
-      for (int s = 0; s < kKeys / 16; ++s)
-        mma_tmem(at + 256 + i * D, at + i * 128 + s * 8, v + s * (2048 >> 4), instr_desc(D, true, kBf16), add || s > 0, leader);
-    };
-    for (int k = 0; ok && take_work(k); ++k) {
-      const int tiles = sh.work[k % kWorksAhead].tiles;
-      leave_work(k);
-      for (int j = 0; j <= tiles && ok; ++j) {
-        const int jj = base + j;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (j > 0) {
-            ok = ok && mbar_wait(&sh.v_full[(jj - 1) & 1], ((jj - 1) >> 1) & 1, &sh.dead) &&
-                 mbar_wait(&sh.p_full[i], (jj - 1) & 1, &sh.dead);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            fence_after();
-            values(i, jj - 1, j > 1);
-            if (i == 1) commit(&sh.v_empty[(jj - 1) & 1], leader);
-          }
-          if (j < tiles) {
-            ok = (j > 0 || mbar_wait(&sh.q_full[i], k & 1, &sh.dead)) &&
-                 mbar_wait(&sh.k_full[jj & 1], (jj >> 1) & 1, &sh.dead);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            fence_after();
-            scores(i, jj);
-            if (i == 1) commit(&sh.k_empty[jj & 1], leader);
-          } else {
-            commit(&sh.s_full[i], leader);  // O_i is complete
-          }
-        }
-      }
-      base += tiles;
-    }
-    __syncwarp();
   }
   __syncthreads();
   if (warp == kProductWarp) {
@@ -629,7 +722,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
       if (lane == 0) flag_error(p.err, HC_DEVERR_WAIT);
       int32_t no = 0;
       commit(&sh.drain, elect_leader());
-      mbar_wait(&sh.drain, 0, &no);
+      mbar_wait_inline(&sh.drain, 0, &no);
       __syncwarp();
     }
     fence_after();
@@ -670,12 +763,12 @@ cudaError_t pages_map(CUtensorMap* map, const void* pages, const AttendPagedPara
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <bool kBf16, int D, bool kMods>
+template <bool kBf16, int D, Scores kScores>
 cudaError_t launch(const AttendPagedParams& p, cudaStream_t s) {
   static KernelOnDevice kernel;
   int resident = 0;
-  cudaError_t e = kernel.resident(reinterpret_cast<const void*>(k_attend_paged_tiles<kBf16, D, kMods>), kThreadsTiles,
-                                  TileSmem<D>::kAsk, &resident);
+  cudaError_t e = kernel.resident(reinterpret_cast<const void*>(k_attend_paged_tiles<kBf16, D, kScores>), kThreadsTiles,
+                                  Tiles<D>::kAsk, &resident);
   if (e != cudaSuccess) return e;
   CUtensorMap k_map, v_map;
   e = pages_map<kBf16>(&k_map, p.k_pages, p, D);
@@ -684,15 +777,19 @@ cudaError_t launch(const AttendPagedParams& p, cudaStream_t s) {
   const int64_t runs = (static_cast<int64_t>(p.max_new) * p.G + kRowsTile - 1) / kRowsTile;
   const double works = static_cast<double>(runs) * p.n_req * p.H;
   const int grid = works < resident ? static_cast<int>(works) : resident;
-  k_attend_paged_tiles<kBf16, D, kMods><<<grid, kThreadsTiles, TileSmem<D>::kAsk, s>>>(p, k_map, v_map);
+  k_attend_paged_tiles<kBf16, D, kScores><<<grid, kThreadsTiles, Tiles<D>::kAsk, s>>>(p, k_map, v_map);
   return cudaGetLastError();
+}
+
+template <bool kBf16, int D>
+cudaError_t launch_scores(const AttendPagedParams& p, cudaStream_t s) {
+  if (p.slopes) return launch<kBf16, D, kBiased>(p, s);
+  return p.cap_log2 != 0.f ? launch<kBf16, D, kCapped>(p, s) : launch<kBf16, D, kPlain>(p, s);
 }
 
 template <int D>
 cudaError_t launch_type(const AttendPagedParams& p, cudaStream_t s) {
-  const bool mods = p.cap_log2 != 0.f || p.slopes != nullptr;
-  if (p.bf16) return mods ? launch<true, D, true>(p, s) : launch<true, D, false>(p, s);
-  return mods ? launch<false, D, true>(p, s) : launch<false, D, false>(p, s);
+  return p.bf16 ? launch_scores<true, D>(p, s) : launch_scores<false, D>(p, s);
 }
 
 }  // namespace

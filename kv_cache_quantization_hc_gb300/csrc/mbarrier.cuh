@@ -23,7 +23,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t a, uint32_t parity) {
 }
 // Waits for the phase of this parity to end; false when the wait ran out
 // (two seconds), here or elsewhere in the CTA.
-__device__ __noinline__ bool mbar_wait_long(uint32_t a, uint32_t parity, int32_t* dead) {
+__device__ __forceinline__ bool mbar_wait_timed(uint32_t a, uint32_t parity, int32_t* dead) {
   uint64_t start, now;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
   do {
@@ -33,12 +33,24 @@ __device__ __noinline__ bool mbar_wait_long(uint32_t a, uint32_t parity, int32_t
   *static_cast<volatile int32_t*>(dead) = 1;
   return false;
 }
+__device__ __noinline__ bool mbar_wait_long(uint32_t a, uint32_t parity, int32_t* dead) {
+  return mbar_wait_timed(a, parity, dead);
+}
 __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, int32_t* dead) {
   const uint32_t a = mbar_addr(b);
 #pragma unroll 1
   for (int i = 0; i < 32; ++i)
     if (mbar_try(a, parity)) return true;
   return mbar_wait_long(a, parity, dead);
+}
+// The same without a call, for kernels that share registers out anew
+// (setmaxnreg), in which there may be none.
+__device__ __forceinline__ bool mbar_wait_inline(uint64_t* b, uint32_t parity, int32_t* dead) {
+  const uint32_t a = mbar_addr(b);
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try(a, parity)) return true;
+  return mbar_wait_timed(a, parity, dead);
 }
 
 }  // namespace

@@ -46,7 +46,9 @@ struct AttendPagedParams {
   float cap_in, cap_log2;  // softmax_scale / cap and cap * log2(e); cap_log2 0: no cap
   int32_t rows_above;   // requests with more query rows than this go to k_attend_paged_tiles
   int32_t piece_cost;   // of the rows kernel: what a piece's start and end take, in tiles
+  int32_t out32;        // rows of out lie on 32-byte boundaries
   uint8_t* workspace;
+  int32_t* tiles_taken;  // in the workspace: works of the tiles kernel that are taken, CTAs that are done
   int32_t* err;
 };
 
@@ -62,9 +64,10 @@ struct MergeParams {
   FastDivmod by_heads;
 };
 
-// Bytes of the attention's workspace: one counter per CTA of the largest
-// grid, then two partial results per CTA.
-int64_t attend_paged_workspace_bytes();
+// Bytes of the rows kernel's workspace: one counter per CTA of the largest
+// grid, then two partial results per CTA.  The tiles kernel's two counters
+// follow.
+int64_t attend_paged_rows_bytes();
 
 cudaError_t launch_append_paged(int dtype, int pairing, const AppendPagedParams& p, cudaStream_t s);
 // The requests with at most p.rows_above query rows, and those with more.
