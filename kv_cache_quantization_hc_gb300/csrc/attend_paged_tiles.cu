@@ -105,10 +105,11 @@ __device__ __forceinline__ bool at_edge(const Range& v, int key0) { return key0 
 template <int D>
 struct TileShared {
   uint64_t k_full[Tiles<D>::kStages], k_empty[Tiles<D>::kStages], v_full[Tiles<D>::kStages], v_empty[Tiles<D>::kStages],
-      v_edge[Tiles<D>::kStages], s_full[Tiles<D>::kBuffers], p_full[Tiles<D>::kBuffers], q_full[2], q_empty[2], o_full[2][2],
+      v_edge[Tiles<D>::kStages], s_full[Tiles<D>::kBuffers], p_full[Tiles<D>::kBuffers], q_full[2], q_empty[2], o_full[2][2], o_empty[2], l_full[2][2],
       work_full[kWorksAhead], work_empty[kWorksAhead], work_due, drain;
   uint32_t tmem;
   int32_t dead;               // some wait ran out
+  float2 rows[2][kRowsTile];  // of work k at k & 1: a row's reference and sum
   Work work[kWorksAhead];     // work k at k % kWorksAhead
 };
 
@@ -130,6 +131,14 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
       "l"(map), "r"(mbar_addr(b)), "r"(channel), "r"(head), "r"(0), "r"(slot), "r"(leader)
       : "memory");
 }
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, uint64_t* b, int x, int y, int z,
+                                          uint32_t leader) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.u32 q, %6, 0;\n"
+      "@q cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];\n}" ::"r"(dst),
+      "l"(map), "r"(mbar_addr(b)), "r"(x), "r"(y), "r"(z), "r"(leader)
+      : "memory");
+}
 __device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
                "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -145,10 +154,18 @@ __device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
 constexpr int kFewestKeys = 256, kMostRequests = 256;
 struct Cursor {
   int r0 = 0, before = 0;  // first request of 32, works of those before it
-  int upto;                // the works of this class see fewer keys
+  int upto, from;          // this class' works see from `from` up to below `upto` keys
+  // the lane's request, of the 32: read once as long as they stay, counted once a class
+  bool read = false, counted = false;
+  PagedRequest q;
+  int rows, runs, to_end, inc;
+  __device__ __forceinline__ void take_class(const AttendPagedParams& p) {
+    from = p.n_req > kMostRequests || upto <= kFewestKeys ? 0 : upto == INT_MAX ? 1 << 30 : upto >> 1;
+  }
   __device__ __forceinline__ explicit Cursor(const AttendPagedParams& p) {
     const int64_t keys = static_cast<int64_t>(p.table_width) << p.B_log2;
     upto = p.n_req > kMostRequests || keys >= 1 << 30 ? INT_MAX : 1 << (32 - __clz(static_cast<int>(keys)));
+    take_class(p);
   }
 };
 // Runs of 256 rows of a request, of `runs` in all, whose last row's keys end at
@@ -168,50 +185,57 @@ __device__ __forceinline__ int runs_seeing(const AttendPagedParams& p, const Pag
 }
 __device__ __forceinline__ bool find_work(const AttendPagedParams& p, Cursor& c, int idx, int lane, Work& w) {
   for (;;) {
-    const int from = p.n_req > kMostRequests || c.upto <= kFewestKeys ? 0 : c.upto == INT_MAX ? 1 << 30 : c.upto >> 1;
-    for (; c.r0 < p.n_req; c.r0 += 32) {
-      PagedRequest q{0, 0, 0, 0};
+    if (!c.read) {
       int bad = 0;  // lengths are reported by k_attend_paged_rows
-      if (c.r0 + lane < p.n_req) q = load_request(p, c.r0 + lane, bad);
-      const int rows = q.n * p.G > p.rows_above ? q.n * p.G : 0;
-      const int runs = (rows + kRowsTile - 1) / kRowsTile;
-      const int to_end = runs_seeing(p, q, runs, from);
+      c.q = PagedRequest{0, 0, 0, 0};
+      if (c.r0 + lane < p.n_req) c.q = load_request(p, c.r0 + lane, bad);
+      c.rows = c.q.n * p.G > p.rows_above ? c.q.n * p.G : 0;
+      c.runs = (c.rows + kRowsTile - 1) / kRowsTile;
+      c.read = true;
+    }
+    if (!c.counted) {
+      c.to_end = runs_seeing(p, c.q, c.runs, c.from);
       // positions that fall, which are flagged, may make this negative
-      const int works = max(0, to_end - runs_seeing(p, q, runs, c.upto)) * p.H;
-      int inc = works;
+      c.inc = max(0, c.to_end - runs_seeing(p, c.q, c.runs, c.upto)) * p.H;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+        const int v = __shfl_up_sync(0xffffffffu, c.inc, o);
+        if (lane >= o) c.inc += v;
       }
-      const uint32_t upto = __ballot_sync(0xffffffffu, idx < c.before + inc);
-      if (upto == 0) {
-        c.before += __shfl_sync(0xffffffffu, inc, 31);
-        continue;
-      }
+      c.counted = true;
+    }
+    const uint32_t upto = __ballot_sync(0xffffffffu, idx < c.before + c.inc);
+    if (upto != 0) {
       const int src = __ffs(static_cast<int>(upto)) - 1;
       w.r = c.r0 + src;
-      w.rq = {__shfl_sync(0xffffffffu, q.q0, src), __shfl_sync(0xffffffffu, q.n, src),
-              __shfl_sync(0xffffffffu, q.kv, src), __shfl_sync(0xffffffffu, q.prefix, src)};
-      w.rows_all = __shfl_sync(0xffffffffu, rows, src);
-      const int left = __shfl_sync(0xffffffffu, c.before + inc, src) - 1 - idx;  // the last rows first
-      const int run = left / p.H;
+      w.rq = {__shfl_sync(0xffffffffu, c.q.q0, src), __shfl_sync(0xffffffffu, c.q.n, src),
+              __shfl_sync(0xffffffffu, c.q.kv, src), __shfl_sync(0xffffffffu, c.q.prefix, src)};
+      w.rows_all = __shfl_sync(0xffffffffu, c.rows, src);
+      const int left = __shfl_sync(0xffffffffu, c.before + c.inc, src) - 1 - idx;  // the last rows first
+      const int run = static_cast<int>(p.by_heads.div(left));
       w.head = left - run * p.H;
-      w.row0 = (__shfl_sync(0xffffffffu, runs - to_end, src) + run) * kRowsTile;
+      w.row0 = (__shfl_sync(0xffffffffu, c.runs - c.to_end, src) + run) * kRowsTile;
       w.vis = visible<kKeys>(p, w.rq, w.row0, min(w.row0 + kRowsTile, w.rows_all));
       w.tiles = w.vis.tiles;
       return true;
     }
-    if (from == 0) return false;
-    c.upto = from;
-    c.r0 = 0;
+    c.before += __shfl_sync(0xffffffffu, c.inc, 31);
+    c.counted = false;
+    c.r0 += 32;
+    c.read = p.n_req <= 32;
+    if (c.r0 >= p.n_req) {
+      if (c.from == 0) return false;
+      c.upto = c.from;
+      c.take_class(p);
+      c.r0 = 0;
+    }
   }
 }
 
 template <bool kBf16, int D, Scores kScores>
 __global__ void __launch_bounds__(kThreadsTiles, 1)
     k_attend_paged_tiles(const __grid_constant__ AttendPagedParams p, const __grid_constant__ CUtensorMap k_map,
-                         const __grid_constant__ CUtensorMap v_map) {
+                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
   using L = Tiles<D>;
   using Soft = Softmax<kBf16>;
   constexpr int kStages = L::kStages, kBuffers = L::kBuffers;
@@ -234,8 +258,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
       mbar_init(&sh.p_full[i], kHalf);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 64);
+      mbar_init(&sh.q_full[i], p.q_tma ? 1 : 64);
       mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.o_empty[i], 4);
+      mbar_init(&sh.l_full[i][0], kHalf);
+      mbar_init(&sh.l_full[i][1], kHalf);
       mbar_init(&sh.o_full[i][0], 1);
       mbar_init(&sh.o_full[i][1], 1);
     }
@@ -293,6 +320,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         if (kScores == kBiased) slope = p.slopes ? __ldg(p.slopes + head) * kLog2e : 0.f;
       }
 
+      // what a hidden score is overwritten with: -inf once it is multiplied (a factor of 0 would make it NaN)
+      const float factor = p.scale_log2 == 0.f ? 0x1p-126f : p.scale_log2;
+      const uint32_t hidden = __float_as_uint(kScores == kPlain && factor < 0.f ? -kNegInf : kNegInf);
+
       float m = kNegInf, l = 0.f;
       int key0 = tile_key(work.vis, 0);
       for (int j = 0; j < tiles && ok; ++j, key0 -= kKeys) {
@@ -300,7 +331,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         const uint32_t s_at = tmem + lanes + buffer * 128;
         const int lo = first - key0, hi = last - key0;  // columns [lo, hi) count
         // Most tiles: all of it seen, by rows that have a reference.
-        const bool partly = lo > 0 || hi < kKeys, fresh = m == kNegInf && max(lo, 0) < min(hi, kKeys);
+        const bool partly = live && (lo > 0 || hi < kKeys), fresh = live && m == kNegInf && max(lo, 0) < min(hi, kKeys);
         const bool special = __any_sync(0xffffffffu, partly || fresh);
         ok = mbar_wait_inline(&sh.s_full[buffer], (n / kBuffers) & 1, &sh.dead);
         if (!__all_sync(0xffffffffu, ok)) break;
@@ -310,36 +341,86 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           if (kScores == kCapped || (kScores == kBiased && p.cap_log2 != 0.f))
             x = tanh_of(x * p.cap_in) * p.cap_log2;
           else
-            x *= p.scale_log2;
+            x *= factor;
           if (kScores == kBiased) x = fmaf(-slope, fabsf(static_cast<float>(pos - key0) - static_cast<float>(c)), x);
           return x;
         };
-        // P against the reference, and its sum.  It stays in registers until that is known, since it goes over S.
-        uint32_t h[64];
-        auto exponentials = [&](float2 (&v)[8], int c, float2& part) {  // of 16 columns from c on
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[i].x = ex2(v[i].x);
-            v[i].y = ex2(v[i].y);
-            part = __fadd2_rn(part, v[i]);
-            h[c / 2 + i] = pack2(v[i].x, v[i].y);
-          }
+        // Which of 32 columns count, a bit each.
+        auto seen_of = [&](int c) {
+          const int count = min(max(hi - c, 0), 32), skip = min(max(lo - c, 0), 32);
+          return (count == 32 ? ~0u : (1u << count) - 1u) & (skip == 32 ? 0u : ~0u << skip);
         };
-        // Whether no sum is too large, nor a probability for fp16.
-        auto fits = [&](float sum) {
-          bool fit = __all_sync(0xffffffffu, sum < Soft::kMostSum);
-          if (!kBf16 && !fit) {
-            __half2 most = half2_of(h[0]);
-#pragma unroll
-            for (int i = 1; i < 64; ++i) most = __hmax2_nan(most, half2_of(h[i]));
-            fit = __all_sync(0xffffffffu, __hlt(__hmax_nan(__low2half(most), __high2half(most)), __ushort_as_half(0x7c00)));
+        // The row's reference, given its largest score here, and O with it.
+        auto refer = [&](float top, bool crowded) {
+          float ahead = Soft::kAhead;
+          if (!kBf16) {  // n keys in all, fewer than a tile: 128 / n times lower, as n of them do not pass kMostSum either
+            const int all = last - first;
+            if (all < kKeys) ahead -= static_cast<float>(__clz(max(all - 1, 0)) - __clz(kKeys - 1));
           }
-          return fit;
+          const float m_new =
+              top > m + (crowded ? -Soft::kAhead : Soft::kMoveAt) || (m == kNegInf && top > m) ? top + ahead : m;
+          if (__any_sync(0xffffffffu, m_new != m && m != kNegInf)) {  // O of a row without one is 0
+            const float by = m == kNegInf ? 0.f : ex2(m - m_new);
+            l *= by;
+            ok = mbar_wait_inline(&sh.o_full[half][(base + j - 1) & 1], ((base + j - 1) >> 1) & 1, &sh.dead) && ok;
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_load32(o, o_at + c);
+              tmem_wait_load(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+              tmem_store32(o_at + c, o);
+            }
+          }
+          m = m_new;
         };
-        float sum = 0.f;
-        bool done = false, crowded = false;
-        if (!special) {
-          const float off = Soft::kTop - m;
+        // The first keys of a row, or keys that some row does not see: what is hidden is overwritten where it is, and the
+        // largest score found, in a loop that is short in code, as it is seldom in the instruction cache.  With a cap or
+        // a bias, scores are written as they count.
+        float top = kNegInf;
+        const bool first_keys = __any_sync(0xffffffffu, fresh);
+        if (special) {
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 32) {
+            const uint32_t seen = seen_of(c);
+            const bool all = __all_sync(0xffffffffu, seen == ~0u || !live);
+            if (kScores == kPlain && all && !first_keys) continue;
+            uint32_t y[32];
+            if (!__any_sync(0xffffffffu, seen != 0)) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = hidden;
+              tmem_store32(s_at + c, y);
+              continue;
+            }
+            tmem_load32(y, s_at + c);
+            tmem_wait_load(y);
+            if (kScores != kPlain) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(score(__uint_as_float(y[i]), c + i));
+            }
+            if (!all) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = seen & 1u << i ? y[i] : hidden;
+            }
+            if (kScores != kPlain || !all) tmem_store32(s_at + c, y);
+            if (kScores == kPlain && factor < 0.f) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] ^= 0x80000000u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(y[i])), __uint_as_float(y[i + 1]));
+          }
+          wait_store();
+          if (first_keys) refer(kScores == kPlain ? top * fabsf(factor) : top, false);
+        }
+        // P stays in registers until its sum is known, since it goes over S.
+        const bool counted = kScores != kPlain && special;  // scores as they count
+        float sum;
+        uint32_t h[2][32];
+        for (bool moved = first_keys;; moved = true) {
+          const float off = m == kNegInf ? 0.f : Soft::kTop - m;
           float2 part = make_float2(0.f, 0.f);
           uint32_t x[2][16];
           tmem_load16(x[0], s_at);
@@ -348,130 +429,57 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
             uint32_t(&y)[16] = x[c & 1];
             tmem_wait_load16(y);
             if (c < 7) tmem_load16(x[(c & 1) ^ 1], s_at + (c + 1) * 16);
-            float2 v[8];
+            if (kScores != kPlain && !counted) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              v[i] = make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
-              if constexpr (kScores == kPlain)
-                v[i] = __ffma2_rn(v[i], make_float2(p.scale_log2, p.scale_log2), make_float2(off, off));
-              else
-                v[i] = make_float2(score(v[i].x, c * 16 + 2 * i) + off, score(v[i].y, c * 16 + 2 * i + 1) + off);
+              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(score(__uint_as_float(y[i]), c * 16 + i));
             }
-            exponentials(v, c * 16, part);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              float2 v = make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+              v = kScores == kPlain ? __ffma2_rn(v, make_float2(factor, factor), make_float2(off, off))
+                                    : __fadd2_rn(v, make_float2(off, off));
+              v.x = ex2(v.x);
+              v.y = ex2(v.y);
+              part = __fadd2_rn(part, v);
+              h[c / 4][(c % 4) * 8 + i / 2] = pack2(v.x, v.y);
+            }
           }
           sum = part.x + part.y;
-          done = fits(sum);
-          crowded = !done;
-        }
-        // The first keys of a row, keys that some row does not see, or a reference to move: all scores in registers.
-        for (bool moves = crowded || __any_sync(0xffffffffu, fresh); !done; moves = crowded = true) {
-          uint32_t y[8][16];
+          if (moved) break;
+          bool fits = __all_sync(0xffffffffu, sum < Soft::kMostSum || !live);
+          if (!kBf16 && !fits) {  // many keys, or one that fp16 does not hold
+            __half2 most = half2_of(h[0][0]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) tmem_load16(y[c], s_at + c * 16);
-          uint32_t none = 0, some = 0;  // what 16 columns are to the warp: seen by no row, not seen by some
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            none |= __any_sync(0xffffffffu, lo < c * 16 + 16 && hi > c * 16) ? 0u : 1u << c;
-            some |= __all_sync(0xffffffffu, lo <= c * 16 && hi >= c * 16 + 16) ? 0u : 1u << c;
+            for (int i = 1; i < 64; ++i) most = __hmax2_nan(most, half2_of(h[i / 32][i % 32]));
+            fits = __all_sync(0xffffffffu,
+                              __hlt(__hmax_nan(__low2half(most), __high2half(most)), __ushort_as_half(0x7c00)) || !live);
           }
-#pragma unroll
-          for (int c = 0; c < 8; ++c) tmem_wait_load16(y[c]);
-          float top = kNegInf;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (none >> c & 1u) continue;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[c][i] = __float_as_uint(score(__uint_as_float(y[c][i]), c * 16 + i));
-            if (some >> c & 1u) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (c * 16 + i < lo || c * 16 + i >= hi) y[c][i] = __float_as_uint(kNegInf);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(y[c][i]));
-          }
-          if (moves) {  // the reference, and O with it
-            float ahead = Soft::kAhead;
-            if (!kBf16) {  // n keys in all, fewer than a tile: 128 / n times lower, as n of them do not pass kMostSum either
-              const int all = last - first;
-              if (all < kKeys) ahead -= static_cast<float>(__clz(max(all - 1, 0)) - __clz(kKeys - 1));
-            }
-            const float m_new =
-                top > m + (crowded ? -Soft::kAhead : Soft::kMoveAt) || (m == kNegInf && top > m) ? top + ahead : m;
-            if (__any_sync(0xffffffffu, m_new != m && m != kNegInf)) {  // O of a row without one is 0
-              const float by = m == kNegInf ? 0.f : ex2(m - m_new);
-              l *= by;
-              ok = mbar_wait_inline(&sh.o_full[half][(base + j - 1) & 1], ((base + j - 1) >> 1) & 1, &sh.dead) && ok;
-              fence_after();
+          if (fits) break;
+          // scores far above the reference: it moves
+          top = kNegInf;
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tmem_load16(o, o_at + c);
-                tmem_wait_load16(o);
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t y[32];
+            tmem_load32(y, s_at + c);
+            tmem_wait_load(y);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-                tmem_store16(o_at + c, o);
-              }
-            }
-            m = m_new;
+            for (int i = 0; i < 32; ++i)
+              top = fmaxf(top, counted ? __uint_as_float(y[i]) : score(__uint_as_float(y[i]), c + i));
           }
-          const float off = m == kNegInf ? 0.f : Soft::kTop - m;
-          float2 part = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (none >> c & 1u) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) h[c * 8 + i] = 0;
-            } else {
-              float2 v[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                v[i] = __fadd2_rn(make_float2(__uint_as_float(y[c][2 * i]), __uint_as_float(y[c][2 * i + 1])), make_float2(off, off));
-              exponentials(v, c * 16, part);
-            }
-          }
-          sum = part.x + part.y;
-          done = moves || fits(sum);
+          refer(top, true);
         }
-        tmem_store32(s_at, reinterpret_cast<const uint32_t(&)[32]>(h[0]));
-        tmem_store32(s_at + 32, reinterpret_cast<const uint32_t(&)[32]>(h[32]));
+        tmem_store32(s_at, h[0]);
+        tmem_store32(s_at + 32, h[1]);
         l += sum;
         wait_store();
         fence_before();
         mbar_arrive(&sh.p_full[buffer]);
       }
       base += tiles;
-      // ---- the result
-      ok = ok && mbar_wait_inline(&sh.o_full[half][(base - 1) & 1], ((base - 1) >> 1) & 1, &sh.dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      fence_after();
-      const float by = l > 0.f ? 1.f / l : 0.f;
-      uint16_t* const out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(work.rq.q0 + token) * p.o_token +
-                            static_cast<int64_t>(head) * p.o_head;
-      uint32_t x[D / 32][32];
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) tmem_load32(x[c], o_at + c * 32);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) tmem_wait_load(x[c]);
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          w[i] = pack2(__uint_as_float(x[c / 2][c % 2 * 16 + 2 * i]) * by, __uint_as_float(x[c / 2][c % 2 * 16 + 2 * i + 1]) * by);
-        uint16_t* const to = out + c * 16;
-        if (live && p.out32) {
-          store32(to, w);
-        } else if (live) {
-          reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-      }
-      fence_before();
-      if (p.lse && live)
-        p.lse[static_cast<int64_t>(work.rq.q0 + token) * (static_cast<int64_t>(p.H) * p.G) + head] =
-            l > 0.f ? (m - Soft::kTop + log2f(l)) * kLn2 : kNegInf;
+      sh.rows[k & 1][tid] = make_float2(m, l);
+      mbar_arrive(&sh.l_full[half][k & 1]);
       leave_work(k);
     }
   } else {
@@ -647,16 +655,20 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           ++s_tile;
         }
       };
-      auto values = [&](int i, bool add) {  // O_i (+)= P_i(j) V(j)
-        const uint32_t st = p_tile % kStages;
+      // O_i (+)= P_i(j) V(j), for the oldest scores without it.  Scores are up to kBuffers ahead, into the next work.
+      int p_left = 0, p_next = 0;             // products left of the work that they are in, and of the next
+      uint32_t p_done = 0, p_work = 0, p_fresh = 2;  // products so far; that work's number; its products with a new O
+      auto values = [&] {
+        const uint32_t i = p_done & 1, st = p_tile % kStages;
         if (i == 0) wait(&sh.v_full[st], (p_tile / kStages) & 1);
         wait(&sh.p_full[p_buffer], p_parity);
+        if (p_fresh > 0 && p_work > 0) wait(&sh.o_empty[i], (p_work - 1) & 1);  // the last work's O is read
         fence_after();
         const uint64_t v = smem_desc(tiles_at + L::kV + st * L::kTileBytes, kBlockBytes);
 #pragma unroll
         for (int s = 0; s < kKeys / 16; ++s)
           mma_tmem(at + L::kOut + i * D, at + p_buffer * 128 + s * 8, v + s * (2048 >> 4), instr_desc(D, true, kBf16),
-                   add || s > 0, leader);
+                   p_fresh == 0 || s > 0, leader);
         commit(&sh.o_full[i][p_tile & 1], leader);
         if (i == 1) {
           commit(&sh.v_empty[st], leader);
@@ -664,40 +676,76 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         }
         p_parity ^= p_buffer == kBuffers - 1 ? 1 : 0;
         p_buffer = p_buffer == kBuffers - 1 ? 0 : p_buffer + 1;
+        ++p_done;
+        if (p_fresh > 0) --p_fresh;
+        if (--p_left == 0) {
+          p_left = p_next;
+          p_next = 0;
+          p_fresh = 2;
+          ++p_work;
+        }
       };
-      for (int k = 0; take_work(k); ++k) {
+      uint32_t ahead = 0;  // scores whose products are not issued yet
+      for (uint32_t k = 0;; ++k) {
+        if (!take_work(static_cast<int>(k))) break;
         const int count = 2 * __shfl_sync(0xffffffffu, sh.work[k % kWorksAhead].tiles, 0);  // tiles and halves
-        leave_work(k);
+        leave_work(static_cast<int>(k));
+        if (p_left == 0)
+          p_left = count;
+        else
+          p_next = count;
 #pragma unroll 1
-        for (int n = 0; n < count + kBuffers; n += 2) {  // scores n, and probabilities n - kBuffers whose place they take
+        for (int n = 0; n < count; n += 2) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int nn = n + i - kBuffers;
-            if (nn >= 0 && nn < count) values((i + kBuffers) & 1, nn > 1);
-            if (n < count) {
-              if (n == 0) wait(&sh.q_full[i], k & 1);
-              scores(i);
-              if (n == count - 2) commit(&sh.q_empty[i], leader);
+            if (ahead == kBuffers) {
+              values();
+              --ahead;
             }
+            if (n == 0) wait(&sh.q_full[i], k & 1);
+            scores(i);
+            ++ahead;
+            if (n == count - 2) commit(&sh.q_empty[i], leader);
           }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
+        if (!ok) break;
+        // the next work is not there before the last one's result is: its products first
+        for (; p_work < k; --ahead) values();
       }
+      if (ok)
+        for (; ahead > 0; --ahead) values();
+      ok = __all_sync(0xffffffffu, ok);
       __syncwarp();
     } else {
-      // ================================================== queries: two warps a half, of the next work as soon as
-      // the last scores of this one are there
+      // ================================================== queries and results
+      // The next work's queries as soon as the last scores of this one are there, two warps a half; then this one's
+      // result, 32 rows of each half a warp.
       constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;  // 16-byte pieces of a row; rows at a time
-      const int half = (warp - kQueryWarp) >> 1, piece = lane % kLanes;
-      const int row_first = (warp - kQueryWarp) * 64 + lane / kLanes;  // of the 256
-      const uint32_t to = smem_addr(dyn) + L::kQ + half * L::kTileBytes + (piece / 8) * kBlockBytes;
-      for (int k = 0; take_work(k); ++k) {
+      const int quarter = warp - kQueryWarp, piece = lane % kLanes;
+      auto pack2 = [](float lo, float hi) { return kBf16 ? pack_bf16(lo, hi) : pack_f16(lo, hi); };
+      const int q_half = quarter >> 1;
+      const uint32_t q_smem = __shfl_sync(0xffffffffu, smem_addr(dyn), 0) + L::kQ + q_half * L::kTileBytes;
+      int q_sent = 0;
+      auto load_queries = [&](int k) {
         const Work& work = sh.work[k % kWorksAhead];
         const int row0 = work.row0, rows_all = work.rows_all, q0 = work.rq.q0, head = work.head * p.G;
-        leave_work(k);
-        if (k > 0) ok = mbar_wait_inline(&sh.q_empty[half], (k - 1) & 1, &sh.dead);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        const int token0 = q0 + static_cast<int>(p.by_group.div(row0 + q_half * kHalf));
+        if (k > 0) ok = mbar_wait_inline(&sh.q_empty[q_half], (k - 1) & 1, &sh.dead);
+        if (!__all_sync(0xffffffffu, ok)) return;
+        if (p.q_tma) {  // a half is whole tokens: a box of them by their heads.  Rows of other requests do no harm.
+          if (quarter & 1) return;
+          if (lane == 0) mbar_expect(&sh.q_full[q_half], L::kTileBytes);
+          __syncwarp();
+          const uint32_t leader = elect_leader();
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load3(q_smem + c * kBlockBytes, &q_map, &sh.q_full[q_half], c * 64, head, token0, leader);
+          q_sent = k + 1;
+          return;
+        }
+        const int row_first = quarter * 64 + lane / kLanes;  // of the 256
 #pragma unroll 4
         for (int r = 0; r < 64; r += kRowsAt) {
           const int at = row_first + r, row = row0 + at;
@@ -705,13 +753,61 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           const int i = static_cast<int>(p.by_group.div(live ? row : 0));
           const uint16_t* const from = static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(q0 + i) * p.q_token +
                                        static_cast<int64_t>(head + (live ? row : 0) - i * p.G) * p.q_head + piece * 8;
-          cp_async16(to + (at % kHalf) * 128 + (((piece % 8) ^ (at & 7)) << 4), live ? from : static_cast<const uint16_t*>(p.q),
-                     live ? 16 : 0);
+          cp_async16(q_smem + (piece / 8) * kBlockBytes + (at % kHalf) * 128 + (((piece % 8) ^ (at & 7)) << 4),
+                     live ? from : static_cast<const uint16_t*>(p.q), live ? 16 : 0);
         }
         cp_async_commit();
         cp_async_wait<0>();
         fence_async();
-        mbar_arrive(&sh.q_full[half]);
+        mbar_arrive(&sh.q_full[q_half]);
+      };
+      bool more = take_work(0);
+      if (more) load_queries(0);
+      for (int k = 0; more && ok; ++k) {
+        const Work& work = sh.work[k % kWorksAhead];
+        base += work.tiles;
+        more = take_work(k + 1);
+        if (more) load_queries(k + 1);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int at = half * kHalf + quarter * 32 + lane, row = work.row0 + at;
+          const bool live = row < work.rows_all;
+          const int token = static_cast<int>(p.by_group.div(live ? row : 0));
+          const int64_t t = work.rq.q0 + token, head = work.head * p.G + row - token * p.G;
+          uint16_t* const out = static_cast<uint16_t*>(p.out) + t * p.o_token + head * p.o_head;
+          ok = mbar_wait_inline(&sh.l_full[half][k & 1], (k >> 1) & 1, &sh.dead) && ok;
+          ok = mbar_wait_inline(&sh.o_full[half][(base - 1) & 1], ((base - 1) >> 1) & 1, &sh.dead) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          fence_after();
+          const float2 ml = sh.rows[k & 1][at];
+          const float by = ml.y > 0.f ? 1.f / ml.y : 0.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t x[16], w[8];
+            tmem_load16(x, tmem + (static_cast<uint32_t>(quarter) << 21) + L::kOut + half * D + c);
+            tmem_wait_load16(x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = pack2(__uint_as_float(x[2 * i]) * by, __uint_as_float(x[2 * i + 1]) * by);
+            if (live && p.out32) {
+              store32(out + c, w);
+            } else if (live) {
+              reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.o_empty[half]);
+          if (p.lse && live)
+            p.lse[t * (static_cast<int64_t>(p.H) * p.G) + head] =
+                ml.y > 0.f ? (ml.x - Softmax<kBf16>::kTop + log2f(ml.y)) * kLn2 : kNegInf;
+        }
+        if (ok) leave_work(k);
+      }
+      if (!ok && q_sent > 0) {  // a wait ran out: the copy may still be on its way
+        int32_t no = 0;
+        mbar_wait_inline(&sh.q_full[q_half], (q_sent - 1) & 1, &no);
       }
       __syncwarp();
     }
@@ -763,21 +859,40 @@ cudaError_t pages_map(CUtensorMap* map, const void* pages, const AttendPagedPara
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Queries as [token][head][channel], copied 64 channels of a cache head's query heads for as many tokens as make 128
+// rows.  False where that is no box: heads that do not divide 128, or strides that a copy does not take.
+template <bool kBf16>
+bool queries_map(CUtensorMap* map, const AttendPagedParams& p, int d) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode || kHalf % p.G) return false;
+  const int64_t heads = static_cast<int64_t>(p.H) * p.G;
+  const cuuint64_t sizes[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(p.n_tokens)};
+  // of one head or token the stride is not used, and may be anything
+  const int64_t head = heads > 1 ? 2 * p.q_head : 2 * d, token = p.n_tokens > 1 ? 2 * p.q_token : 2 * d;
+  if (head <= 0 || token <= 0 || head >= int64_t{1} << 40 || token >= int64_t{1} << 40) return false;
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head), static_cast<cuuint64_t>(token)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(kHalf / p.G)}, step[3] = {1, 1, 1};
+  return encode(map, kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p.q),
+                sizes, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool kBf16, int D, Scores kScores>
-cudaError_t launch(const AttendPagedParams& p, cudaStream_t s) {
+cudaError_t launch(AttendPagedParams p, cudaStream_t s) {
   static KernelOnDevice kernel;
   int resident = 0;
   cudaError_t e = kernel.resident(reinterpret_cast<const void*>(k_attend_paged_tiles<kBf16, D, kScores>), kThreadsTiles,
                                   Tiles<D>::kAsk, &resident);
   if (e != cudaSuccess) return e;
-  CUtensorMap k_map, v_map;
+  CUtensorMap k_map, v_map, q_map = {};
   e = pages_map<kBf16>(&k_map, p.k_pages, p, D);
   if (e == cudaSuccess) e = pages_map<kBf16>(&v_map, p.v_pages, p, D);
   if (e != cudaSuccess) return e;
+  p.q_tma = queries_map<kBf16>(&q_map, p, D);
   const int64_t runs = (static_cast<int64_t>(p.max_new) * p.G + kRowsTile - 1) / kRowsTile;
   const double works = static_cast<double>(runs) * p.n_req * p.H;
   const int grid = works < resident ? static_cast<int>(works) : resident;
-  k_attend_paged_tiles<kBf16, D, kScores><<<grid, kThreadsTiles, Tiles<D>::kAsk, s>>>(p, k_map, v_map);
+  k_attend_paged_tiles<kBf16, D, kScores><<<grid, kThreadsTiles, Tiles<D>::kAsk, s>>>(p, k_map, v_map, q_map);
   return cudaGetLastError();
 }
 
