@@ -31,7 +31,8 @@
 //   otherwise.  fp16 ends at 65504: top = 11.5, m is 3 above the maximum and
 //   moves when that exceeds m by 3.5 or a tile's sum passes 60000; a
 //   probability keeps 11 bits down to 2^-22 of the largest.  Rows that see n
-//   keys in all, fewer than a tile, have m 128 / n times lower.
+//   keys in all, fewer than a tile, have m 128 / n times lower; rows that see n
+//   in their first tile and more later, sqrt(128 / n) times higher.
 //
 // Bound: the tensor cores (4 d flops per row and key).
 #include <algorithm>
@@ -138,6 +139,46 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
       "@q cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];\n}" ::"r"(dst),
       "l"(map), "r"(mbar_addr(b)), "r"(x), "r"(y), "r"(z), "r"(leader)
       : "memory");
+}
+// Two fp32 in a register pair, kept as one value: left to itself the compiler makes a constant's pair anew for each use.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+  Pair d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ Pair fixed_pair(float a) {
+  Pair d;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(a));
+  return d;
+}
+__device__ __forceinline__ float2 floats_of(Pair p) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float largest(const uint32_t (&y)[32]) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = fmaxf(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+#pragma unroll
+  for (int i = 8; i < 32; i += 2) m[i / 2 % 4] = max3(m[i / 2 % 4], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 __device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
@@ -322,7 +363,25 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
 
       // what a hidden score is overwritten with: -inf once it is multiplied (a factor of 0 would make it NaN)
       const float factor = p.scale_log2 == 0.f ? 0x1p-126f : p.scale_log2;
-      const uint32_t hidden = __float_as_uint(kScores == kPlain && factor < 0.f ? -kNegInf : kNegInf);
+      uint32_t hidden = __float_as_uint(kScores == kPlain && factor < 0.f ? -kNegInf : kNegInf);
+      // cap * tanh(s * cap_in) up to |s * cap_in| = 3/4 as an odd polynomial in s: the minimax fit of tanh(y) / y in y^2
+      // by Remez' exchange, off by 2.9e-8, with the factors in its terms; its last term is negative, so that a score
+      // of y = 1000 is one that no probability comes of.  Factors whose powers fp32 does not hold do without.
+      Pair tanh_terms[6];
+      float tanh_reach = -1.f;
+      if constexpr (kScores == kCapped) {
+        constexpr float kTerms[6] = {0.999999971015f, -0.333329588875f, 0.13325406137f,
+                                     -0.0533444364837f, 0.0195829218425f, -0.0047162673917f};
+        const float t = p.cap_in * p.cap_in;
+        float power = p.scale_log2;
+#pragma unroll
+        for (int k = 0; k < 6; ++k) {
+          tanh_terms[k] = fixed_pair(kTerms[k] * power);
+          power *= t;
+        }
+        if (t >= 1e-6f && t <= 1e6f) tanh_reach = 0.5625f / t;
+        hidden = __float_as_uint(1000.f / p.cap_in);
+      }
 
       float m = kNegInf, l = 0.f;
       int key0 = tile_key(work.vis, 0);
@@ -353,9 +412,13 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         // The row's reference, given its largest score here, and O with it.
         auto refer = [&](float top, bool crowded) {
           float ahead = Soft::kAhead;
-          if (!kBf16) {  // n keys in all, fewer than a tile: 128 / n times lower, as n of them do not pass kMostSum either
-            const int all = last - first;
-            if (all < kKeys) ahead -= static_cast<float>(__clz(max(all - 1, 0)) - __clz(kKeys - 1));
+          if (!kBf16) {
+            const auto steps = [](int n) { return static_cast<float>(__clz(max(n - 1, 0)) - __clz(kKeys - 1)); };  // log2(128 / n)
+            const int all = last - first, here = min(hi, kKeys) - max(lo, 0);
+            if (all < kKeys)  // few keys in all: as much lower, as n of them do not pass kMostSum either
+              ahead -= steps(all);
+            else if (here < kKeys)  // few keys here: half as much higher, as larger ones may follow
+              ahead += 0.5f * steps(here);
           }
           const float m_new =
               top > m + (crowded ? -Soft::kAhead : Soft::kMoveAt) || (m == kNegInf && top > m) ? top + ahead : m;
@@ -377,11 +440,12 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           m = m_new;
         };
         // The first keys of a row, or keys that some row does not see: what is hidden is overwritten where it is, and the
-        // largest score found, in a loop that is short in code, as it is seldom in the instruction cache.  With a cap or
-        // a bias, scores are written as they count.
-        float top = kNegInf;
+        // largest score found (a cap does not change which it is), in a loop that is short in code, as it is seldom in
+        // the instruction cache.  With a bias, scores are written as they count.
+        float top = kNegInf, most = 0.f;  // most: of the scores' magnitudes
         const bool first_keys = __any_sync(0xffffffffu, fresh);
-        if (special) {
+        bool counted = kScores == kBiased && (special || p.cap_log2 != 0.f);
+        if (special || counted) {
 #pragma unroll 1
           for (int c = 0; c < kKeys; c += 32) {
             const uint32_t seen = seen_of(c);
@@ -396,32 +460,69 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
             }
             tmem_load32(y, s_at + c);
             tmem_wait_load(y);
-            if (kScores != kPlain) {
+            if (kScores == kBiased) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(score(__uint_as_float(y[i]), c + i));
             }
-            if (!all) {
+            if (kScores == kCapped) {
+              uint32_t z[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[i] = seen & 1u << i ? y[i] & 0x7fffffffu : 0u;
+              most = fmaxf(most, largest(z));
+            }
+            const uint32_t lowest = __float_as_uint(factor < 0.f ? -kNegInf : kNegInf);
+            if (kScores == kCapped && !all) {  // looked through as -inf, written as `hidden`
+              uint32_t z[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                z[i] = seen & 1u << i ? y[i] : hidden;
+                y[i] = seen & 1u << i ? y[i] : lowest;
+              }
+              tmem_store32(s_at + c, z);
+            } else if (!all) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) y[i] = seen & 1u << i ? y[i] : hidden;
             }
-            if (kScores != kPlain || !all) tmem_store32(s_at + c, y);
-            if (kScores == kPlain && factor < 0.f) {
+            if (kScores == kBiased || (kScores == kPlain && !all)) tmem_store32(s_at + c, y);
+            if (kScores != kBiased && factor < 0.f) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) y[i] ^= 0x80000000u;
             }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(y[i])), __uint_as_float(y[i + 1]));
+            top = fmaxf(top, largest(y));
           }
           wait_store();
-          if (first_keys) refer(kScores == kPlain ? top * fabsf(factor) : top, false);
+          if (first_keys) {
+            if (kScores == kPlain) top *= fabsf(factor);
+            if (kScores == kCapped && top != kNegInf) top = score(factor < 0.f ? -top : top, 0);
+            refer(top, false);
+          }
         }
+        // Scores beyond the polynomial's reach: written as they count.
+        auto count = [&] {
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 32) {
+            const uint32_t seen = seen_of(c);
+            uint32_t y[32];
+            tmem_load32(y, s_at + c);
+            tmem_wait_load(y);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              y[i] = __float_as_uint(seen & 1u << i ? score(__uint_as_float(y[i]), c + i) : kNegInf);
+            tmem_store32(s_at + c, y);
+          }
+          wait_store();
+          counted = true;
+        };
+        if (kScores == kCapped && special && !__all_sync(0xffffffffu, most * most <= tanh_reach || !live)) count();
         // P stays in registers until its sum is known, since it goes over S.
-        const bool counted = kScores != kPlain && special;  // scores as they count
-        float sum;
+        float sum, reach;
         uint32_t h[2][32];
-        for (bool moved = first_keys;; moved = true) {
+        auto probabilities = [&](auto as_counted) {
+          constexpr bool kCounted = decltype(as_counted)::value;
           const float off = m == kNegInf ? 0.f : Soft::kTop - m;
+          [[maybe_unused]] const Pair off2 = kScores == kCapped && !kCounted ? fixed_pair(off) : 0;
           float2 part = make_float2(0.f, 0.f);
+          float far[4] = {0.f, 0.f, 0.f, 0.f};  // four, so that one need not wait for the other
           uint32_t x[2][16];
           tmem_load16(x[0], s_at);
 #pragma unroll
@@ -429,30 +530,70 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
             uint32_t(&y)[16] = x[c & 1];
             tmem_wait_load16(y);
             if (c < 7) tmem_load16(x[(c & 1) ^ 1], s_at + (c + 1) * 16);
-            if (kScores != kPlain && !counted) {
+            float2 v[8];
+            if constexpr (!kCounted && kScores == kCapped) {
+              Pair s2[8], u2[8], t2[8];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(score(__uint_as_float(y[i]), c * 16 + i));
+              for (int i = 0; i < 8; ++i) {
+                s2[i] = pair_of(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+                u2[i] = mul2(s2[i], s2[i]);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 u = floats_of(u2[i]);
+                far[i & 3] = max3(far[i & 3], u.x, u.y);
+                t2[i] = fma2(tanh_terms[5], u2[i], tanh_terms[4]);
+              }
+#pragma unroll
+              for (int k = 3; k >= 0; --k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) t2[i] = fma2(t2[i], u2[i], tanh_terms[k]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = floats_of(fma2(s2[i], t2[i], off2));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                v[i] = make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+                if constexpr (kCounted) {
+                  v[i] = __fadd2_rn(v[i], make_float2(off, off));
+                } else {
+                  v[i] = __ffma2_rn(v[i], make_float2(factor, factor), make_float2(off, off));
+                  if (kScores == kBiased) {
+                    const float away = static_cast<float>(pos - key0);
+                    v[i].x = fmaf(-slope, fabsf(away - static_cast<float>(c * 16 + 2 * i)), v[i].x);
+                    v[i].y = fmaf(-slope, fabsf(away - static_cast<float>(c * 16 + 2 * i + 1)), v[i].y);
+                  }
+                }
+              }
             }
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float2 v = make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-              v = kScores == kPlain ? __ffma2_rn(v, make_float2(factor, factor), make_float2(off, off))
-                                    : __fadd2_rn(v, make_float2(off, off));
-              v.x = ex2(v.x);
-              v.y = ex2(v.y);
-              part = __fadd2_rn(part, v);
-              h[c / 4][(c % 4) * 8 + i / 2] = pack2(v.x, v.y);
+            for (int i = 0; i < 8; ++i) {
+              v[i].x = ex2(v[i].x);
+              v[i].y = ex2(v[i].y);
+              part = __fadd2_rn(part, v[i]);
+              h[c / 4][(c % 4) * 8 + i] = pack2(v[i].x, v[i].y);
             }
           }
           sum = part.x + part.y;
+          reach = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3]));
+        };
+        for (bool moved = first_keys;;) {
+          if (kScores != kPlain && counted)
+            probabilities(std::true_type());
+          else
+            probabilities(std::false_type());
+          if (kScores == kCapped && !special && !counted && !__all_sync(0xffffffffu, reach <= tanh_reach || !live)) {
+            count();
+            continue;
+          }
           if (moved) break;
           bool fits = __all_sync(0xffffffffu, sum < Soft::kMostSum || !live);
           if (!kBf16 && !fits) {  // many keys, or one that fp16 does not hold
-            __half2 most = half2_of(h[0][0]);
+            __half2 high = half2_of(h[0][0]);
 #pragma unroll
-            for (int i = 1; i < 64; ++i) most = __hmax2_nan(most, half2_of(h[i / 32][i % 32]));
+            for (int i = 1; i < 64; ++i) high = __hmax2_nan(high, half2_of(h[i / 32][i % 32]));
             fits = __all_sync(0xffffffffu,
-                              __hlt(__hmax_nan(__low2half(most), __high2half(most)), __ushort_as_half(0x7c00)) || !live);
+                              __hlt(__hmax_nan(__low2half(high), __high2half(high)), __ushort_as_half(0x7c00)) || !live);
           }
           if (fits) break;
           // scores far above the reference: it moves
@@ -462,11 +603,19 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
             uint32_t y[32];
             tmem_load32(y, s_at + c);
             tmem_wait_load(y);
+            if (kScores == kCapped && !counted) {
+              const uint32_t seen = seen_of(c), sign = factor < 0.f ? 0x80000000u : 0u;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              top = fmaxf(top, counted ? __uint_as_float(y[i]) : score(__uint_as_float(y[i]), c + i));
+              for (int i = 0; i < 32; ++i) y[i] = seen & 1u << i ? y[i] ^ sign : __float_as_uint(kNegInf);
+            } else if (kScores == kPlain || !counted) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(score(__uint_as_float(y[i]), c + i));
+            }
+            top = fmaxf(top, largest(y));
           }
+          if (kScores == kCapped && !counted && top != kNegInf) top = score(factor < 0.f ? -top : top, 0);
           refer(top, true);
+          moved = true;
         }
         tmem_store32(s_at, h[0]);
         tmem_store32(s_at + 32, h[1]);
