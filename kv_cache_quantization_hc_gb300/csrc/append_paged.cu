@@ -2,119 +2,151 @@
 // copied, in one launch.  Memory-bound: q, k, v read once, q_out and the
 // buffer's rows written once.
 //
-// A warp takes some heads of a token: of its queries, its keys or its values.
-// Rotated rows go as k_rope_axes takes them, (cos, sin) in registers where a
-// row's pieces divide the warp and in shared memory where they do not; a row of
-// the buffer is a token's heads side by side.
+// A warp takes some heads of a token's queries, keys or values, and the same
+// heads of later tokens.  A lane has the same pieces of every row (lanes are
+// left over where a partial rotation's pieces are no power of two), so what it
+// needs of (cos, sin) is in registers, and the next token's rows are on their
+// way while this one's are turned.
+//
+// 8197 tokens of 32 query and 8 cache heads of 128 channels: fp16, interleaved
+// pairs 43 us of 30 that the bytes take at the copy rate; bf16 55, with pairs half
+// a rotation apart 58; fp32 71 of 60.  Bound by latency: a token's positions, then
+// its (cos, sin), then 400 instructions, by 16 warps an SM (120 registers; 24 warps
+// at 80 spill: 57 us instead of 43; half as many rows in hand, 46 to 75).  A warp
+// for each token, without the next one's rows on their way: 45 us.
+#include <algorithm>
+
 #include "paged.cuh"
 #include "rope.cuh"
 
 namespace hc {
 namespace {
 
-// Whether the token's positions are in the table (a lane per axis).
-__device__ __forceinline__ bool positions_exist(const RopeParams& p, int64_t t, int lane) {
-  bool ok = true;
-  if (p.table != nullptr && (p.axes >> lane & 1u)) {
-    const int pos = __ldg(p.positions + lane * p.position_stride + t);
-    ok = pos >= 0 && pos < p.n_positions;
-  }
-  return __all_sync(0xffffffffu, ok);
+// Rows that a lane has in hand of a token: 16 registers of them, as many again of the next token's.
+template <int kPairing>
+constexpr int kRowsInHand = kPairing == HC_PAIR_HALF_SPLIT ? 2 : 4;
+
+// Some heads of the queries, keys or values: where they are, where they go, and whether they turn.
+template <typename T>
+struct Part {
+  const T* from;
+  T* to;
+  int64_t from_token, from_head, to_head;
+  int h0, h1;
+  bool queries, turns;
+};
+template <typename T>
+__device__ __forceinline__ Part<T> part_of(const AppendPagedParams& p, int part) {
+  Part<T> w;
+  w.queries = part < p.q_parts;
+  const bool keys = !w.queries && part < p.q_parts + p.kv_parts;
+  w.turns = p.rope.table != nullptr && (w.queries || keys);
+  part -= w.queries ? 0 : keys ? p.q_parts : p.q_parts + p.kv_parts;
+  w.h0 = part * p.heads_per_warp;
+  w.h1 = min(w.h0 + p.heads_per_warp, w.queries ? p.n_q_heads : p.H);
+  w.from = static_cast<const T*>(w.queries ? p.q : keys ? p.k : p.v);
+  w.to = static_cast<T*>(w.queries ? p.q_out : keys ? p.k_pages : p.v_pages);
+  w.from_token = w.queries ? p.q_token : keys ? p.k_token : p.v_token;
+  w.from_head = w.queries ? p.q_head : keys ? p.k_head : p.v_head;
+  w.to_head = w.queries ? p.o_head : p.d;
+  return w;
+}
+// Where a token's rows of a part go, given its row in the pages, which exists.
+template <typename T>
+__device__ __forceinline__ T* destination(const AppendPagedParams& p, const Part<T>& w, int64_t t, int64_t row) {
+  if (w.queries) return w.to + t * p.o_token;
+  return w.to + (row >> p.B_log2) * p.slot_stride + (row & ((1 << p.B_log2) - 1)) * (static_cast<int64_t>(p.H) * p.d);
 }
 
-template <typename T, int kPairing, bool kInLanes>
-__global__ void __launch_bounds__(kRopeWarps * 32) k_append_paged(const __grid_constant__ AppendPagedParams p) {
-  constexpr int V = 16 / sizeof(T);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t tok, part_of;
-  p.parts.divmod(blockIdx.x * kRopeWarps + warp, tok, part_of);
-  if (tok >= static_cast<uint32_t>(p.n_tokens)) return;
-  const int64_t t = tok;
-  int part = static_cast<int>(part_of);
-  // asked after the data is on its way: what is read is there whatever the row says
-  const int64_t row = __ldg(p.token_rows + t);
-  const bool row_ok = row >= -1 && row < p.n_rows;
-  const T *x;
-  T* y;
-  int64_t x_head, y_head;
-  int heads;
-  if (part < p.q_parts) {
-    x = static_cast<const T*>(p.q) + t * p.q_token;
-    y = static_cast<T*>(p.q_out) + t * p.o_token;
-    x_head = p.q_head;
-    y_head = p.o_head;
-    heads = p.n_q_heads;
-  } else {
-    part -= p.q_parts;
-    const bool keys = part < p.kv_parts;
-    if (!keys) part -= p.kv_parts;
-    x = keys ? static_cast<const T*>(p.k) + t * p.k_token : static_cast<const T*>(p.v) + t * p.v_token;
-    x_head = keys ? p.k_head : p.v_head;
-    y_head = p.d;
-    heads = p.H;
-    // rows that are not there (and a padding token's) are not written: see below
-    const int64_t slot = row >> p.B_log2, in_slot = row & ((1 << p.B_log2) - 1);
-    y = static_cast<T*>(keys ? p.k_pages : p.v_pages) + slot * p.slot_stride + in_slot * (static_cast<int64_t>(p.H) * p.d);
-    if (!keys) {
-      const int h0 = part * p.heads_per_warp, h1 = min(h0 + p.heads_per_warp, heads);
-      const int pieces = p.d / V, total = (h1 - h0) * pieces;  // pieces of a row: a power of two
-      constexpr int kUnroll = 4;
-      bool allowed = false, asked = false;
-      for (int first = lane; first < total + lane; first += 32 * kUnroll) {  // the same for all lanes
-        Piece<T, V> a[kUnroll];
+template <typename T, int kPairing>
+__global__ void __launch_bounds__(kRopeWarps * 32, 2) k_append_paged(const __grid_constant__ AppendPagedParams p) {
+  constexpr int V = 16 / sizeof(T), R = kRowsInHand<kPairing>;
+  constexpr bool kSplit = kPairing == HC_PAIR_HALF_SPLIT;
+  using Item = LaneItem<T, kPairing, V>;
+  const int lane = threadIdx.x & 31;
+  uint32_t first, part;
+  p.parts.divmod(blockIdx.x * kRopeWarps + (threadIdx.x >> 5), first, part);
+  if (first >= static_cast<uint32_t>(p.token_step)) return;
+  const Part<T> w = part_of<T>(p, static_cast<int>(part));
+  const Item item(lane, p.lanes_per_row, p.rope.half);
+  const PairAxes<Item::kPairs> axes(p.rope, item.first_pair(), item.rotates);
+  const T* const from = w.from + (w.h0 + item.sub) * w.from_head + item.c;
+  const int heads = item.it < p.items ? w.h1 - w.h0 - item.sub : 0;  // of this lane, every at_once-th
+  struct {
+    Piece<T, V> a[R], b[R];
+    int64_t row;
+    int pos;
+  } in[2];
+  auto fetch = [&](auto& to, int64_t t) {
+    const T* x = from + t * w.from_token;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int i = first + u * 32;
-          if (i < total) a[u] = load_piece<T, V>(x + (h0 + i / pieces) * x_head + (i & (pieces - 1)) * V);
-        }
-        if (!asked) {
-          const bool pos_ok = positions_exist(p.rope, t, lane);
-          allowed = pos_ok && row_ok && row >= 0;
-          asked = true;
-          if (lane == 0) flag_error(p.err, (pos_ok ? 0 : HC_DEVERR_POS) | (row_ok ? 0 : HC_DEVERR_SLOT));
-        }
-        if (!allowed) return;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int i = first + u * 32;
-          if (i < total) store_piece<T, V>(y + (h0 + i / pieces) * y_head + (i & (pieces - 1)) * V, a[u]);
-        }
+    for (int u = 0; u < R; ++u)
+      if (u * item.at_once < heads) {
+        to.a[u] = load_piece<T, V>(x + u * item.at_once * w.from_head);
+        if (kSplit && item.rotates) to.b[u] = load_piece<T, V>(x + u * item.at_once * w.from_head + item.half);
       }
-      return;
+    to.row = __ldg(p.token_rows + t);
+    to.pos = p.rope.table != nullptr ? lane_position(p.rope, static_cast<int>(t), lane) : 0;
+  };
+  int64_t t = first;
+  fetch(in[0], t);
+  for (;;) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      auto& now = in[s];
+      if (t + p.token_step < p.n_tokens) fetch(in[s ^ 1], t + p.token_step);
+      const bool known = p.rope.table == nullptr || positions_exist(p.rope, now.pos, lane);
+      const bool exists = now.row >= -1 && now.row < p.n_rows;
+      if (lane == 0) flag_error(p.err, (known ? 0 : HC_DEVERR_POS) | (exists ? 0 : HC_DEVERR_SLOT));
+      if (known && exists && (w.queries || now.row >= 0)) {
+        float2 cs[Item::kPairs];
+        if (w.turns) turns_at(p.rope, axes, now.pos, item.first_pair(), item.rotates, cs);
+        T* y = destination(p, w, t, now.row) + (w.h0 + item.sub) * w.to_head + item.c;
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+          if (u * item.at_once < heads) {
+            T* to = y + u * item.at_once * w.to_head;
+            if (w.turns && item.rotates) {
+              float x[V], x2[V];
+              widen_piece(now.a[u], x);
+              if (kSplit) widen_piece(now.b[u], x2);
+#pragma unroll
+              for (int i = 0; i < Item::kPairs; ++i)
+                turn(kSplit ? x[i] : x[2 * i], kSplit ? x2[i] : x[2 * i + 1], cs[i]);
+              narrow_piece(x, now.a[u]);
+              if (kSplit) narrow_piece(x2, now.b[u]);
+            }
+            store_piece<T, V>(to, now.a[u]);
+            if (kSplit && item.rotates) store_piece<T, V>(to + item.half, now.b[u]);
+          }
+      }
+      t += p.token_step;
+      if (t >= p.n_tokens) return;
     }
   }
-  const bool writes = row_ok && (part_of < static_cast<uint32_t>(p.q_parts) || row >= 0);
-  if (!row_ok && lane == 0) flag_error(p.err, HC_DEVERR_SLOT);
-  const int h0 = part * p.heads_per_warp, h1 = min(h0 + p.heads_per_warp, heads);
-  bool ok;
-  if constexpr (kInLanes) {
-    ok = rotate_rows_in_lanes<T, kPairing, V>(p.rope, static_cast<int>(t), x, x_head, y, y_head, h0, h1,
-                                              static_cast<int>(p.items_per_row.d), lane, [&] { return writes; });
-  } else {
-    __shared__ float2 cs[kRopeWarps][64];
-    ok = stage_cos_sin(p.rope, static_cast<int>(t), lane, cs[warp]);
-    if (ok && writes)
-      rotate_rows<T, kPairing, V, 4>(x, x_head, y, y_head, h0, h1, p.rope.half, cs[warp], p.items_per_row, lane);
-  }
-  if (!ok && lane == 0) flag_error(p.err, HC_DEVERR_POS);
 }
 
 template <typename T, int kPairing>
 cudaError_t launch(AppendPagedParams p, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const int items = rope_items<kPairing, V>(p.rope.half, p.d);
-  p.items_per_row = FastDivmod(static_cast<uint32_t>(items));
-  const bool in_lanes = items <= 32 && 32 % items == 0;
-  p.heads_per_warp = heads_per_warp(p.n_tokens, p.n_q_heads + 2 * p.H, items, in_lanes);
+  p.items = rope_items<kPairing, V>(p.rope.half, p.d);
+  p.lanes_per_row = 1;
+  while (p.lanes_per_row < p.items) p.lanes_per_row *= 2;  // at most 32: of 128 fp32 channels
+  p.heads_per_warp = std::min(std::max(p.n_q_heads, p.H), kRowsInHand<kPairing> * (32 / p.lanes_per_row));
   p.q_parts = (p.n_q_heads + p.heads_per_warp - 1) / p.heads_per_warp;
   p.kv_parts = (p.H + p.heads_per_warp - 1) / p.heads_per_warp;
   p.parts = FastDivmod(static_cast<uint32_t>(p.q_parts + 2 * p.kv_parts));
-  const int64_t warps = static_cast<int64_t>(p.n_tokens) * p.parts.d;
+  // as many warps as the device holds at once, each with every token_step-th token
+  static KernelOnDevice kernel;
+  int resident = 0;
+  const cudaError_t e =
+      kernel.resident(reinterpret_cast<const void*>(k_append_paged<T, kPairing>), kRopeWarps * 32, 0, &resident);
+  if (e != cudaSuccess) return e;
+  p.token_step = static_cast<int32_t>(
+      std::min<int64_t>(p.n_tokens, std::max<int64_t>(1, int64_t{resident} * kRopeWarps / p.parts.d)));
+  const int64_t warps = static_cast<int64_t>(p.token_step) * p.parts.d;
   const unsigned grid = static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps);
-  if (in_lanes)
-    k_append_paged<T, kPairing, true><<<grid, kRopeWarps * 32, 0, s>>>(p);
-  else
-    k_append_paged<T, kPairing, false><<<grid, kRopeWarps * 32, 0, s>>>(p);
+  k_append_paged<T, kPairing><<<grid, kRopeWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 

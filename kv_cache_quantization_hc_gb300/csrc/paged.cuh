@@ -17,8 +17,9 @@ struct AppendPagedParams {
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
   int64_t slot_stride;  // elements
   int32_t n_tokens, n_q_heads, H, d, B_log2;
-  int32_t heads_per_warp, q_parts, kv_parts;
-  FastDivmod parts, items_per_row;  // warps of a token; pieces of a row
+  int32_t heads_per_warp, q_parts, kv_parts, token_step;
+  int32_t items, lanes_per_row;  // pieces of a row, and the lanes that take them
+  FastDivmod parts;              // warps of a token
   const int64_t* token_rows;
   int64_t n_rows;  // num_slots * block_size
   int32_t* err;

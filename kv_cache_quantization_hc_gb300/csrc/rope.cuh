@@ -83,40 +83,47 @@ __device__ __forceinline__ void store_piece(T* p, const Piece<T, V>& r) {
   }
 }
 
-// (cos, sin) of pairs first..first+N-1 for token t, in registers; false if a
-// position that some pair needs is outside the table (nothing is read for it).
-// Called by whole warps with N pairs for each lane.
+// A lane's position of token t, of the axis that is its number; false if a
+// position that some pair needs is outside the table.  Called by whole warps.
+__device__ __forceinline__ int lane_position(const RopeParams& p, int t, int lane) {
+  return p.axes >> lane & 1u ? __ldg(p.positions + lane * p.position_stride + t) : 0;
+}
+__device__ __forceinline__ bool positions_exist(const RopeParams& p, int pos, int lane) {
+  return __all_sync(0xffffffffu, !(p.axes >> lane & 1u) || (pos >= 0 && pos < p.n_positions));
+}
+// The axes of pairs first..first+N-1, which differ from lane to lane: a kernel
+// that takes several tokens looks them up once.  Called by whole warps.
 template <int N>
-__device__ __forceinline__ bool load_turns(const RopeParams& p, int t, int first, bool rotates, int lane,
-                                           float2 (&cs)[N]) {
-  int pos = 0;
-  bool ok = true;
-  if (p.axes >> lane & 1u) {  // a lane per axis
-    pos = __ldg(p.positions + lane * p.position_stride + t);
-    ok = pos >= 0 && pos < p.n_positions;
-  }
-  ok = __all_sync(0xffffffffu, ok);
-  if (!ok) return false;
-  // the pairs' axes, 4 bytes at a time (N and first are even, or N is 1)
+struct PairAxes {
   uint32_t axis[N];
-  bool same = true;
-  if constexpr (N % 4 == 0) {
+  bool same;  // for every lane, all its pairs have one axis
+  __device__ __forceinline__ PairAxes(const RopeParams& p, int first, bool rotates) {
+    same = true;
+    // 4 bytes at a time (N and first are even, or N is 1)
+    if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint32_t w = rotates ? *reinterpret_cast<const uint32_t*>(p.pair_axis + first + i) : 0u;
+      for (int i = 0; i < N; i += 4) {
+        const uint32_t w = rotates ? *reinterpret_cast<const uint32_t*>(p.pair_axis + first + i) : 0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) axis[i + j] = __byte_perm(w, 0, 0x4440 + j);
-      same = same && w == axis[0] * 0x01010101u;
+        for (int j = 0; j < 4; ++j) axis[i + j] = __byte_perm(w, 0, 0x4440 + j);
+        same = same && w == axis[0] * 0x01010101u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        axis[i] = rotates ? p.pair_axis[first + i] : 0u;
+        same = same && axis[i] == axis[0];
+      }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      axis[i] = rotates ? p.pair_axis[first + i] : 0u;
-      same = same && axis[i] == axis[0];
-    }
+    same = N % 2 == 0 && p.pairs16 && __all_sync(0xffffffffu, same);
   }
-  if (N % 2 == 0 && p.pairs16 && __all_sync(0xffffffffu, same)) {
-    const int at = __shfl_sync(0xffffffffu, pos, axis[0]);
+};
+// (cos, sin) of these pairs at the lanes' positions, which exist, in registers.
+template <int N>
+__device__ __forceinline__ void turns_at(const RopeParams& p, const PairAxes<N>& axes, int pos, int first, bool rotates,
+                                         float2 (&cs)[N]) {
+  if (axes.same) {
+    const int at = __shfl_sync(0xffffffffu, pos, axes.axis[0]);
     if (rotates) {
       const float4* src = reinterpret_cast<const float4*>(p.table + static_cast<int64_t>(at) * p.half + first);
 #pragma unroll
@@ -129,7 +136,7 @@ __device__ __forceinline__ bool load_turns(const RopeParams& p, int t, int first
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int at = __shfl_sync(0xffffffffu, pos, axis[i]);
+      const int at = __shfl_sync(0xffffffffu, pos, axes.axis[i]);
       if (rotates) cs[i] = __ldg(p.table + static_cast<int64_t>(at) * p.half + first + i);
     }
   }
@@ -137,6 +144,14 @@ __device__ __forceinline__ bool load_turns(const RopeParams& p, int t, int first
 #pragma unroll
     for (int i = 0; i < N; ++i) cs[i].y = -cs[i].y;
   }
+}
+// The same for token t; false if a position is outside the table (nothing is read for it then).
+template <int N>
+__device__ __forceinline__ bool load_turns(const RopeParams& p, int t, int first, bool rotates, int lane,
+                                           float2 (&cs)[N]) {
+  const int pos = lane_position(p, t, lane);
+  if (!positions_exist(p, pos, lane)) return false;
+  turns_at(p, PairAxes<N>(p, first, rotates), pos, first, rotates, cs);
   return true;
 }
 
