@@ -626,10 +626,10 @@ typedef struct hc_attend_scores {
  * times n_q_heads / n_kv_heads; hc_attend_paged_few_rows says how many) has its
  * keys split over the GPU and probabilities of 16 (bf16) or 22 bits (f16); one
  * of more rows is attended in tiles of 256 rows with probabilities in the pages'
- * dtype.  So the last bits of a request's result depend on the number of
- * requests in its call, which the limit depends on; for the same call they are
- * the same every time.  In f16 what is below 2^-33 of a row's largest
- * probability is lost.  Values are below 2^80 in magnitude. */
+ * dtype.  So the last bits of a request's result depend on the other requests of
+ * its call and the width of its tables, which the limit and where keys are split
+ * depend on; for the same call they are the same every time.  In f16 what is below 2^-29 of
+ * a row's largest probability may be lost.  Values are below 2^80 in magnitude. */
 int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_tokens, int32_t n_q_heads,
                     const hc_paged_desc* desc, const void* k_pages, const void* v_pages, const int32_t* block_tables,
                     int64_t table_stride, int32_t table_width, const int32_t* q_starts, const int32_t* kv_lens,
@@ -637,9 +637,10 @@ int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_
                     int64_t workspace_bytes, int32_t* err_flag, void* stream);
 
 /* hc_attend_paged_few_rows: the largest number of query rows of a request that
- * an hc_attend_paged call of n_req requests takes as few (a host function; see
- * there), or a negative hc_status. */
-int32_t hc_attend_paged_few_rows(int32_t n_req, int32_t n_kv_heads, int32_t d_head);
+ * an hc_attend_paged call of n_req requests, with tables of table_keys (table_width
+ * times block_size) keys each, takes as few (a host function; see there), or a
+ * negative hc_status. */
+int32_t hc_attend_paged_few_rows(int32_t n_req, int32_t n_kv_heads, int32_t d_head, int64_t table_keys);
 
 /* hc_attend_paged_workspace: bytes of workspace that any hc_attend_paged call
  * needs (a host function; the same on every call). */

@@ -22,22 +22,37 @@ int check_pages(const hc_paged_desc* d, const void* k, const void* v) {
   return HC_OK;
 }
 
-// A request with more query rows (new tokens times query heads per cache
-// head) than this is attended in tiles of 256 rows on the 5th-generation
-// tensor cores (one CTA walks all keys of a tile), one with fewer in pieces of
-// 16 rows whose keys are split over the SMs.
-int rows_for_pieces(int64_t n_req, int64_t heads, int d_head) {
-  const int64_t sms = hc::device_sm_count();
-  constexpr int kMost = 384;
-  const int64_t each = n_req * heads, factor = d_head == 128 ? 300 : 500;
-  for (int rows = 16; rows <= kMost; rows += 16) {
-    const int64_t tiles = each * ((rows + 255) / 256);
-    if (each * (rows / 16) > factor * ((tiles + sms - 1) / sms)) return std::max(16, rows - 16);
+// The rows kernel's counters, then partial sums: the tiles kernel's, and once those are joined the rows kernel's; at
+// the end the tiles kernel's two counters.
+constexpr int64_t kWorkspace = int64_t{32} << 20, kTileCounters = 256;
+int64_t workspace_bytes_needed() { return std::max(kWorkspace, hc::attend_paged_rows_bytes() + kTileCounters); }
+
+int64_t part_bytes() { return workspace_bytes_needed() - kTileCounters - hc::attend_paged_counter_bytes(); }
+
+// A request with more query rows (new tokens times query heads per cache head)
+// than this is attended in tiles of 256 rows on the 5th-generation tensor cores,
+// one with fewer in pieces of 16 rows whose keys are split over the SMs.  What
+// each takes, in us, fitted to both kernels on even lengths (1 to 64 requests of
+// 1000 to 16000 keys, 2 and 8 cache heads, 16 to 384 rows):
+//   pieces: 11 + 0.0118 (64 channels: 0.0062) for each piece and 128 keys of a head
+//   tiles:  8 + 1.27 (0.88) for each tile of the slowest SM
+// For example, of 128 channels, pieces against tiles: 8 heads of one request of
+// 1000 keys, 64 rows 16.5 against 20.8, 256 rows 24.6 against 21.7; of 16 requests
+// of 4000 keys, 16 rows 57 against 60, 32 rows 84 against 60.  Pieces share out
+// ragged lengths better than tiles do: what they take counts 0.85.
+int rows_for_pieces(int64_t n_req, int64_t heads, int d_head, int64_t keys) {
+  const int sms = hc::device_sm_count();
+  constexpr int kMost = 1024;
+  const int64_t each = n_req * heads, tiles = std::max<int64_t>(1, (keys + 127) / 128);
+  const double piece = 0.85 * (d_head == 128 ? 0.0118 : 0.0062) * static_cast<double>(each) * static_cast<double>(tiles);
+  for (int block = 1; block * 256 <= kMost; ++block) {
+    const hc::Split split = hc::split_tiles(each * block, keys, part_bytes() / (256 * (d_head * 4 + 8)), sms);
+    const double time = 8 + (d_head == 128 ? 1.27 : 0.88) * static_cast<double>(split.time);
+    const double rows = 16 * std::floor((time - 0.85 * 11) / piece);
+    if (rows < block * 256) return std::max(16, std::max(static_cast<int>(rows), (block - 1) * 256));
   }
   return kMost;
 }
-
-int64_t workspace_bytes_needed() { return hc::attend_paged_rows_bytes() + 256; }
 
 }  // namespace
 
@@ -100,10 +115,10 @@ int hc_append_paged(const hc_rows* q, const hc_rows* k, const hc_rows* v, int32_
   return hc::record_cuda(hc::launch_append_paged(desc->dtype, pairing, p, static_cast<cudaStream_t>(stream)));
 }
 
-int32_t hc_attend_paged_few_rows(int32_t n_req, int32_t n_kv_heads, int32_t d_head) {
-  if (n_req < 1 || n_kv_heads < 1 || d_head < 1) return HC_ERR_INVALID_ARG;
+int32_t hc_attend_paged_few_rows(int32_t n_req, int32_t n_kv_heads, int32_t d_head, int64_t table_keys) {
+  if (n_req < 1 || n_kv_heads < 1 || d_head < 1 || table_keys < 0 || table_keys >= int64_t{1} << 31) return HC_ERR_INVALID_ARG;
   if (d_head != 64 && d_head != 128) return HC_ERR_UNSUPPORTED;
-  return rows_for_pieces(n_req, n_kv_heads, d_head);
+  return rows_for_pieces(n_req, n_kv_heads, d_head, table_keys);
 }
 
 int64_t hc_attend_paged_workspace(void) { return workspace_bytes_needed(); }
@@ -141,7 +156,7 @@ int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_
   const int G = n_q_heads / H;
   // rows of a request, pieces of 8 rows times tiles of 64 keys, and tiles of 256 rows are counted in 32 bits
   if (int64_t{max_new} * G >= (int64_t{1} << 30)) return HC_ERR_INVALID_ARG;
-  const int rows_above = n_req > 0 ? rows_for_pieces(n_req, H, d) : 0;
+  const int rows_above = n_req > 0 ? rows_for_pieces(n_req, H, d, int64_t{table_width} << log2) : 0;
   const int64_t pieces = (std::min<int64_t>(int64_t{max_new} * G, rows_above) + 7) / 8;
   const int64_t tiles = ((int64_t{table_width} << log2) + 63) / 64 + 3;
   const double runs = static_cast<double>((int64_t{max_new} * G + 255) / 256);
@@ -185,7 +200,9 @@ int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_
   p.cap_log2 = cap_log2;
   p.out32 = aligned(out->ptr, 32) && out->token_stride % 16 == 0 && out->head_stride % 16 == 0;
   p.workspace = static_cast<uint8_t*>(workspace);
-  p.tiles_taken = reinterpret_cast<int32_t*>(p.workspace + hc::attend_paged_rows_bytes());
+  p.tiles_taken = reinterpret_cast<int32_t*>(p.workspace + workspace_bytes_needed() - kTileCounters);
+  p.part_sums = p.workspace + hc::attend_paged_counter_bytes();
+  p.part_bytes = part_bytes();
   p.err = err_flag;
   p.rows_above = rows_above;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -579,8 +579,10 @@ cudaError_t launch_type(const AttendPagedParams& p, cudaStream_t s) {
 
 }  // namespace
 
+int64_t attend_paged_counter_bytes() { return kMaxCtas * static_cast<int64_t>(sizeof(int32_t)); }
+
 int64_t attend_paged_rows_bytes() {
-  return kMaxCtas * static_cast<int64_t>(sizeof(int32_t)) +
+  return attend_paged_counter_bytes() +
          static_cast<int64_t>(kMaxCtas) * 2 * kPartialFloats * static_cast<int64_t>(sizeof(float));
 }
 

@@ -12,6 +12,9 @@
 //                   memory, O += P V with P from tensor memory;
 //   warp 10         finds the runs, up to four ahead;
 //   warp 11         zeros in place of values that no row sees.
+// Where there are fewer runs than SMs, their tiles are shared out as well, and
+// the parts' sums joined by a second kernel.
+//
 // While one half's softmax runs, the other half's products do: per half the
 // order is S(j), softmax(j), O += P(j) V(j), S(j + 1).  Tensor memory is full:
 // two S of 128 columns, over which P is written, and two O of d.
@@ -95,7 +98,8 @@ struct Tiles {
 struct alignas(16) Work {
   PagedRequest rq;
   int r, head, row0, rows_all, tiles;  // tiles 0: no work, the CTA is done
-  Range vis;
+  int parts, part;  // of the run's tiles, and which of its partial sums this is (parts 1: the result)
+  Range vis;        // its tiles: of this part
 };
 // Tile j of a work, from the last one on: its first key.
 __device__ __forceinline__ int tile_key(const Range& v, int j) { return (v.tile0 + v.tiles - 1 - j) * kKeys; }
@@ -186,8 +190,9 @@ __device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// Number `idx` of the call's works, found by a warp (all lanes get it); false
-// past the last.  `c` goes forward only, so idx may not fall.
+// The run of rows that is number `idx` of the call's, whole, found by a warp
+// (all lanes get it); false past the last.  `c` goes forward only, so idx may
+// not fall.
 //
 // The order: works whose last rows see the most keys, by powers of two; within
 // one, by request and from its last rows.  Each class goes through the requests
@@ -224,7 +229,7 @@ __device__ __forceinline__ int runs_seeing(const AttendPagedParams& p, const Pag
   }
   return runs - lo;
 }
-__device__ __forceinline__ bool find_work(const AttendPagedParams& p, Cursor& c, int idx, int lane, Work& w) {
+__device__ __forceinline__ bool find_run(const AttendPagedParams& p, Cursor& c, int idx, int lane, Work& w) {
   for (;;) {
     if (!c.read) {
       int bad = 0;  // lengths are reported by k_attend_paged_rows
@@ -271,6 +276,29 @@ __device__ __forceinline__ bool find_work(const AttendPagedParams& p, Cursor& c,
       c.r0 = 0;
     }
   }
+}
+
+// Where a call has fewer runs than SMs their tiles are shared out too: run idx
+// is parts idx * split + i, from its last tiles on, of equal numbers of tiles
+// but kLeastTiles at least.  False past the last; tiles 0 where the run has no
+// such part.
+constexpr int kLeastTiles = kLeastPartTiles;
+__device__ __forceinline__ bool find_work(const AttendPagedParams& p, Cursor& c, int idx, int lane, Work& w) {
+  const int run = p.split > 1 ? idx / p.split : idx;
+  if (!find_run(p, c, run, lane, w)) return false;
+  const int each = p.split > 1 ? max((w.tiles + p.split - 1) / p.split, kLeastTiles) : w.tiles;
+  const int i = idx - run * p.split, from = i * each;
+  w.parts = (w.tiles + each - 1) / each;
+  w.part = idx;
+  w.tiles = max(0, min(each, w.tiles - from));
+  w.vis.tile0 += w.vis.tiles - from - w.tiles;
+  w.vis.tiles = w.tiles;
+  return true;
+}
+// A part's sums in the workspace: O by fours of channels [D / 4][rows], then (reference, sum) [rows].
+template <int D>
+__device__ __forceinline__ float4* part_sums(const AttendPagedParams& p, int part) {
+  return reinterpret_cast<float4*>(p.part_sums + static_cast<int64_t>(part) * p.part_rows * (D * 4 + 8));
 }
 
 template <bool kBf16, int D, Scores kScores>
@@ -749,6 +777,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
       Cursor cursor(p);
       Work work;
       int number = blockIdx.x;
+      bool taken = false;
       for (int k = 0;; ++k) {
         if (k >= kWorksAhead)
           ok = mbar_wait_inline(&sh.work_empty[k % kWorksAhead], (k / kWorksAhead - 1) & 1, &sh.dead);
@@ -756,10 +785,16 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         if (k > 0) {
           ok = mbar_wait_inline(&sh.work_due, (k - 1) & 1, &sh.dead);
           if (!__all_sync(0xffffffffu, ok)) break;
-          if (lane == 0) number = static_cast<int>(gridDim.x) + atomicAdd(p.tiles_taken, 1);
-          number = __shfl_sync(0xffffffffu, number, 0);
         }
-        const bool more = find_work(p, cursor, number, lane, work);
+        bool more = true;
+        do {
+          if (taken) {
+            if (lane == 0) number = static_cast<int>(gridDim.x) + atomicAdd(p.tiles_taken, 1);
+            number = __shfl_sync(0xffffffffu, number, 0);
+          }
+          taken = true;
+          more = find_work(p, cursor, number, lane, work);
+        } while (more && work.tiles == 0);
         if (!more) work.tiles = 0;
         if (lane == 0) {
           sh.work[k % kWorksAhead] = work;
@@ -931,11 +966,22 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           fence_after();
           const float2 ml = sh.rows[k & 1][at];
           const float by = ml.y > 0.f ? 1.f / ml.y : 0.f;
+          const bool whole = work.parts == 1, stored = at < p.part_rows;
+          float4* const sums = whole ? nullptr : part_sums<D>(p, work.part);
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             uint32_t x[16], w[8];
             tmem_load16(x, tmem + (static_cast<uint32_t>(quarter) << 21) + L::kOut + half * D + c);
             tmem_wait_load16(x);
+            if (!whole) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (stored)
+                  __stcg(sums + (c / 4 + i) * p.part_rows + at,
+                         make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
+                                     __uint_as_float(x[4 * i + 3])));
+              continue;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = pack2(__uint_as_float(x[2 * i]) * by, __uint_as_float(x[2 * i + 1]) * by);
             if (live && p.out32) {
@@ -945,10 +991,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
               reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
           }
+          if (!whole && stored) __stcg(reinterpret_cast<float2*>(sums + D / 4 * p.part_rows) + at, ml);
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.o_empty[half]);
-          if (p.lse && live)
+          if (whole && p.lse && live)
             p.lse[t * (static_cast<int64_t>(p.H) * p.G) + head] =
                 ml.y > 0.f ? (ml.x - Softmax<kBf16>::kTop + log2f(ml.y)) * kLn2 : kNegInf;
         }
@@ -974,6 +1021,65 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
   if (bad) flag_error(p.err, bad);
+}
+
+// The parts' sums of a run joined, in their order: 32 rows of a run a CTA, a
+// lane for each.
+constexpr int kJoinThreads = 256;
+template <bool kBf16, int D>
+__global__ void __launch_bounds__(kJoinThreads) k_join_paged_tiles(const __grid_constant__ AttendPagedParams p) {
+  __shared__ Work shared;
+  __shared__ bool there;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunks = p.part_rows / 32, run = blockIdx.x / chunks, at = (blockIdx.x - run * chunks) * 32 + lane;
+  if (warp == 0) {
+    Cursor cursor(p);
+    Work work;
+    const bool found = find_work(p, cursor, run * p.split, lane, work);
+    if (lane == 0) {
+      shared = work;
+      there = found;
+    }
+  }
+  __syncthreads();
+  if (!there || shared.parts == 1) return;
+  const Work& work = shared;
+  const int row = work.row0 + at;
+  if (row >= work.rows_all) return;
+  const int token = static_cast<int>(p.by_group.div(row));
+  const int64_t t = work.rq.q0 + token, head = work.head * p.G + row - token * p.G;
+  uint16_t* const out = static_cast<uint16_t*>(p.out) + t * p.o_token + head * p.o_head;
+  constexpr int kFours = D / 4 / (kJoinThreads / 32);  // of channels, of a thread
+  float top = kNegInf, sum = 0.f;
+  float4 acc[kFours];
+#pragma unroll
+  for (int i = 0; i < kFours; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = 0; k < work.parts; ++k) {
+    const float4* const sums = part_sums<D>(p, work.part + k);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(sums + D / 4 * p.part_rows) + at);
+    float4 v[kFours];
+#pragma unroll
+    for (int i = 0; i < kFours; ++i) v[i] = __ldcg(sums + (warp * kFours + i) * p.part_rows + at);
+    if (ml.x == kNegInf) continue;
+    const float to = fmaxf(top, ml.x), old = ex2(top - to), wt = ex2(ml.x - to);  // top -inf: old 0
+    top = to;
+    sum = sum * old + wt * ml.y;
+#pragma unroll
+    for (int i = 0; i < kFours; ++i) {
+      acc[i].x = acc[i].x * old + wt * v[i].x, acc[i].y = acc[i].y * old + wt * v[i].y;
+      acc[i].z = acc[i].z * old + wt * v[i].z, acc[i].w = acc[i].w * old + wt * v[i].w;
+    }
+  }
+  const float by = sum > 0.f ? 1.f / sum : 0.f;
+  auto pack2 = [](float lo, float hi) { return kBf16 ? pack_bf16(lo, hi) : pack_f16(lo, hi); };
+#pragma unroll
+  for (int i = 0; i < kFours; ++i)
+    reinterpret_cast<uint2*>(out)[warp * kFours + i] =
+        make_uint2(pack2(acc[i].x * by, acc[i].y * by), pack2(acc[i].z * by, acc[i].w * by));
+  if (p.lse && warp == 0)
+    p.lse[t * (static_cast<int64_t>(p.H) * p.G) + head] =
+        sum > 0.f ? (top - Softmax<kBf16>::kTop + log2f(sum)) * kLn2 : kNegInf;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1038,10 +1144,17 @@ cudaError_t launch(AttendPagedParams p, cudaStream_t s) {
   if (e == cudaSuccess) e = pages_map<kBf16>(&v_map, p.v_pages, p, D);
   if (e != cudaSuccess) return e;
   p.q_tma = queries_map<kBf16>(&q_map, p, D);
-  const int64_t runs = (static_cast<int64_t>(p.max_new) * p.G + kRowsTile - 1) / kRowsTile;
-  const double works = static_cast<double>(runs) * p.n_req * p.H;
-  const int grid = works < resident ? static_cast<int>(works) : resident;
+  const int64_t rows = static_cast<int64_t>(p.max_new) * p.G, runs = (rows + kRowsTile - 1) / kRowsTile * p.n_req * p.H;
+  p.part_rows = static_cast<int32_t>(std::min<int64_t>((rows + 31) / 32 * 32, kRowsTile));
+  const int64_t keys = static_cast<int64_t>(p.table_width) << p.B_log2;
+  p.split = split_tiles(runs, keys, p.part_bytes / (p.part_rows * (D * 4 + 8)), resident).parts;
+  const int64_t works = runs * p.split;
+  const int grid = static_cast<int>(std::min<int64_t>(works, resident));
   k_attend_paged_tiles<kBf16, D, kScores><<<grid, kThreadsTiles, Tiles<D>::kAsk, s>>>(p, k_map, v_map, q_map);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.split == 1) return e;
+  const unsigned chunks = static_cast<unsigned>(p.part_rows / 32);
+  k_join_paged_tiles<kBf16, D><<<static_cast<unsigned>(runs) * chunks, kJoinThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -2,6 +2,8 @@
 // attention, merge), shared by their kernels and the C ABI.
 #pragma once
 
+#include <algorithm>
+
 #include "serve.cuh"
 
 namespace hc {
@@ -51,6 +53,9 @@ struct AttendPagedParams {
   int32_t q_tma;        // of the tiles kernel: 128 rows of queries are a box of whole tokens
   uint8_t* workspace;
   int32_t* tiles_taken;  // in the workspace: works of the tiles kernel that are taken, CTAs that are done
+  uint8_t* part_sums;    // in the workspace, where the rows kernel has its partial sums later
+  int64_t part_bytes;
+  int32_t split, part_rows;  // of the tiles kernel: parts of a run's tiles, rows of a part's sums
   int32_t* err;
 };
 
@@ -66,10 +71,33 @@ struct MergeParams {
   FastDivmod by_heads;
 };
 
-// Bytes of the rows kernel's workspace: one counter per CTA of the largest
-// grid, then two partial results per CTA.  The tiles kernel's two counters
-// follow.
+// The rows kernel's workspace: bytes of its counters, one per CTA of the largest
+// grid, and with the two partial results per CTA that follow.
+int64_t attend_paged_counter_bytes();
 int64_t attend_paged_rows_bytes();
+
+// Parts that the tiles of a run of 256 rows are shared out in where a call has
+// fewer runs than SMs, and the time of the slowest SM in tiles of 128 keys: a
+// part's start and end take 3, the join of the parts 6.  At most `places` parts
+// of all runs fit the workspace.
+constexpr int kLeastPartTiles = 4;
+struct Split {
+  int parts;
+  int64_t time;
+};
+inline Split split_tiles(int64_t runs, int64_t keys, int64_t places, int sms) {
+  const int64_t tiles = std::max<int64_t>(1, (keys + 127) / 128), waves = (runs + sms - 1) / sms;
+  Split best{1, waves * (tiles + 3)};
+  if (runs >= sms) return best;
+  const int64_t most = std::min((tiles + kLeastPartTiles - 1) / kLeastPartTiles, places / runs);
+  for (int64_t w = 1; w <= 3; ++w) {  // as many parts as w of them an SM
+    const int64_t n = std::min(most, w * sms / runs);
+    if (n < 2) continue;
+    const int64_t time = w * ((tiles + n - 1) / n + 3) + 6;
+    if (time < best.time) best = {static_cast<int>(n), time};
+  }
+  return best;
+}
 
 cudaError_t launch_append_paged(int dtype, int pairing, const AppendPagedParams& p, cudaStream_t s);
 // The requests with at most p.rows_above query rows, and those with more.

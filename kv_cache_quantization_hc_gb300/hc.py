@@ -104,7 +104,7 @@ def lib():
         L.hc_attend_paged.argtypes = [rows_p, rows_p, _P, _I32, _I32, desc_p, _P, _P, _P, _I64, _I32, _P, _P, _I32,
                                       _I32, scores_p, _P, _I64, _P, _P]
         L.hc_merge_attention.argtypes = [rows_p, _P, rows_p, _P, rows_p, _P, _I32, _I32, _I32, _I32, _P]
-        L.hc_attend_paged_few_rows.argtypes = [_I32, _I32, _I32]
+        L.hc_attend_paged_few_rows.argtypes = [_I32, _I32, _I32, _I64]
         L.hc_attend_paged_few_rows.restype = _I32
         L.hc_attend_paged_workspace.argtypes = []
         L.hc_attend_paged_workspace.restype = _I64

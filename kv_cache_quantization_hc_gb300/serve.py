@@ -121,9 +121,10 @@ def paged_cache(num_slots, H, B, d, dtype=torch.bfloat16, n_layers=None, device=
     return tuple(torch.zeros(lead + (num_slots, B, H, d), dtype=dtype, device=device) for _ in range(2))
 
 
-def attend_paged_few_rows(n_req, n_kv_heads, d):
-    """hc_attend_paged_few_rows: attend_few_rows for attend_paged."""
-    rows = hc.lib().hc_attend_paged_few_rows(n_req, n_kv_heads, d)
+def attend_paged_few_rows(n_req, n_kv_heads, d, table_keys):
+    """hc_attend_paged_few_rows: attend_few_rows for attend_paged; table_keys:
+    the keys that a row of block_tables has room for."""
+    rows = hc.lib().hc_attend_paged_few_rows(n_req, n_kv_heads, d, table_keys)
     if rows < 0:
         hc._check("hc_attend_paged_few_rows", rows)
     return rows

@@ -76,7 +76,7 @@ def test_append_skips_bad_rows_and_positions(serve):  # noqa: F811
 def check_attend(serve, workspace, c, scale=None, few=None, **kw):  # noqa: F811
     import torch
     t, err = c.tensors(), _err()
-    few_rows = serve.attend_paged_few_rows(max(len(c.kv), 1), c.H, c.d)
+    few_rows = serve.attend_paged_few_rows(max(len(c.kv), 1), c.H, c.d, c.table.shape[1] * c.B)
     got, lse = serve.attend_paged(**t, max_new=max(c.new + [0]), workspace=workspace, err=err, softmax_scale=scale,
                                   return_lse=True, **kw)
     out, want_lse, weight, reach, far = c.expected(scale)
@@ -154,6 +154,24 @@ def test_attend_split_over_ctas(serve, workspace, n_req):  # noqa: F811
     b = check_attend(serve, workspace, c)
     assert all(torch.equal(x, y) for x, y in zip(a, b))        # the same bits every time
     assert int(workspace[:4096].count_nonzero()) == 0
+
+
+SPLITS = [dict(kv_lens=[5000], new_lens=[80], Hq=12, H=1, d=64, B=16), dict(kv_lens=[4100, 3], new_lens=[150, 3], Hq=4, H=2, d=128, B=64, dtype="f16"),
+          dict(kv_lens=[3000, 900, 2100], new_lens=[40, 700, 100], Hq=10, H=1, d=128, B=32),
+          dict(kv_lens=[6000], new_lens=[450], Hq=2, H=2, d=64, B=128, window=2500), dict(kv_lens=[4000, 2600], new_lens=[90, 90], Hq=8, H=1, d=64, B=16, dtype="f16", softcap=20.0, slopes=True),
+          dict(kv_lens=[3500], new_lens=[450], Hq=2, H=1, d=128, B=16, prefix=[3400], softcap=30.0)]
+
+
+@pytest.mark.parametrize("case", SPLITS, ids=lambda c: "-".join(map(str, c["kv_lens"] + c["new_lens"])))
+def test_attend_few_runs_of_many_keys(serve, workspace, case):  # noqa: F811
+    """Fewer runs of 256 rows than SMs: their keys are shared out, and the parts joined."""
+    import torch
+    c = Pages(13, **case)
+    assert max(c.new) * c.Hq // c.H > serve.attend_paged_few_rows(len(c.kv), c.H, c.d, c.table.shape[1] * c.B)
+    a = check_attend(serve, workspace, c)
+    b = check_attend(serve, workspace, c)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))        # the same bits every time
+    assert int(workspace[:4096].count_nonzero()) == 0 and int(workspace[-256:].count_nonzero()) == 0
 
 
 def test_attend_more_heads_than_places(serve, workspace):  # noqa: F811
@@ -240,6 +258,9 @@ def test_attend_flags_bad_lengths_slots_and_positions(serve, workspace, new):  #
         serve.attend_paged(**dict(dict(t, max_new=new, workspace=workspace, err=err, out=out), **kw))
         return int(err)
 
+    def same(a, b):  # up to a rounding: where keys are split depends on all of the call's lengths
+        return bool(((a.float() - b.float()).abs() <= 2.0 ** -7 * b.float().abs() + 2.0 ** -14).all())
+
     assert run() == 0
     good = out.clone()
     for bad in (-1, 10_000_000):
@@ -248,22 +269,22 @@ def test_attend_flags_bad_lengths_slots_and_positions(serve, workspace, new):  #
         out.fill_(5.0)
         assert run(kv_lens=kv) == 8
         assert bool((out[new:2 * new] == 5).all())
-        assert torch.equal(out[:new], good[:new]) and torch.equal(out[2 * new:], good[2 * new:])
+        assert same(out[:new], good[:new]) and same(out[2 * new:], good[2 * new:])
     starts = t["q_starts"].clone()
     starts[3] = 10_000                                             # past the queries
     out.fill_(5.0)
     assert run(q_starts=starts, max_new=20_000) == 8
-    assert bool((out[2 * new:] == 5).all()) and torch.equal(out[:2 * new], good[:2 * new])
+    assert bool((out[2 * new:] == 5).all()) and same(out[:2 * new], good[:2 * new])
     for slot in (-1, c.k.shape[0]):
         table = t["block_tables"].clone()
         table[0, 1] = slot
-        assert run(block_tables=table) == 1 and torch.equal(out[new:], good[new:]) and bool(out.isfinite().all())
+        assert run(block_tables=table) == 1 and same(out[new:], good[new:]) and bool(out.isfinite().all())
     if new > 1:
         pos = torch.arange(3 * new, dtype=torch.int32, device="cuda") % new
         assert run(positions=pos) == 0
         want = out.clone()
         pos[5] = 100
-        assert run(positions=pos) == 32 and torch.equal(out[new:], want[new:])
+        assert run(positions=pos) == 32 and same(out[new:], want[new:])
 
 
 def test_padded_steps_and_nothing(serve, workspace):  # noqa: F811
