@@ -611,9 +611,11 @@ typedef struct hc_attend_scores {
  *   max_new   : at least every request's number of queries; 0 launches nothing.
  *               Queries of no request (from q_starts[n_req] on) have their rows
  *               of out and lse left as they were
- *   scores    : host pointer, read during the call only.  A position below 0 sees
- *               no key but the prefix's, one past the keys sees them all; any
- *               negative one counts as -1 for the bias
+ *   scores    : host pointer, read during the call only.  A position below 0 (of
+ *               more queries than keys, too) counts as -1 and sees no key but the
+ *               prefix's; one past the keys sees them all.  With positions and a
+ *               window, keys between two queries' windows count as seen.  slopes
+ *               are finite
  *   workspace : device, 256-byte aligned, zero before its first use; every call
  *               leaves it ready for the next, of hc_attend_int4 too.  Calls that
  *               may run at the same time need workspaces of their own.

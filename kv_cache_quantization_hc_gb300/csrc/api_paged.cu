@@ -144,7 +144,8 @@ int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_
   if (!table_ok(block_tables, table_stride, table_width, n_req, log2)) return HC_ERR_INVALID_ARG;
   if ((scores->causal != 0 && scores->causal != 1) || scores->window < 0) return HC_ERR_INVALID_ARG;
   if (!scores->causal && (scores->window > 0 || scores->prefix_lens)) return HC_ERR_INVALID_ARG;
-  if (!std::isfinite(scores->softmax_scale)) return HC_ERR_INVALID_ARG;
+  const float scale_log2 = scores->softmax_scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2)) return HC_ERR_INVALID_ARG;
   const float cap = scores->softcap, cap_log2 = cap * 1.4426950408889634f;
   const float cap_in = cap > 0.f ? scores->softmax_scale / cap : 0.f;
   if (!(cap >= 0.f) || !std::isfinite(cap_log2) || (cap > 0.f && cap_log2 == 0.f) || !std::isfinite(cap_in))
@@ -195,7 +196,7 @@ int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_
   p.window = scores->window;
   p.by_group = hc::FastDivmod(static_cast<uint32_t>(G));
   p.by_heads = hc::FastDivmod(static_cast<uint32_t>(H));
-  p.scale_log2 = scores->softmax_scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.cap_in = cap_in;
   p.cap_log2 = cap_log2;
   p.out32 = aligned(out->ptr, 32) && out->token_stride % 16 == 0 && out->head_stride % 16 == 0;

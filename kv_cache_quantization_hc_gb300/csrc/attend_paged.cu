@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasPerSm) k_attend_paged_rows(
       // -- queries as A operands (rows 8 to 15 are there for NT = 2 only), and what each row sees
       uint32_t qf[NT][D / 16][2];
       int lo[NT], hi[NT];
-      float pos_f[NT], slope[NT];
+      int pos[NT];
+      float slope[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int row = row0 + nt * 8 + g;
@@ -263,14 +264,14 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasPerSm) k_attend_paged_rows(
         }
         lo[nt] = 0;
         hi[nt] = 0x7fffffff;
-        pos_f[nt] = slope[nt] = 0.f;
+        pos[nt] = 0;
+        slope[nt] = 0.f;
         if (live) {
-          const int pos = position(p, rq, i);
-          lo[nt] = first_key(p, pos);
-          hi[nt] = last_key(p, rq, pos);
-          pos_f[nt] = static_cast<float>(pos);
+          pos[nt] = position(p, rq, i);
+          lo[nt] = first_key(p, pos[nt]);
+          hi[nt] = last_key(p, rq, pos[nt]);
           if (p.slopes) slope[nt] = __ldg(p.slopes + h) * kLog2e;
-          if (p.positions && i > 0 && __ldg(p.positions + rq.q0 + i - 1) > pos) bad |= HC_DEVERR_POS;
+          if (p.positions && i > 0 && __ldg(p.positions + rq.q0 + i - 1) > pos[nt]) bad |= HC_DEVERR_POS;
         }
       }
 
@@ -335,11 +336,12 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasPerSm) k_attend_paged_rows(
               for (int j = 0; j < 2; ++j) s[nt][n][j] *= p.scale_log2;
           }
           if (p.slopes) {
+            const float away = static_cast<float>(pos[nt] - key0);  // positions themselves pass fp32's 24 bits
 #pragma unroll
             for (int n = 0; n < kKeys / 8; ++n)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                s[nt][n][j] = fmaf(-slope[nt], fabsf(pos_f[nt] - static_cast<float>(key0 + n * 8 + 2 * t + j)), s[nt][n][j]);
+                s[nt][n][j] = fmaf(-slope[nt], fabsf(away - static_cast<float>(n * 8 + 2 * t + j)), s[nt][n][j]);
           }
           if (key0 < lo[nt] || key0 + kKeys > hi[nt]) {
 #pragma unroll

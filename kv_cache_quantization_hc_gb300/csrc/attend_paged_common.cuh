@@ -29,9 +29,9 @@ __device__ __forceinline__ PagedRequest load_request(const AttendPagedParams& p,
   return q;
 }
 
-// Position of the request's query i; any negative one is -1.
+// Position of the request's query i; any negative one (more queries than keys) is -1.
 __device__ __forceinline__ int position(const AttendPagedParams& p, const PagedRequest& q, int i) {
-  return p.positions ? max(__ldg(p.positions + q.q0 + i), -1) : q.kv - q.n + i;
+  return max(p.positions ? __ldg(p.positions + q.q0 + i) : q.kv - q.n + i, -1);
 }
 // Keys [lo, hi) that a query at this position sees; hi <= lo: none.
 __device__ __forceinline__ int last_key(const AttendPagedParams& p, const PagedRequest& q, int pos) {

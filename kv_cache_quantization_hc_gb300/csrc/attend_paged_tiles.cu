@@ -215,7 +215,9 @@ struct Cursor {
   }
 };
 // Runs of 256 rows of a request, of `runs` in all, whose last row's keys end at
-// `key` or later; positions do not fall, so they are the last ones.
+// `key` or later; positions do not fall, so they are the last ones.  Where they
+// do, which is flagged, it is some number that does not rise with `key` either:
+// each run is some class's, once.
 __device__ __forceinline__ int runs_seeing(const AttendPagedParams& p, const PagedRequest& q, int runs, int key) {
   if (key <= 0) return runs;
   int lo = 0, hi = runs;  // the first such run
@@ -241,8 +243,7 @@ __device__ __forceinline__ bool find_run(const AttendPagedParams& p, Cursor& c, 
     }
     if (!c.counted) {
       c.to_end = runs_seeing(p, c.q, c.runs, c.from);
-      // positions that fall, which are flagged, may make this negative
-      c.inc = max(0, c.to_end - runs_seeing(p, c.q, c.runs, c.upto)) * p.H;
+      c.inc = (c.to_end - runs_seeing(p, c.q, c.runs, c.upto)) * p.H;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, c.inc, o);
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
   int base = 0;  // tiles of the works so far
   // Work k is read where it is needed, which leaves the registers to the loops.
   auto take_work = [&](int k) {  // false: none left (or a wait ran out)
-    const bool there = mbar_wait_inline(&sh.work_full[k % kWorksAhead], (k / kWorksAhead) & 1, &sh.dead);
+    const bool there = mbar_wait_inline(&sh.work_full[k % kWorksAhead], (k / kWorksAhead) & 1, &sh.dead, p.wait_limit);
     ok = __all_sync(0xffffffffu, ok && there);
     return ok && sh.work[k % kWorksAhead].tiles > 0;
   };
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
       uint32_t hidden = __float_as_uint(kScores == kPlain && factor < 0.f ? -kNegInf : kNegInf);
       // cap * tanh(s * cap_in) up to |s * cap_in| = 3/4 as an odd polynomial in s: the minimax fit of tanh(y) / y in y^2
       // by Remez' exchange, off by 2.9e-8, with the factors in its terms; its last term is negative, so that a score
-      // of y = 1000 is one that no probability comes of.  Factors whose powers fp32 does not hold do without.
+      // of y = 1000 is one that no probability comes of.  Caps and factors whose products fp32 does not hold do without.
       Pair tanh_terms[6];
       float tanh_reach = -1.f;
       if constexpr (kScores == kCapped) {
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           tanh_terms[k] = fixed_pair(kTerms[k] * power);
           power *= t;
         }
-        if (t >= 1e-6f && t <= 1e6f) tanh_reach = 0.5625f / t;
+        if (t >= 1e-6f && t <= 1e6f && p.cap_log2 >= 0.01f && p.cap_log2 <= 1e6f) tanh_reach = 0.5625f / t;
         hidden = __float_as_uint(1000.f / p.cap_in);
       }
 
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         // Most tiles: all of it seen, by rows that have a reference.
         const bool partly = live && (lo > 0 || hi < kKeys), fresh = live && m == kNegInf && max(lo, 0) < min(hi, kKeys);
         const bool special = __any_sync(0xffffffffu, partly || fresh);
-        ok = mbar_wait_inline(&sh.s_full[buffer], (n / kBuffers) & 1, &sh.dead);
+        ok = mbar_wait_inline(&sh.s_full[buffer], (n / kBuffers) & 1, &sh.dead, p.wait_limit);
         if (!__all_sync(0xffffffffu, ok)) break;
         fence_after();
         // A score in units of log2.
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           if (__any_sync(0xffffffffu, m_new != m && m != kNegInf)) {  // O of a row without one is 0
             const float by = m == kNegInf ? 0.f : ex2(m - m_new);
             l *= by;
-            ok = mbar_wait_inline(&sh.o_full[half][(base + j - 1) & 1], ((base + j - 1) >> 1) & 1, &sh.dead) && ok;
+            ok = mbar_wait_inline(&sh.o_full[half][(base + j - 1) & 1], ((base + j - 1) >> 1) & 1, &sh.dead, p.wait_limit) && ok;
             fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -704,13 +705,13 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           const int st = (base + j) % kStages, round = (base + j) / kStages;
           const int next = slot_of(j + 1);
           if (lane == 0 && j == max(tiles - kDue, 0)) mbar_arrive(&sh.work_due);
-          if (round > 0) ok = mbar_wait_inline(&sh.k_empty[st], (round - 1) & 1, &sh.dead);
+          if (round > 0) ok = mbar_wait_inline(&sh.k_empty[st], (round - 1) & 1, &sh.dead, p.wait_limit);
           if (!__all_sync(0xffffffffu, ok)) break;
           if (lane == 0) mbar_expect(&sh.k_full[st], L::kTileBytes);
           __syncwarp();
           ++k_sent;
           load(tiles_at + L::kK + st * L::kTileBytes, &k_map, &sh.k_full[st], slot);
-          if (round > 0) ok = mbar_wait_inline(&sh.v_empty[st], (round - 1) & 1, &sh.dead);
+          if (round > 0) ok = mbar_wait_inline(&sh.v_empty[st], (round - 1) & 1, &sh.dead, p.wait_limit);
           if (!__all_sync(0xffffffffu, ok)) break;
           const bool edge = at_edge(vis, tile_key(vis, j));
           uint64_t* const full = edge ? &sh.v_edge[st] : &sh.v_full[st];
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         for (int j = 0; j < vis.tiles && ok; ++j) {
           const int key0 = tile_key(vis, j), st = (base + j) % kStages;
           if (!at_edge(vis, key0)) continue;
-          ok = mbar_wait_inline(&sh.v_edge[st], edges >> st & 1u, &sh.dead);
+          ok = mbar_wait_inline(&sh.v_edge[st], edges >> st & 1u, &sh.dead, p.wait_limit);
           if (!__all_sync(0xffffffffu, ok)) break;
           edges ^= 1u << st;
           unsigned char* const tile = dyn + L::kV + st * L::kTileBytes;
@@ -780,10 +781,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
       bool taken = false;
       for (int k = 0;; ++k) {
         if (k >= kWorksAhead)
-          ok = mbar_wait_inline(&sh.work_empty[k % kWorksAhead], (k / kWorksAhead - 1) & 1, &sh.dead);
+          ok = mbar_wait_inline(&sh.work_empty[k % kWorksAhead], (k / kWorksAhead - 1) & 1, &sh.dead, p.wait_limit);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (k > 0) {
-          ok = mbar_wait_inline(&sh.work_due, (k - 1) & 1, &sh.dead);
+          ok = mbar_wait_inline(&sh.work_due, (k - 1) & 1, &sh.dead, p.wait_limit);
           if (!__all_sync(0xffffffffu, ok)) break;
         }
         bool more = true;
@@ -820,7 +821,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
       uint32_t s_tile = 0, p_tile = 0;                          // tiles of keys and of values so far
       uint32_t s_buffer = 0, p_buffer = 0, p_parity = 0;        // of the next scores, of the next probabilities
       // Whether a wait ran out is asked once per tile: products on what is not there yet spoil results only.
-      auto wait = [&](uint64_t* b, uint32_t parity) { ok = mbar_wait_inline(b, parity, &sh.dead) && ok; };
+      auto wait = [&](uint64_t* b, uint32_t parity) { ok = mbar_wait_inline(b, parity, &sh.dead, p.wait_limit) && ok; };
       auto scores = [&](int i) {  // S_i = Q_i K(j)^T
         const uint32_t st = s_tile % kStages;
         if (i == 0) wait(&sh.k_full[st], (s_tile / kStages) & 1);
@@ -916,7 +917,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         const Work& work = sh.work[k % kWorksAhead];
         const int row0 = work.row0, rows_all = work.rows_all, q0 = work.rq.q0, head = work.head * p.G;
         const int token0 = q0 + static_cast<int>(p.by_group.div(row0 + q_half * kHalf));
-        if (k > 0) ok = mbar_wait_inline(&sh.q_empty[q_half], (k - 1) & 1, &sh.dead);
+        if (k > 0) ok = mbar_wait_inline(&sh.q_empty[q_half], (k - 1) & 1, &sh.dead, p.wait_limit);
         if (!__all_sync(0xffffffffu, ok)) return;
         if (p.q_tma) {  // a half is whole tokens: a box of them by their heads.  Rows of other requests do no harm.
           if (quarter & 1) return;
@@ -959,8 +960,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           const int token = static_cast<int>(p.by_group.div(live ? row : 0));
           const int64_t t = work.rq.q0 + token, head = work.head * p.G + row - token * p.G;
           uint16_t* const out = static_cast<uint16_t*>(p.out) + t * p.o_token + head * p.o_head;
-          ok = mbar_wait_inline(&sh.l_full[half][k & 1], (k >> 1) & 1, &sh.dead) && ok;
-          ok = mbar_wait_inline(&sh.o_full[half][(base - 1) & 1], ((base - 1) >> 1) & 1, &sh.dead) && ok;
+          ok = mbar_wait_inline(&sh.l_full[half][k & 1], (k >> 1) & 1, &sh.dead, p.wait_limit) && ok;
+          ok = mbar_wait_inline(&sh.o_full[half][(base - 1) & 1], ((base - 1) >> 1) & 1, &sh.dead, p.wait_limit) && ok;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           fence_after();
@@ -1150,6 +1151,8 @@ cudaError_t launch(AttendPagedParams p, cudaStream_t s) {
   p.split = split_tiles(runs, keys, p.part_bytes / (p.part_rows * (D * 4 + 8)), resident).parts;
   const int64_t works = runs * p.split;
   const int grid = static_cast<int>(std::min<int64_t>(works, resident));
+  // the longest wait is for a whole run, whose tiles take 1 to 2 us each
+  p.wait_limit = kWaitLimit + static_cast<uint64_t>(keys / kKeys) * 20000;
   k_attend_paged_tiles<kBf16, D, kScores><<<grid, kThreadsTiles, Tiles<D>::kAsk, s>>>(p, k_map, v_map, q_map);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.split == 1) return e;

@@ -1,5 +1,5 @@
-// mbarriers of a CTA's own, with waits that end: after two seconds, or once
-// another of the CTA's waits has run out.
+// mbarriers of a CTA's own, with waits that end: after two seconds (or what a
+// kernel gives for its longest), or once another of the CTA's waits has run out.
 #pragma once
 
 #include <stdint.h>
@@ -22,14 +22,15 @@ __device__ __forceinline__ bool mbar_try(uint32_t a, uint32_t parity) {
   return done != 0;
 }
 // Waits for the phase of this parity to end; false when the wait ran out
-// (two seconds), here or elsewhere in the CTA.
-__device__ __forceinline__ bool mbar_wait_timed(uint32_t a, uint32_t parity, int32_t* dead) {
+// (after `limit` ns), here or elsewhere in the CTA.
+constexpr uint64_t kWaitLimit = 2000000000;
+__device__ __forceinline__ bool mbar_wait_timed(uint32_t a, uint32_t parity, int32_t* dead, uint64_t limit = kWaitLimit) {
   uint64_t start, now;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
   do {
     if (mbar_try(a, parity)) return true;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-  } while (now - start < 2000000000ull && !*static_cast<volatile int32_t*>(dead));
+  } while (now - start < limit && !*static_cast<volatile int32_t*>(dead));
   *static_cast<volatile int32_t*>(dead) = 1;
   return false;
 }
@@ -45,12 +46,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, int32_t*
 }
 // The same without a call, for kernels that share registers out anew
 // (setmaxnreg), in which there may be none.
-__device__ __forceinline__ bool mbar_wait_inline(uint64_t* b, uint32_t parity, int32_t* dead) {
+__device__ __forceinline__ bool mbar_wait_inline(uint64_t* b, uint32_t parity, int32_t* dead, uint64_t limit = kWaitLimit) {
   const uint32_t a = mbar_addr(b);
 #pragma unroll 1
   for (int i = 0; i < 32; ++i)
     if (mbar_try(a, parity)) return true;
-  return mbar_wait_timed(a, parity, dead);
+  return mbar_wait_timed(a, parity, dead, limit);
 }
 
 }  // namespace

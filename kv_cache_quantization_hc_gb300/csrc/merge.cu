@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kMergeThreads = 256;
 
-// Read and written once: nothing of it is worth keeping in the caches (33.3 us without, 31.5 with: see below).
+// Read and written once: nothing of it is worth keeping in the caches (the above 33.3 us so, 31.5 with it).
 template <typename T, int V>
 __device__ __forceinline__ void load_once(const T* p, float (&x)[V]) {
   const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
@@ -46,7 +46,8 @@ __global__ void __launch_bounds__(kMergeThreads) k_merge(const __grid_constant__
   uint4 w;
   memcpy(&w, &out, 16);
   __stcs(reinterpret_cast<uint4*>(static_cast<T*>(p.out) + token * p.o_token + head * p.o_head + ch), w);
-  __syncwarp(__activemask());  // the row's log sums are read
+  // the row's lanes have read its log sums; the warp's rows end together or not at all
+  __syncwarp((pieces == 32 ? ~0u : (1u << pieces) - 1) << (threadIdx.x & 31 & -pieces));
   if (ch == 0 && p.lse) p.lse[row] = none ? -INFINITY : top + logf(total);
 }
 

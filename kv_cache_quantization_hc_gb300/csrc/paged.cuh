@@ -51,6 +51,7 @@ struct AttendPagedParams {
   int32_t piece_cost;   // of the rows kernel: what a piece's start and end take, in tiles
   int32_t out32;        // rows of out lie on 32-byte boundaries
   int32_t q_tma;        // of the tiles kernel: 128 rows of queries are a box of whole tokens
+  uint64_t wait_limit;  // of the tiles kernel: ns
   uint8_t* workspace;
   int32_t* tiles_taken;  // in the workspace: works of the tiles kernel that are taken, CTAs that are done
   uint8_t* part_sums;    // in the workspace, where the rows kernel has its partial sums later

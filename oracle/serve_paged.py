@@ -36,7 +36,7 @@ def attend(q, k_pages, v_pages, table, q_starts, kv_lens, causal=True, window=0,
     for r, kv in enumerate(map(int, kv_lens)):
         a, b = int(q_starts[r]), int(q_starts[r + 1])
         for t in range(a, b):
-            p = kv - (b - a) + (t - a) if positions is None else max(int(positions[t]), -1)
+            p = max(kv - (b - a) + (t - a) if positions is None else int(positions[t]), -1)
             j = np.arange(kv)
             seen = np.ones(kv, bool)
             if causal:
