@@ -23,32 +23,39 @@ int check_pages(const hc_paged_desc* d, const void* k, const void* v) {
 }
 
 // The rows kernel's counters, then partial sums: the tiles kernel's, and once those are joined the rows kernel's; at
-// the end the tiles kernel's two counters.
-constexpr int64_t kWorkspace = int64_t{32} << 20, kTileCounters = 256;
-int64_t workspace_bytes_needed() { return std::max(kWorkspace, hc::attend_paged_rows_bytes() + kTileCounters); }
+// the end the list of the runs to join and the tiles kernel's four counters.
+constexpr int64_t kWorkspace = int64_t{32} << 20, kTileCounters = 256, kJoinList = hc::kSplitRuns * 32;
+int64_t workspace_bytes_needed() { return std::max(kWorkspace, hc::attend_paged_rows_bytes() + kJoinList + kTileCounters); }
 
-int64_t part_bytes() { return workspace_bytes_needed() - kTileCounters - hc::attend_paged_counter_bytes(); }
+int64_t part_bytes() { return workspace_bytes_needed() - kJoinList - kTileCounters - hc::attend_paged_counter_bytes(); }
 
 // A request with more query rows (new tokens times query heads per cache head)
 // than this is attended in tiles of 256 rows on the 5th-generation tensor cores,
 // one with fewer in pieces of 16 rows whose keys are split over the SMs.  What
-// each takes, in us, fitted to both kernels on even lengths (1 to 64 requests of
-// 1000 to 16000 keys, 2 and 8 cache heads, 16 to 384 rows):
+// each takes, in us, fitted to both kernels (1 to 64 requests of 1000 to 30000
+// keys, 2 and 8 cache heads, 16 to 512 rows):
 //   pieces: 11 + 0.0118 (64 channels: 0.0062) for each piece and 128 keys of a head
-//   tiles:  8 + 1.27 (0.88) for each tile of the slowest SM
-// For example, of 128 channels, pieces against tiles: 8 heads of one request of
-// 1000 keys, 64 rows 16.5 against 20.8, 256 rows 24.6 against 21.7; of 16 requests
-// of 4000 keys, 16 rows 57 against 60, 32 rows 84 against 60.  Pieces share out
-// ragged lengths better than tiles do: what they take counts 0.85.
+//   tiles:  14 + 1.27 (0.88) for each tile of the slowest SM
+// The host knows the longest length at most.  Of many requests a piece's keys are
+// taken to be a quarter of it and the slowest SM's tiles half, of n the n-th of
+// the way back; and where some requests are in pieces and others in tiles, one
+// kernel waits for the other: 12.
+// Pieces against tiles, of 128 channels and 8 heads: one request of 3000 keys, 256
+// rows 41 against 31, of 1000 keys, 64 rows 17 against 25; 16 requests of 4000 keys,
+// 16 rows 57 against 60, 32 rows 84 against 60; 16 of 200 to 22000 keys, 64 rows
+// 193 against 103; of 64 channels, 2 heads, 37 of 60 to 8400 keys, 14 to 49 rows
+// 21 against 50, 112 rows 46 against 49.
 int rows_for_pieces(int64_t n_req, int64_t heads, int d_head, int64_t keys) {
   const int sms = hc::device_sm_count();
   constexpr int kMost = 1024;
   const int64_t each = n_req * heads, tiles = std::max<int64_t>(1, (keys + 127) / 128);
-  const double piece = 0.85 * (d_head == 128 ? 0.0118 : 0.0062) * static_cast<double>(each) * static_cast<double>(tiles);
+  const int64_t places = part_bytes() / (256 * (d_head * 4 + 8));
+  const double known = 1.0 / static_cast<double>(n_req);
+  const double piece = (0.25 + 0.75 * known) * (d_head == 128 ? 0.0118 : 0.0062) * static_cast<double>(each) * static_cast<double>(tiles);
   for (int block = 1; block * 256 <= kMost; ++block) {
-    const hc::Split split = hc::split_tiles(each * block, keys, part_bytes() / (256 * (d_head * 4 + 8)), sms);
-    const double time = 8 + (d_head == 128 ? 1.27 : 0.88) * static_cast<double>(split.time);
-    const double rows = 16 * std::floor((time - 0.85 * 11) / piece);
+    const double slowest = (0.5 + 0.5 * known) * hc::even_time(n_req, each * block, keys, 256, places, sms);
+    const double time = 14 + (d_head == 128 ? 1.27 : 0.88) * slowest + (n_req > 1 ? 12 : 0);
+    const double rows = 16 * std::floor((time - 11) / piece);
     if (rows < block * 256) return std::max(16, std::max(static_cast<int>(rows), (block - 1) * 256));
   }
   return kMost;

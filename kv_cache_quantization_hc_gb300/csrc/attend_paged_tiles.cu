@@ -98,7 +98,7 @@ struct Tiles {
 struct alignas(16) Work {
   PagedRequest rq;
   int r, head, row0, rows_all, tiles;  // tiles 0: no work, the CTA is done
-  int parts, part;  // of the run's tiles, and which of its partial sums this is (parts 1: the result)
+  int parts, part, first_part;  // of the run's tiles, and the places of this one's and the first one's sums (parts 1: the result)
   Range vis;        // its tiles: of this part
 };
 // Tile j of a work, from the last one on: its first key.
@@ -190,21 +190,20 @@ __device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// The run of rows that is number `idx` of the call's, whole, found by a warp
-// (all lanes get it); false past the last.  `c` goes forward only, so idx may
-// not fall.
-//
-// The order: works whose last rows see the most keys, by powers of two; within
-// one, by request and from its last rows.  Each class goes through the requests
-// again, so many requests, which even out by themselves, are one class.
+// The order of works: runs of 256 rows whose last rows see the most keys, by
+// powers of two; within one such class, by request and from its last rows; and a
+// run's parts, from its last tiles.  Each class goes through the requests again,
+// so many requests, which even out by themselves, are one class, and so are runs
+// that are shared out.
 constexpr int kFewestKeys = 256, kMostRequests = 256;
 struct Cursor {
   int r0 = 0, before = 0;  // first request of 32, works of those before it
-  int upto, from;          // this class' works see from `from` up to below `upto` keys
+  int upto, from;          // this class' runs see from `from` up to below `upto` keys
+  int target = INT_MAX;    // tiles of a part, or a few more
   // the lane's request, of the 32: read once as long as they stay, counted once a class
   bool read = false, counted = false;
   PagedRequest q;
-  int rows, runs, to_end, inc;
+  int rows, runs, parts, to_end, inc;  // parts: of each of its runs
   __device__ __forceinline__ void take_class(const AttendPagedParams& p) {
     from = p.n_req > kMostRequests || upto <= kFewestKeys ? 0 : upto == INT_MAX ? 1 << 30 : upto >> 1;
   }
@@ -213,7 +212,63 @@ struct Cursor {
     upto = p.n_req > kMostRequests || keys >= 1 << 30 ? INT_MAX : 1 << (32 - __clz(static_cast<int>(keys)));
     take_class(p);
   }
+  // Short parts need no order, and classes take time (37 requests of 60 to 8400 keys: 36 us in seven, 31 in one); long
+  // ones do (64 of 200 to 24000: 277 us and 298).
+  __device__ __forceinline__ void share_out(int tiles) {
+    target = tiles;
+    if (tiles < 16) upto = INT_MAX, from = 0;
+  }
 };
+__device__ __forceinline__ PagedRequest tiled_request(const AttendPagedParams& p, int r, int& rows) {
+  int bad = 0;  // lengths are reported by k_attend_paged_rows
+  PagedRequest q{0, 0, 0, 0};
+  if (r < p.n_req) q = load_request(p, r, bad);
+  rows = q.n * p.G > p.rows_above ? q.n * p.G : 0;
+  return q;
+}
+__device__ __forceinline__ int parts_of(int tiles, int target) { return max(1, tiles / target); }
+// How long the parts shall be, found by a warp: of one part a run and the rule's
+// choices the one of the least time, with a request's runs all as long as its last.
+__device__ __forceinline__ int part_tiles(const AttendPagedParams& p, int lane) {
+  constexpr int kEach = kSplitRequests / 32;
+  int tiles[kEach], runs[kEach];
+  float total = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    int rows;
+    const PagedRequest q = tiled_request(p, i * 32 + lane, rows);
+    runs[i] = (rows + kRowsTile - 1) / kRowsTile * p.H;
+    tiles[i] = rows > 0 ? visible<kKeys>(p, q, (rows - 1) / kRowsTile * kRowsTile, rows).tiles : 0;
+    total += static_cast<float>(runs[i]) * static_cast<float>(tiles[i]);
+  }
+  auto sum = [](float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  total = sum(total);
+  int best = INT_MAX;
+  float time = 0.f;
+#pragma unroll 1
+  for (int c = -1; c < SplitRule::kChoices; ++c) {
+    const int target = c < 0 ? INT_MAX : p.split.target(total, c);
+    float works = 0.f;
+    int longest = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int parts = parts_of(tiles[i], target);
+      works += static_cast<float>(runs[i]) * static_cast<float>(parts);
+      if (runs[i] > 0) longest = max(longest, (tiles[i] + parts - 1) / parts);
+    }
+    const float t = p.split.time(sum(works), static_cast<float>(__reduce_max_sync(0xffffffffu, longest)), total) +
+                    (c < 0 ? 0.f : SplitRule::kJoin);
+    if (c < 0 || t < time) {
+      time = t;
+      best = target;
+    }
+  }
+  return best;
+}
 // Runs of 256 rows of a request, of `runs` in all, whose last row's keys end at
 // `key` or later; positions do not fall, so they are the last ones.  Where they
 // do, which is flagged, it is some number that does not rise with `key` either:
@@ -231,19 +286,22 @@ __device__ __forceinline__ int runs_seeing(const AttendPagedParams& p, const Pag
   }
   return runs - lo;
 }
-__device__ __forceinline__ bool find_run(const AttendPagedParams& p, Cursor& c, int idx, int lane, Work& w) {
+// Work number `idx` of the call, found by a warp (all lanes get it); false past
+// the last.  `c` goes forward only, so idx may not fall.  A run's parts have equal
+// numbers of tiles but kLeastPartTiles at least; tiles 0 where it has no such part.
+__device__ __forceinline__ bool find_work(const AttendPagedParams& p, Cursor& c, int idx, int lane, Work& w) {
   for (;;) {
     if (!c.read) {
-      int bad = 0;  // lengths are reported by k_attend_paged_rows
-      c.q = PagedRequest{0, 0, 0, 0};
-      if (c.r0 + lane < p.n_req) c.q = load_request(p, c.r0 + lane, bad);
-      c.rows = c.q.n * p.G > p.rows_above ? c.q.n * p.G : 0;
+      c.q = tiled_request(p, c.r0 + lane, c.rows);
       c.runs = (c.rows + kRowsTile - 1) / kRowsTile;
+      c.parts = 1;
+      if (c.target != INT_MAX && c.rows > 0)
+        c.parts = parts_of(visible<kKeys>(p, c.q, (c.runs - 1) * kRowsTile, c.rows).tiles, c.target);
       c.read = true;
     }
     if (!c.counted) {
       c.to_end = runs_seeing(p, c.q, c.runs, c.from);
-      c.inc = (c.to_end - runs_seeing(p, c.q, c.runs, c.upto)) * p.H;
+      c.inc = (c.to_end - runs_seeing(p, c.q, c.runs, c.upto)) * p.H * c.parts;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, c.inc, o);
@@ -258,12 +316,20 @@ __device__ __forceinline__ bool find_run(const AttendPagedParams& p, Cursor& c, 
       w.rq = {__shfl_sync(0xffffffffu, c.q.q0, src), __shfl_sync(0xffffffffu, c.q.n, src),
               __shfl_sync(0xffffffffu, c.q.kv, src), __shfl_sync(0xffffffffu, c.q.prefix, src)};
       w.rows_all = __shfl_sync(0xffffffffu, c.rows, src);
-      const int left = __shfl_sync(0xffffffffu, c.before + c.inc, src) - 1 - idx;  // the last rows first
+      const int most = __shfl_sync(0xffffffffu, c.parts, src);
+      const int after = __shfl_sync(0xffffffffu, c.before + c.inc, src) - 1 - idx, left = after / most;  // the last rows first
+      const int i = most - 1 - (after - left * most);
+      w.part = idx;
+      w.first_part = idx - i;
       const int run = static_cast<int>(p.by_heads.div(left));
       w.head = left - run * p.H;
       w.row0 = (__shfl_sync(0xffffffffu, c.runs - c.to_end, src) + run) * kRowsTile;
       w.vis = visible<kKeys>(p, w.rq, w.row0, min(w.row0 + kRowsTile, w.rows_all));
-      w.tiles = w.vis.tiles;
+      const int each = max((w.vis.tiles + most - 1) / most, most > 1 ? kLeastPartTiles : 1), from = i * each;
+      w.parts = (w.vis.tiles + each - 1) / each;
+      w.tiles = max(0, min(each, w.vis.tiles - from));
+      w.vis.tile0 += w.vis.tiles - from - w.tiles;
+      w.vis.tiles = w.tiles;
       return true;
     }
     c.before += __shfl_sync(0xffffffffu, c.inc, 31);
@@ -278,24 +344,11 @@ __device__ __forceinline__ bool find_run(const AttendPagedParams& p, Cursor& c, 
     }
   }
 }
-
-// Where a call has fewer runs than SMs their tiles are shared out too: run idx
-// is parts idx * split + i, from its last tiles on, of equal numbers of tiles
-// but kLeastTiles at least.  False past the last; tiles 0 where the run has no
-// such part.
-constexpr int kLeastTiles = kLeastPartTiles;
-__device__ __forceinline__ bool find_work(const AttendPagedParams& p, Cursor& c, int idx, int lane, Work& w) {
-  const int run = p.split > 1 ? idx / p.split : idx;
-  if (!find_run(p, c, run, lane, w)) return false;
-  const int each = p.split > 1 ? max((w.tiles + p.split - 1) / p.split, kLeastTiles) : w.tiles;
-  const int i = idx - run * p.split, from = i * each;
-  w.parts = (w.tiles + each - 1) / each;
-  w.part = idx;
-  w.tiles = max(0, min(each, w.tiles - from));
-  w.vis.tile0 += w.vis.tiles - from - w.tiles;
-  w.vis.tiles = w.tiles;
-  return true;
-}
+// A run whose parts are to be joined.
+struct alignas(32) Join {
+  int q0, rows_all, head, row0, parts, part;
+};
+__device__ __forceinline__ Join* joins(const AttendPagedParams& p) { return reinterpret_cast<Join*>(p.part_sums + p.part_bytes); }
 // A part's sums in the workspace: O by fours of channels [D / 4][rows], then (reference, sum) [rows].
 template <int D>
 __device__ __forceinline__ float4* part_sums(const AttendPagedParams& p, int part) {
@@ -776,6 +829,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
       // ================================================== works, found ahead of the warps that do them
       // The first is the CTA's number; the others are taken from a counter, each when the one before is nearly loaded.
       Cursor cursor(p);
+      if (p.may_split) cursor.share_out(part_tiles(p, lane));
       Work work;
       int number = blockIdx.x;
       bool taken = false;
@@ -798,6 +852,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         } while (more && work.tiles == 0);
         if (!more) work.tiles = 0;
         if (lane == 0) {
+          if (more && work.parts > 1 && work.part == work.first_part)
+            joins(p)[atomicAdd(p.tiles_taken + 2, 1)] = {work.rq.q0, work.rows_all, work.head, work.row0, work.parts, work.part};
           sh.work[k % kWorksAhead] = work;
           mbar_arrive(&sh.work_full[k % kWorksAhead]);
         }
@@ -1025,51 +1081,54 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
 }
 
 // The parts' sums of a run joined, in their order: 32 rows of a run a CTA, a
-// lane for each.
+// lane for each, several parts' sums on their way together.
 constexpr int kJoinThreads = 256;
 template <bool kBf16, int D>
-__global__ void __launch_bounds__(kJoinThreads) k_join_paged_tiles(const __grid_constant__ AttendPagedParams p) {
-  __shared__ Work shared;
-  __shared__ bool there;
+__global__ void __launch_bounds__(kJoinThreads, 2) k_join_paged_tiles(const __grid_constant__ AttendPagedParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunks = p.part_rows / 32, run = blockIdx.x / chunks, at = (blockIdx.x - run * chunks) * 32 + lane;
-  if (warp == 0) {
-    Cursor cursor(p);
-    Work work;
-    const bool found = find_work(p, cursor, run * p.split, lane, work);
-    if (lane == 0) {
-      shared = work;
-      there = found;
-    }
-  }
+  const bool there = run < __ldcg(p.tiles_taken + 2);
   __syncthreads();
-  if (!there || shared.parts == 1) return;
-  const Work& work = shared;
-  const int row = work.row0 + at;
-  if (row >= work.rows_all) return;
+  // the last CTA to come here leaves the counters as they were found
+  if (threadIdx.x == 0 && atomicAdd(p.tiles_taken + 3, 1) == static_cast<int>(gridDim.x) - 1) {
+    p.tiles_taken[2] = 0;
+    p.tiles_taken[3] = 0;
+  }
+  if (!there) return;
+  const Join w = joins(p)[run];
+  const int row = w.row0 + at;
+  if (row >= w.rows_all) return;
   const int token = static_cast<int>(p.by_group.div(row));
-  const int64_t t = work.rq.q0 + token, head = work.head * p.G + row - token * p.G;
+  const int64_t t = w.q0 + token, head = w.head * p.G + row - token * p.G;
   uint16_t* const out = static_cast<uint16_t*>(p.out) + t * p.o_token + head * p.o_head;
   constexpr int kFours = D / 4 / (kJoinThreads / 32);  // of channels, of a thread
+  constexpr int kAtOnce = 16 / kFours;
   float top = kNegInf, sum = 0.f;
   float4 acc[kFours];
 #pragma unroll
   for (int i = 0; i < kFours; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int k = 0; k < work.parts; ++k) {
-    const float4* const sums = part_sums<D>(p, work.part + k);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(sums + D / 4 * p.part_rows) + at);
-    float4 v[kFours];
+#pragma unroll 1
+  for (int k = 0; k < w.parts; k += kAtOnce) {
+    float2 ml[kAtOnce];
+    float4 v[kAtOnce][kFours];
 #pragma unroll
-    for (int i = 0; i < kFours; ++i) v[i] = __ldcg(sums + (warp * kFours + i) * p.part_rows + at);
-    if (ml.x == kNegInf) continue;
-    const float to = fmaxf(top, ml.x), old = ex2(top - to), wt = ex2(ml.x - to);  // top -inf: old 0
-    top = to;
-    sum = sum * old + wt * ml.y;
+    for (int u = 0; u < kAtOnce; ++u) {
+      const float4* const sums = part_sums<D>(p, w.part + min(k + u, w.parts - 1));
+      ml[u] = __ldcg(reinterpret_cast<const float2*>(sums + D / 4 * p.part_rows) + at);
 #pragma unroll
-    for (int i = 0; i < kFours; ++i) {
-      acc[i].x = acc[i].x * old + wt * v[i].x, acc[i].y = acc[i].y * old + wt * v[i].y;
-      acc[i].z = acc[i].z * old + wt * v[i].z, acc[i].w = acc[i].w * old + wt * v[i].w;
+      for (int i = 0; i < kFours; ++i) v[u][i] = __ldcg(sums + (warp * kFours + i) * p.part_rows + at);
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (k + u >= w.parts || ml[u].x == kNegInf) continue;
+      const float to = fmaxf(top, ml[u].x), old = ex2(top - to), wt = ex2(ml[u].x - to);  // top -inf: old 0
+      top = to;
+      sum = sum * old + wt * ml[u].y;
+#pragma unroll
+      for (int i = 0; i < kFours; ++i) {
+        acc[i].x = acc[i].x * old + wt * v[u][i].x, acc[i].y = acc[i].y * old + wt * v[u][i].y;
+        acc[i].z = acc[i].z * old + wt * v[u][i].z, acc[i].w = acc[i].w * old + wt * v[u][i].w;
+      }
     }
   }
   const float by = sum > 0.f ? 1.f / sum : 0.f;
@@ -1147,15 +1206,16 @@ cudaError_t launch(AttendPagedParams p, cudaStream_t s) {
   p.q_tma = queries_map<kBf16>(&q_map, p, D);
   const int64_t rows = static_cast<int64_t>(p.max_new) * p.G, runs = (rows + kRowsTile - 1) / kRowsTile * p.n_req * p.H;
   p.part_rows = static_cast<int32_t>(std::min<int64_t>((rows + 31) / 32 * 32, kRowsTile));
-  const int64_t keys = static_cast<int64_t>(p.table_width) << p.B_log2;
-  p.split = split_tiles(runs, keys, p.part_bytes / (p.part_rows * (D * 4 + 8)), resident).parts;
-  const int64_t works = runs * p.split;
+  const int64_t keys = static_cast<int64_t>(p.table_width) << p.B_log2, places = p.part_bytes / (p.part_rows * (D * 4 + 8));
+  p.may_split = split_rule(p.n_req, runs, keys, p.part_rows, places, resident, &p.split);
+  // a CTA per work, as far as the host can tell
+  const int64_t works = p.may_split ? resident : runs;
   const int grid = static_cast<int>(std::min<int64_t>(works, resident));
   // the longest wait is for a whole run, whose tiles take 1 to 2 us each
   p.wait_limit = kWaitLimit + static_cast<uint64_t>(keys / kKeys) * 20000;
   k_attend_paged_tiles<kBf16, D, kScores><<<grid, kThreadsTiles, Tiles<D>::kAsk, s>>>(p, k_map, v_map, q_map);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.split == 1) return e;
+  if (e != cudaSuccess || !p.may_split) return e;
   const unsigned chunks = static_cast<unsigned>(p.part_rows / 32);
   k_join_paged_tiles<kBf16, D><<<static_cast<unsigned>(runs) * chunks, kJoinThreads, 0, s>>>(p);
   return cudaGetLastError();

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 
 #include "serve.cuh"
 
@@ -26,6 +27,51 @@ struct AppendPagedParams {
   int64_t n_rows;  // num_slots * block_size
   int32_t* err;
 };
+
+// How the tiles of runs of 256 rows are shared out over the SMs where a call has
+// few runs: a run of n tiles (of 128 keys) is max(1, n / target) parts.  Decided
+// by the kernel, which sees the lengths, and by the host as if they were even.
+constexpr int kLeastPartTiles = 4;
+struct SplitRule {
+  float by_sms = 0.f, by_places = 0.f;  // reciprocals: of the SMs, of the parts that there may be beside one of each run
+  // Of three choices, as many parts as 1, 2 or 3 an SM; all parts have a place.
+  static constexpr int kChoices = 3;
+  HC_HD int target(float total, int c) const {
+    const float want = total * by_sms * (c == 0 ? 1.f : c == 1 ? 0.5f : 1.f / 3.f), fits = total * by_places;
+    const float t = ceilf(want > fits ? want : fits);
+    return t < kLeastPartTiles ? kLeastPartTiles : t > 0x1p30f ? 1 << 30 : static_cast<int>(t);
+  }
+  // The time of the slowest SM, in tiles, where they take `works` parts of at most `longest` tiles, `total` in all, as
+  // they come: a part's start and end take 3.
+  HC_HD float time(float works, float longest, float total) const {
+    const float waves = ceilf(works * by_sms - 1e-3f) * (longest + 3.f), even = (total + 3.f * works) * by_sms + longest + 3.f;
+    return works * by_sms <= 1.001f || waves < even ? waves : even;
+  }
+  static constexpr float kJoin = 6.f;  // the time of the join
+};
+// Whether a call's runs may be shared out: a lane holds 5 requests, part sums have
+// places, and the join is one wave of CTAs of 32 rows.
+constexpr int kSplitRequests = 160, kSplitRuns = 2000;
+inline bool split_rule(int64_t n_req, int64_t runs, int64_t keys, int64_t part_rows, int64_t places, int sms, SplitRule* rule) {
+  rule->by_sms = 1.f / static_cast<float>(sms);
+  if (n_req > kSplitRequests || keys <= 2 * kLeastPartTiles * 128 || places < runs + sms / 2 ||
+      runs * (part_rows / 32) > int64_t{8} * sms || runs > kSplitRuns)
+    return false;
+  rule->by_places = 1.0001f / static_cast<float>(places - runs);
+  return true;
+}
+// The time of `runs` runs of as many tiles each.
+inline float even_time(int64_t n_req, int64_t runs, int64_t keys, int64_t part_rows, int64_t places, int sms) {
+  SplitRule rule;
+  const float n = static_cast<float>(runs), tiles = static_cast<float>(std::max<int64_t>(1, (keys + 127) / 128));
+  const bool may = split_rule(n_req, runs, keys, part_rows, places, sms, &rule);
+  float best = rule.time(n, tiles, n * tiles);
+  for (int c = 0; may && c < SplitRule::kChoices; ++c) {
+    const float parts = std::max(1.f, std::floor(tiles / static_cast<float>(rule.target(n * tiles, c))));
+    if (parts > 1.f) best = std::min(best, rule.time(n * parts, std::ceil(tiles / parts), n * tiles) + SplitRule::kJoin);
+  }
+  return best;
+}
 
 struct AttendPagedParams {
   const void* q;
@@ -53,10 +99,13 @@ struct AttendPagedParams {
   int32_t q_tma;        // of the tiles kernel: 128 rows of queries are a box of whole tokens
   uint64_t wait_limit;  // of the tiles kernel: ns
   uint8_t* workspace;
-  int32_t* tiles_taken;  // in the workspace: works of the tiles kernel that are taken, CTAs that are done
+  // in the workspace: works of the tiles kernel that are taken, CTAs that are done; runs to join, CTAs that are done
+  int32_t* tiles_taken;
   uint8_t* part_sums;    // in the workspace, where the rows kernel has its partial sums later
-  int64_t part_bytes;
-  int32_t split, part_rows;  // of the tiles kernel: parts of a run's tiles, rows of a part's sums
+  int64_t part_bytes;    // the list of runs to join is behind them
+  // of the tiles kernel: whether runs may be shared out, and how; rows of a part's sums
+  int32_t may_split, part_rows;
+  SplitRule split;
   int32_t* err;
 };
 
@@ -76,29 +125,6 @@ struct MergeParams {
 // grid, and with the two partial results per CTA that follow.
 int64_t attend_paged_counter_bytes();
 int64_t attend_paged_rows_bytes();
-
-// Parts that the tiles of a run of 256 rows are shared out in where a call has
-// fewer runs than SMs, and the time of the slowest SM in tiles of 128 keys: a
-// part's start and end take 3, the join of the parts 6.  At most `places` parts
-// of all runs fit the workspace.
-constexpr int kLeastPartTiles = 4;
-struct Split {
-  int parts;
-  int64_t time;
-};
-inline Split split_tiles(int64_t runs, int64_t keys, int64_t places, int sms) {
-  const int64_t tiles = std::max<int64_t>(1, (keys + 127) / 128), waves = (runs + sms - 1) / sms;
-  Split best{1, waves * (tiles + 3)};
-  if (runs >= sms) return best;
-  const int64_t most = std::min((tiles + kLeastPartTiles - 1) / kLeastPartTiles, places / runs);
-  for (int64_t w = 1; w <= 3; ++w) {  // as many parts as w of them an SM
-    const int64_t n = std::min(most, w * sms / runs);
-    if (n < 2) continue;
-    const int64_t time = w * ((tiles + n - 1) / n + 3) + 6;
-    if (time < best.time) best = {static_cast<int>(n), time};
-  }
-  return best;
-}
 
 cudaError_t launch_append_paged(int dtype, int pairing, const AppendPagedParams& p, cudaStream_t s);
 // The requests with at most p.rows_above query rows, and those with more.

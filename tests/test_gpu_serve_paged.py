@@ -156,10 +156,10 @@ def test_attend_split_over_ctas(serve, workspace, n_req):  # noqa: F811
     assert int(workspace[:4096].count_nonzero()) == 0
 
 
-SPLITS = [dict(kv_lens=[5000], new_lens=[80], Hq=12, H=1, d=64, B=16), dict(kv_lens=[4100, 3], new_lens=[150, 3], Hq=4, H=2, d=128, B=64, dtype="f16"),
+SPLITS = [dict(kv_lens=[5000], new_lens=[80], Hq=12, H=1, d=64, B=16), dict(kv_lens=[4100, 3], new_lens=[300, 3], Hq=4, H=2, d=128, B=64, dtype="f16"),
           dict(kv_lens=[3000, 900, 2100], new_lens=[40, 700, 100], Hq=10, H=1, d=128, B=32),
-          dict(kv_lens=[6000], new_lens=[450], Hq=2, H=2, d=64, B=128, window=2500), dict(kv_lens=[4000, 2600], new_lens=[90, 90], Hq=8, H=1, d=64, B=16, dtype="f16", softcap=20.0, slopes=True),
-          dict(kv_lens=[3500], new_lens=[450], Hq=2, H=1, d=128, B=16, prefix=[3400], softcap=30.0)]
+          dict(kv_lens=[6000], new_lens=[450], Hq=2, H=2, d=64, B=128, window=2500), dict(kv_lens=[4000, 2600], new_lens=[200, 200], Hq=8, H=1, d=64, B=16, dtype="f16", softcap=20.0, slopes=True),
+          dict(kv_lens=[3500], new_lens=[600], Hq=2, H=1, d=128, B=16, prefix=[3400], softcap=30.0)]
 
 
 @pytest.mark.parametrize("case", SPLITS, ids=lambda c: "-".join(map(str, c["kv_lens"] + c["new_lens"])))

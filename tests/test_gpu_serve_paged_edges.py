@@ -86,3 +86,16 @@ def test_a_call_of_one_row_and_any_strides(serve, workspace):  # noqa: F811
     got = serve.attend_paged(**dict(t, q=odd(t["q"], 1, 3, 1), k_pages=odd(t["k_pages"], 5, 64, 7, 1),
                                     v_pages=odd(t["v_pages"], 9, 64, 1, 1)), max_new=1, workspace=workspace, err=err)
     assert torch.equal(got, want) and int(err) == 0
+
+
+@pytest.mark.parametrize("dtype,d,prefix", [("bf16", 128, False), ("f16", 64, True)])
+def test_ragged_lengths_shared_out(serve, workspace, dtype, d, prefix):  # noqa: F811
+    """A long request among short ones, in tiles: its keys are many parts, theirs are one; some see nothing."""
+    import torch
+    kv = [7000, 30, 700, 0, 2500, 3, 120, 900]
+    new = [70, 30, 64, 2, 0, 3, 65, 90]
+    c = Pages(35, kv, new, Hq=16, H=2, d=d, B=16, dtype=dtype, prefix=[50, 0, 9000, 0, 5, 1, 100, 300] if prefix else None)
+    assert 64 * 8 > serve.attend_paged_few_rows(len(kv), c.H, c.d, c.table.shape[1] * c.B)
+    a, b = check_attend(serve, workspace, c), check_attend(serve, workspace, c)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))        # the same bits every time
+    assert int(workspace[:4096].count_nonzero()) == 0 and int(workspace[-256:].count_nonzero()) == 0
