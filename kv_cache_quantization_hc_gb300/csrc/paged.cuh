@@ -49,8 +49,8 @@ struct SplitRule {
   }
   static constexpr float kJoin = 6.f;  // the time of the join
 };
-// Whether a call's runs may be shared out: a lane holds 5 requests, part sums have
-// places, and the join is one wave of CTAs of 32 rows.
+// Whether a call's runs may be shared out: a warp goes through the requests
+// several times, part sums have places, and the join is one wave of CTAs of 32 rows.
 constexpr int kSplitRequests = 160, kSplitRuns = 2000;
 inline bool split_rule(int64_t n_req, int64_t runs, int64_t keys, int64_t part_rows, int64_t places, int sms, SplitRule* rule) {
   rule->by_sms = 1.f / static_cast<float>(sms);
@@ -103,8 +103,7 @@ struct AttendPagedParams {
   int32_t* tiles_taken;
   uint8_t* part_sums;    // in the workspace, where the rows kernel has its partial sums later
   int64_t part_bytes;    // the list of runs to join is behind them
-  // of the tiles kernel: whether runs may be shared out, and how; rows of a part's sums
-  int32_t may_split, part_rows;
+  int32_t part_rows;    // of the tiles kernel where runs may be shared out: rows of a part's sums
   SplitRule split;
   int32_t* err;
 };
