@@ -10,7 +10,9 @@
  *     key pair rotated by delta-m = m_new - m_old, using the SO(2) identity
  *     R(m_new t) = R(delta-m t) R(m_old t) ("Core Design", relative RoPE
  *     paragraph), dequantized and rotated "on the fly" ("Example output",
- *     part B, live fetch), then placed in the paged buffer.
+ *     part B, live fetch), then placed in the paged buffer;
+ *   - serving from the 4-bit wire and from the paged buffer: new tokens written,
+ *     attention over either, and results over both joined.
  *
  * Conventions shared by every call
  * --------------------------------

@@ -23,7 +23,12 @@
 //   rounded as coarsely as the output.  fp16 ends at 65504 and 2^-24, so there
 //   up = 15: what is below 2^-39 of a row's largest is lost.
 //
-// Bound: the cache's bytes.
+// Bound: the cache's bytes.  64 requests of 200 to 25000 keys, 32 query and 8
+// cache heads of 128 bf16 channels: 204 us, 6.6 TB/s, 97% of the measured copy
+// rate; 8 requests of 131000 keys, 8 query heads a cache head: 600 us, 7.2 TB/s.
+// With few keys a CTA, latency: one request of 1000 keys 10 us (lengths, slots,
+// keys, partial sums: a chain of reads).  Several pieces of a request each read
+// its keys: 37 requests, 14 to 49 rows, 20.6 us of 4.9.
 #include <algorithm>
 
 #include "attend_paged_common.cuh"
