@@ -632,7 +632,7 @@ typedef struct hc_attend_scores {
  * of more rows is attended in tiles of 256 rows with probabilities in the pages'
  * dtype.  So the last bits of a request's result depend on the other requests of
  * its call and the width of its tables, which the limit and where keys are split
- * depend on; for the same call they are the same every time.  In f16 what is below 2^-29 of
+ * depend on; for the same call they are the same every time.  In f16 what is below 2^-28 of
  * a row's largest probability may be lost.  Values are below 2^80 in magnitude. */
 int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_tokens, int32_t n_q_heads,
                     const hc_paged_desc* desc, const void* k_pages, const void* v_pages, const int32_t* block_tables,

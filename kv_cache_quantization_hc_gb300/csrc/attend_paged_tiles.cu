@@ -35,11 +35,16 @@
 //   well; and a bias by distance has its largest scores there.
 // * bf16 has fp32's range, so m is the maximum of the first tile and moves only
 //   when a tile's probabilities sum up to 2^40; no maximum is looked for
-//   otherwise.  fp16 ends at 65504: top = 11.5, m is 3 above the maximum and
-//   moves when that exceeds m by 3.5 or a tile's sum passes 60000; a
-//   probability keeps 11 bits down to 2^-22 of the largest.  Rows that see n
-//   keys in all, fewer than a tile, have m 128 / n times lower; rows that see n
-//   in their first tile and more later, sqrt(128 / n) times higher.
+//   otherwise.  fp16 ends at 65504: top = 11.5, m is 5 above the maximum and
+//   moves when a tile's sum passes 60000 and one of it 65504; a probability keeps
+//   11 bits down to 2^-20 of the largest.  Rows that see n keys in all, fewer than
+//   a tile, have m 3 above and 128 / n times lower; rows that see n in their first
+//   tile and more later, sqrt(128 / n) times higher.
+// * A move costs a tile 4000 cycles, and one row of 32 is enough.  So in fp16 the
+//   last two tiles change places: the first has 128 keys for most rows, whose
+//   largest tells more than that of a few (and see kAhead: of 8192 tokens' scores
+//   with a few large channels 1.2% of a warp's tiles moved, 0.4% with the tiles in
+//   this order, 0.05% with 5 above instead of 3).
 //
 // Bound: the tensor cores (4 d flops per row and key).  8192 tokens of 32 query
 // and 8 cache heads of 128 channels: bf16 314 us, 1.75 PFLOP/s, 90% of the
@@ -83,11 +88,11 @@ template <bool kBf16>
 struct Softmax;
 template <>
 struct Softmax<true> {
-  static constexpr float kTop = 0.f, kMoveAt = 30.f, kAhead = 0.f, kMostSum = 0x1p40f;
+  static constexpr float kTop = 0.f, kMoveAt = 30.f, kAhead = 0.f, kAheadOfAll = 0.f, kMostSum = 0x1p40f;
 };
 template <>
 struct Softmax<false> {
-  static constexpr float kTop = 11.5f, kMoveAt = 3.5f, kAhead = 3.f, kMostSum = 60000.f;
+  static constexpr float kTop = 11.5f, kMoveAt = 3.5f, kAhead = 5.f, kAheadOfAll = 3.f, kMostSum = 60000.f;
 };
 
 // Tensor memory is full: see above.  A half's next scores wait for its probabilities' product
@@ -111,8 +116,12 @@ struct alignas(16) Work {
   int parts, part, first_part;  // of the run's tiles, and the places of this one's and the first one's sums (parts 1: the result)
   Range vis;        // its tiles: of this part
 };
-// Tile j of a work, from the last one on: its first key.
-__device__ __forceinline__ int tile_key(const Range& v, int j) { return (v.tile0 + v.tiles - 1 - j) * kKeys; }
+// Tile j of a work, from the last one on (kFullFirst: the last two change places): its first key.
+template <bool kFullFirst>
+__device__ __forceinline__ int tile_key(const Range& v, int j) {
+  const int at = kFullFirst && j < 2 && v.tiles > 1 ? 1 - j : j;
+  return (v.tile0 + v.tiles - 1 - at) * kKeys;
+}
 // Whether some key of the tile is seen by no row of the work.
 __device__ __forceinline__ bool at_edge(const Range& v, int key0) { return key0 < v.lo || key0 + kKeys > v.hi; }
 
@@ -374,6 +383,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
   using L = Tiles<D>;
   using Soft = Softmax<kBf16>;
   constexpr int kStages = L::kStages, kBuffers = L::kBuffers;
+  constexpr bool kFullFirst = !kBf16 && kScores != kBiased;
   extern __shared__ unsigned char dyn_raw[];
   __shared__ TileShared<D> sh;
   unsigned char* const dyn = dyn_raw + (1024 - (smem_addr(dyn_raw) & 1023)) % 1024;
@@ -478,8 +488,9 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
       }
 
       float m = kNegInf, l = 0.f;
-      int key0 = tile_key(work.vis, 0);
-      for (int j = 0; j < tiles && ok; ++j, key0 -= kKeys) {
+      const Range vis = work.vis;
+      for (int j = 0; j < tiles && ok; ++j) {
+        const int key0 = tile_key<kFullFirst>(vis, j);
         const int n = 2 * (base + j) + half, buffer = n % kBuffers;
         const uint32_t s_at = tmem + lanes + buffer * 128;
         const int lo = first - key0, hi = last - key0;  // columns [lo, hi) count
@@ -509,8 +520,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           if (!kBf16) {
             const auto steps = [](int n) { return static_cast<float>(__clz(max(n - 1, 0)) - __clz(kKeys - 1)); };  // log2(128 / n)
             const int all = last - first, here = min(hi, kKeys) - max(lo, 0);
-            if (all < kKeys)  // few keys in all: as much lower, as n of them do not pass kMostSum either
-              ahead -= steps(all);
+            if (all < kKeys)  // few keys in all: as low as n of them do not pass kMostSum
+              ahead = Soft::kAheadOfAll - steps(all);
             else if (here < kKeys)  // few keys here: half as much higher, as larger ones may follow
               ahead += 0.5f * steps(here);
           }
@@ -744,7 +755,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         auto slot_of = [&](int j) {
           int slot = p.num_slots;
           if (lane < slots && j < tiles) {
-            const int key = tile_key(vis, j) + lane * block;
+            const int key = tile_key<kFullFirst>(vis, j) + lane * block;
             if (key < vis.hi && key + block > vis.lo) {
               slot = __ldg(table + (key >> p.B_log2));
               if (static_cast<uint32_t>(slot) >= static_cast<uint32_t>(p.num_slots)) {
@@ -778,7 +789,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
           load(tiles_at + L::kK + st * L::kTileBytes, &k_map, &sh.k_full[st], slot);
           if (round > 0) ok = mbar_wait_inline(&sh.v_empty[st], (round - 1) & 1, &sh.dead, p.wait_limit);
           if (!__all_sync(0xffffffffu, ok)) break;
-          const bool edge = at_edge(vis, tile_key(vis, j));
+          const bool edge = at_edge(vis, tile_key<kFullFirst>(vis, j));
           uint64_t* const full = edge ? &sh.v_edge[st] : &sh.v_full[st];
           if (lane == 0) mbar_expect(full, L::kTileBytes);
           __syncwarp();
@@ -819,7 +830,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         const Range vis = sh.work[k % kWorksAhead].vis;
         leave_work(k);
         for (int j = 0; j < vis.tiles && ok; ++j) {
-          const int key0 = tile_key(vis, j), st = (base + j) % kStages;
+          const int key0 = tile_key<kFullFirst>(vis, j), st = (base + j) % kStages;
           if (!at_edge(vis, key0)) continue;
           ok = mbar_wait_inline(&sh.v_edge[st], edges >> st & 1u, &sh.dead, p.wait_limit);
           if (!__all_sync(0xffffffffu, ok)) break;

@@ -74,11 +74,11 @@ def out_bar(out, weight, reach, far, vmax, d, dtype, few, softcap=0.0):
     errors move the weights by twice that against their sum; exponentials and
     sums are good to 2^-20; probabilities are rounded to the values' type (few
     rows: to 16 bits, the upper 8 cut off and the rest rounded, or 22); in fp16
-    what is below 2^-14 is off by up to 2^-25, where the largest stands at 2^5 or
-    more (11.5 less 3 and at most 3.5; few rows: at 2^15), so n <= 512 keys lose at
-    most 2^-30 * 512 = 2^-21 of the largest value; and the output is rounded."""
+    what is below 2^-14 is off by up to 2^-25, where the largest stands at 2^3 or
+    more (11.5 less 5 and at most 3.5; few rows: at 2^15), so n <= 512 keys lose at
+    most 2^-28 * 512 = 2^-19 of the largest value; and the output is rounded."""
     u = {"bf16": 2.0 ** -15, "f16": 2.0 ** -21}[dtype] if few else HALF[dtype]
-    lost = (2.0 ** -31 if few else 2.0 ** -21) * vmax if dtype == "f16" else 0.0
+    lost = (2.0 ** -31 if few else 2.0 ** -19) * vmax if dtype == "f16" else 0.0
     tiny = 2.0 ** -24 if dtype == "f16" else 0.0
     return (weight * (u + 2 * score_error(reach, far, d, softcap)[..., None] + 2.0 ** -20) * 1.05 + HALF[dtype] * np.abs(out) * 1.01
             + lost + tiny)
