@@ -29,7 +29,8 @@ BINDING = os.path.join(PKG, "_serve" + (sysconfig.get_config_var("EXT_SUFFIX") o
 SOURCES = ["api.cu", "encode.cu", "encode_rows.cu", "fetch_fp8.cu", "fetch_fp8_rows.cu",
            "fetch_int4.cu", "fetch_raw.cu", "table.cu", "crc32.cu", "select.cu",
            "api_serve.cu", "block_tables.cu", "rope_axes.cu", "append.cu", "attend.cu",
-           "attend_tiles.cu", "api_paged.cu", "append_paged.cu", "attend_paged.cu", "attend_paged_tiles.cu", "merge.cu",
+           "attend_tiles.cu", "api_paged.cu", "append_paged.cu", "attend_paged.cu",
+           "attend_paged_tiles_64.cu", "attend_paged_tiles_128.cu", "merge.cu",
            "hash.cpp"]
 
 
@@ -41,9 +42,6 @@ def _headers():
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
-
-# a file of many kernels, compiled several at a time (70 s -> 26)
-FILE_FLAGS = {"attend_paged_tiles.cu": ["--split-compile=0"]}
 
 _ELF_MACHINE = {"x86_64": 62, "aarch64": 183, "arm64": 183}
 
@@ -146,7 +144,7 @@ def _build_library(lib, build_dir, verbose, extra_flags, ex):
 
     def compile_one(src):
         obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
-        _run(f"nvcc on {src}", [nvcc, *FLAGS, *FILE_FLAGS.get(src, []), *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
+        _run(f"nvcc on {src}", [nvcc, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
         return obj
 
     objs = list(ex.map(compile_one, SOURCES))

@@ -215,7 +215,7 @@ int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_
   p.rows_above = rows_above;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (int64_t{max_new} * G > p.rows_above) {
-    const int t = hc::record_cuda(hc::launch_attend_paged_tiles(d, p, s));
+    const int t = hc::record_cuda(d == 64 ? hc::launch_attend_paged_tiles_64(p, s) : hc::launch_attend_paged_tiles_128(p, s));
     if (t != HC_OK) return t;
   }
   return hc::record_cuda(hc::launch_attend_paged_rows(d, p, s));

@@ -54,6 +54,8 @@
 // of 142), and with capped scores, whose polynomial is as long as the rest of it
 // (two prompts of 4097 and 3001 tokens: tensor cores 30% active instead of 61%).
 // Runs of few tiles: a run's first tile takes 1500 to 2300 cycles more.
+#pragma once
+
 #include <algorithm>
 #include <climits>
 #include <cuda.h>
@@ -1258,14 +1260,9 @@ cudaError_t launch_parts(AttendPagedParams p, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t launch_type(const AttendPagedParams& p, cudaStream_t s) {
+cudaError_t launch_tiles(const AttendPagedParams& p, cudaStream_t s) {
   return p.bf16 ? launch_parts<true, D>(p, s) : launch_parts<false, D>(p, s);
 }
 
 }  // namespace
-
-cudaError_t launch_attend_paged_tiles(int d, const AttendPagedParams& p, cudaStream_t s) {
-  return d == 64 ? launch_type<64>(p, s) : launch_type<128>(p, s);
-}
-
 }  // namespace hc

@@ -128,7 +128,8 @@ int64_t attend_paged_rows_bytes();
 cudaError_t launch_append_paged(int dtype, int pairing, const AppendPagedParams& p, cudaStream_t s);
 // The requests with at most p.rows_above query rows, and those with more.
 cudaError_t launch_attend_paged_rows(int d, const AttendPagedParams& p, cudaStream_t s);
-cudaError_t launch_attend_paged_tiles(int d, const AttendPagedParams& p, cudaStream_t s);
+cudaError_t launch_attend_paged_tiles_64(const AttendPagedParams& p, cudaStream_t s);
+cudaError_t launch_attend_paged_tiles_128(const AttendPagedParams& p, cudaStream_t s);
 cudaError_t launch_merge(int dtype, const MergeParams& p, cudaStream_t s);
 
 }  // namespace hc
