@@ -5,7 +5,7 @@
 // One CTA per SM takes runs of 256 rows as they come, the longest first.  Its 16
 // warps each go through the runs by themselves, so that one's keys are loaded
 // while the last one's result is still written (runs in a fixed order, and queries
-// and results by the softmax's warps: 8192 tokens 334 us, so 314):
+// and results by the softmax's warps: 8192 tokens 334 us, like this 314):
 //   warps 0-3, 4-7  the softmax of rows 0-127 and 128-255, a thread per row;
 //   warp 8          keys and values by TMA, a block of the buffer at a time,
 //                   issued by one thread (by a lane per copy: 387 us);
@@ -47,13 +47,13 @@
 //   this order, 0.05% with 5 above instead of 3).
 //
 // Bound: the tensor cores (4 d flops per row and key).  8192 tokens of 32 query
-// and 8 cache heads of 128 channels: bf16 314 us, 1.75 PFLOP/s, 90% of the
-// measured peak; fp16 364 us, where the same products draw more power (a library's
-// large one runs at 1.71 PFLOP/s against 1.82).  What the softmax adds to shows
-// with 64 channels, whose tiles are half the products for the same softmax (227 us
+// and 8 cache heads of 128 channels: bf16 314 to 324 us, 1.70 to 1.75 PFLOP/s, 88
+// to 90% of the measured peak; fp16 349 us, where the same products draw more power
+// (a library's large one runs at 1.71 PFLOP/s against 1.82).  The softmax shows
+// with 64 channels, whose tiles are half the products for the same softmax (232 us
 // of 142), and with capped scores, whose polynomial is as long as the rest of it
-// (two prompts of 4097 and 3001 tokens: tensor cores 30% active instead of 61%).
-// Runs of few tiles: a run's first tile takes 1500 to 2300 cycles more.
+// (516 us; two prompts of 3001 to 4097 tokens: tensor cores 39% active).  Runs of
+// few tiles: a run's first tile takes 1500 to 2300 cycles more.
 #pragma once
 
 #include <algorithm>
