@@ -99,3 +99,11 @@ def test_ragged_lengths_shared_out(serve, workspace, dtype, d, prefix):  # noqa:
     a, b = check_attend(serve, workspace, c), check_attend(serve, workspace, c)
     assert all(torch.equal(x, y) for x, y in zip(a, b))        # the same bits every time
     assert int(workspace[:4096].count_nonzero()) == 0 and int(workspace[-256:].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("n_req,dtype", [(170, "bf16"), (300, "f16")])
+def test_many_requests_in_tiles(serve, workspace, n_req, dtype):  # noqa: F811
+    """More requests than are shared out, and than are put in order of their lengths, each of more rows than go in pieces."""
+    r = np.random.default_rng(n_req)
+    kv = [int(v) for v in r.integers(1, 200, n_req)]
+    check_attend(serve, workspace, Pages(36, kv, [17 if i % 50 else 3 for i in range(n_req)], Hq=64, H=1, d=64, B=16, dtype=dtype))
