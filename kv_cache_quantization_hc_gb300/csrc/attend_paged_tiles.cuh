@@ -467,8 +467,9 @@ __global__ void __launch_bounds__(kThreadsTiles, 1)
         if (kScores == kBiased) slope = p.slopes ? __ldg(p.slopes + head) * kLog2e : 0.f;
       }
 
-      // what a hidden score is overwritten with: -inf once it is multiplied (a factor of 0 would make it NaN)
-      const float factor = p.scale_log2 == 0.f ? 0x1p-126f : p.scale_log2;
+      // what a hidden score is overwritten with: -inf once it is multiplied (a factor of 0 would make it NaN, and the
+      // smallest that is not, the largest score 2^-21)
+      const float factor = p.scale_log2 == 0.f ? 0x1p-149f : p.scale_log2;
       uint32_t hidden = __float_as_uint(kScores == kPlain && factor < 0.f ? -kNegInf : kNegInf);
       // cap * tanh(s * cap_in) up to |s * cap_in| = 3/4 as an odd polynomial in s: the minimax fit of tanh(y) / y in y^2
       // by Remez' exchange, off by 2.9e-8, with the factors in its terms; its last term is negative, so that a score
