@@ -510,8 +510,8 @@ int hc_append_int4_wire(const hc_rows* q, const hc_rows* k, const hc_rows* v, in
  *               same time need workspaces of their own.
  *   workspace_bytes : hc_attend_int4_workspace() at least
  *   err_flag  : HC_DEVERR_LENGTH: a request with more queries than max_new, or
- *               than n_tokens holds, or a length outside its table: its rows of
- *               out and lse are left as they were; HC_DEVERR_SLOT: a slot
+ *               than n_tokens holds, or a length outside its table or above
+ *               2^31 - 1024: its rows of out and lse are left as they were; HC_DEVERR_SLOT: a slot
  *               outside the cache: its block is taken as zeros; HC_DEVERR_WAIT
  *               (set by no other call): a kernel's wait for its own loads or
  *               products ran out after two seconds, which only a defect can

@@ -194,6 +194,7 @@ int hc_attend_paged(const hc_rows* q, const hc_rows* out, float* lse, int32_t n_
   p.n_tokens = n_tokens;
   p.max_new = max_new;
   p.table_width = table_width;
+  p.most_keys = static_cast<int32_t>(std::min(int64_t{table_width} << log2, hc::kMostKeys));
   p.num_slots = desc->num_slots;
   p.H = H;
   p.G = G;

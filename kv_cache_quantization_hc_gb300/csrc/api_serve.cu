@@ -257,6 +257,7 @@ int hc_attend_int4(const hc_rows* q, const hc_rows* out, float* lse, int32_t dty
   p.n_tokens = n_tokens;
   p.max_new = max_new;
   p.table_width = table_width;
+  p.most_keys = static_cast<int32_t>(std::min(int64_t{table_width} << log2, hc::kMostKeys));
   p.num_slots = cache->num_slots;
   p.H = cache->n_kv_heads;
   p.G = G;

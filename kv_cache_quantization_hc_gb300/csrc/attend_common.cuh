@@ -55,7 +55,7 @@ __device__ __forceinline__ Request load_request(const AttendParams& p, int r, in
   q.n = __ldg(p.q_starts + r + 1) - q.q0;
   q.kv = __ldg(p.kv_lens + r);
   const bool ok = q.n >= 0 && q.n <= p.max_new && q.q0 >= 0 && q.q0 <= p.n_tokens - q.n && q.kv >= 0 &&
-                  q.kv <= (static_cast<int64_t>(p.table_width) << p.B_log2);
+                  q.kv <= p.most_keys;
   if (!ok) {
     bad |= HC_DEVERR_LENGTH;
     q.q0 = q.n = q.kv = 0;

@@ -21,7 +21,7 @@ __device__ __forceinline__ PagedRequest load_request(const AttendPagedParams& p,
   q.kv = __ldg(p.kv_lens + r);
   q.prefix = p.prefix_lens ? max(__ldg(p.prefix_lens + r), 0) : 0;
   const bool ok = q.n >= 0 && q.n <= p.max_new && q.q0 >= 0 && q.q0 <= p.n_tokens - q.n && q.kv >= 0 &&
-                  q.kv <= (static_cast<int64_t>(p.table_width) << p.B_log2);
+                  q.kv <= p.most_keys;
   if (!ok) {
     bad |= HC_DEVERR_LENGTH;
     q.q0 = q.n = q.kv = 0;

@@ -93,6 +93,10 @@ struct AppendParams {
   int32_t* err;
 };
 
+// Keys of a request that the attention takes: a tile's keys, and those of the tiles that are loaded ahead, are counted
+// in 32 bits too.
+constexpr int64_t kMostKeys = (int64_t{1} << 31) - 1024;
+
 struct AttendParams {
   const void* q;
   void* out;
@@ -105,6 +109,7 @@ struct AttendParams {
   const int32_t* q_starts;
   const int32_t* kv_lens;
   int32_t n_req, n_tokens, max_new, table_width, num_slots;
+  int32_t most_keys;    // of a request: what its table holds, kMostKeys at most
   int32_t H, G, B_log2, bf16, causal, window;
   FastDivmod by_group;  // division by G
   float scale_log2;     // softmax_scale * log2(e)
