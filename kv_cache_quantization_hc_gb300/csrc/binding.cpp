@@ -435,6 +435,7 @@ PyObject* attend_paged(PyObject* const* a) {
   const at::Tensor& k_pages = in.tensor(a[1], "k_pages");
   const at::Tensor& v_pages = in.tensor(a[2], "v_pages");
   const hc_paged_desc desc = pages_desc(k_pages, v_pages);
+  if (desc.dtype == HC_F32) throw BadArgument("attend_paged takes pages of float16 or bfloat16, not of Float as append_paged does");
   const at::Tensor& q = in.tensor(a[0], "q");
   const hc_rows qr = rows(q, "q", -1, -1, desc.d_head, k_pages.scalar_type());
   const int64_t n = q.size(0), heads = q.size(1);

@@ -116,7 +116,8 @@ def attend_int4(q, codes, scales, block_tables, q_starts, kv_lens, max_new, work
 
 
 def paged_cache(num_slots, H, B, d, dtype=torch.bfloat16, n_layers=None, device="cuda"):
-    """Empty K and V pages [num_slots, B, H, d]; with n_layers, one leading dimension more."""
+    """Empty K and V pages [num_slots, B, H, d]; with n_layers, one leading dimension more.  dtype: float16 or
+    bfloat16, or float32, which append_paged and the codec take but attend_paged refuses."""
     lead = () if n_layers is None else (n_layers,)
     return tuple(torch.zeros(lead + (num_slots, B, H, d), dtype=dtype, device=device) for _ in range(2))
 
