@@ -587,7 +587,7 @@ typedef struct hc_attend_scores {
   float softcap;              /* 0, or the bound of |softcap * tanh(score / softcap)| */
   const float* slopes;        /* device [n_q_heads] or NULL: the bias by distance, -slope * |position - key| */
   const int32_t* positions;   /* device [n_tokens] or NULL: the queries' positions, not falling within a request */
-  const int32_t* prefix_lens; /* device [n_req] or NULL: keys that every query sees; needs causal */
+  const int32_t* prefix_lens; /* device [n_req] or NULL: keys that queries before them see too (in their window); needs causal */
 } hc_attend_scores;
 
 /* hc_attend_paged: attention of queries over the pages.  Request r has queries

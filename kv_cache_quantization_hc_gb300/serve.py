@@ -152,7 +152,8 @@ def attend_paged(q, k_pages, v_pages, block_tables, q_starts, kv_lens, max_new, 
     for attend_int4.  softcap > 0: scores softcap * tanh(score / softcap).
     slopes (float32 [Hq]): less slope * distance.  positions (int32 [n_tokens],
     not falling within a request): queries at these positions instead of the
-    last ones.  prefix_lens (int32 [n_req]): keys that every query sees."""
+    last ones.  prefix_lens (int32 [n_req]): keys that a query sees from before
+    them too; a window hides these as it does others (hc_attend_scores)."""
     return _serve.attend_paged(q, k_pages, v_pages, block_tables, q_starts, kv_lens, max_new, workspace, err, causal,
                                window, softmax_scale, softcap, slopes, positions, prefix_lens, out, lse, return_lse,
                                stream)
