@@ -83,11 +83,12 @@ __device__ __forceinline__ void store_piece(T* p, const Piece<T, V>& r) {
   }
 }
 
-// A lane's position of token t, of the axis that is its number; false if a
-// position that some pair needs is outside the table.  Called by whole warps.
+// A lane's position of token t, of the axis that is its number: as it is
+// stored, so positions_exist is asked before turns_at reads the table there.
 __device__ __forceinline__ int lane_position(const RopeParams& p, int t, int lane) {
   return p.axes >> lane & 1u ? __ldg(p.positions + lane * p.position_stride + t) : 0;
 }
+// False if a position that some pair needs is outside the table.  Called by whole warps.
 __device__ __forceinline__ bool positions_exist(const RopeParams& p, int pos, int lane) {
   return __all_sync(0xffffffffu, !(p.axes >> lane & 1u) || (pos >= 0 && pos < p.n_positions));
 }
