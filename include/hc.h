@@ -564,9 +564,9 @@ int64_t hc_attend_int4_workspace(void);
  * row.
  *
  *   q, q_out : [n_tokens][n_q_heads][d_head], or NULL with n_q_heads = 0; q_out
- *              may be q
- *   k, v     : [n_tokens][n_kv_heads][d_head]; all of desc->dtype, 16-byte
- *              aligned, strides multiples of 16 bytes
+ *              may be q, with its strides, and overlaps no input otherwise
+ *   k, v     : [n_tokens][n_kv_heads][d_head], not in the pages; all of
+ *              desc->dtype, 16-byte aligned, strides multiples of 16 bytes
  *   rope     : as for hc_rope_axes, inverse = 0 and rot_dim a multiple of 16;
  *              NULL: no rotation (q and k are copied)
  *   token_rows : device int64 [n_tokens], distinct where >= 0 (precondition)
