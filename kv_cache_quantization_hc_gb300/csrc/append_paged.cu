@@ -8,12 +8,17 @@
 // needs of (cos, sin) is in registers, and the next token's rows are on their
 // way while this one's are turned.
 //
-// 8197 tokens of 32 query and 8 cache heads of 128 channels: fp16, interleaved
-// pairs 43 us of 30 that the bytes take at the copy rate; bf16 55, with pairs half
-// a rotation apart 58; fp32 71 of 60.  Bound by latency: a token's positions, then
-// its (cos, sin), then 400 instructions, by 16 warps an SM (120 registers; 24 warps
-// at 80 spill: 57 us instead of 43; half as many rows in hand, 46 to 75).  A warp
-// for each token, without the next one's rows on their way: 45 us.
+// 8197 tokens of 32 query and 8 cache heads of 128 channels, of 30 us that the bytes
+// take at the copy rate (fp32 60):
+//                                 fp16   bf16   fp32
+//   interleaved pairs               43     56     72
+//   half a rotation apart           53     59     72
+//   the same, 96 channels of 128    83     91    106
+// fp16 is bound by latency: a token's positions, then its (cos, sin), then 400
+// instructions, by 16 warps an SM (122 and 124 registers; 24 warps at 80 spill: 57 us
+// instead of 43; half as many rows in hand, 46 to 75).  A warp for each token,
+// without the next one's rows on their way: 45 us.  bf16 has the same loads but takes
+// all 128 registers and spills 40 and 44 bytes; fp32 takes 108 and 104.
 #include <algorithm>
 
 #include "paged.cuh"

@@ -39,7 +39,8 @@
 //   moves when a tile's sum passes 60000 and one of it 65504; a probability keeps
 //   11 bits down to 2^-20 of the largest.  Rows that see n keys in all, fewer than
 //   a tile, have m 3 above and 128 / n times lower; rows that see n in their first
-//   tile and more later, sqrt(128 / n) times higher.
+//   tile and more later, sqrt(128 / n) times higher, and 11 bits down to 2^-17 where
+//   n is 1.
 // * A move costs a tile 4000 cycles, and one row of 32 is enough.  So in fp16 the
 //   last two tiles change places: the first has 128 keys for most rows, whose
 //   largest tells more than that of a few (and see kAhead: of 8192 tokens' scores
@@ -47,12 +48,17 @@
 //   this order, 0.05% with 5 above instead of 3).
 //
 // Bound: the tensor cores (4 d flops per row and key).  8192 tokens of 32 query
-// and 8 cache heads of 128 channels: bf16 314 to 324 us, 1.70 to 1.75 PFLOP/s, 88
-// to 90% of the measured peak; fp16 349 us, where the same products draw more power
-// (a library's large one runs at 1.71 PFLOP/s against 1.82).  The softmax shows
+// and 8 cache heads of 128 channels: bf16 320 us, 1.72 PFLOP/s, 89% of a library's
+// largest product in a burst, for the first 45 ms of such calls; then 341 us, 1.61
+// PFLOP/s, 93% of what that product holds for seconds, as the GPU draws all the power
+// that it may and the clock falls (2070 to 1867 MHz), whether inputs repeat or not.
+// fp16 344 and 367 us, where the same products draw more power (a library's large
+// one runs at 1.71 PFLOP/s against 1.82).  The softmax shows
 // with 64 channels, whose tiles are half the products for the same softmax (232 us
 // of 142), and with capped scores, whose polynomial is as long as the rest of it
-// (516 us; two prompts of 3001 to 4097 tokens: tensor cores 39% active).  Runs of
+// (516 us; two prompts of 3001 to 4097 tokens: tensor cores 39% active).  A bias
+// takes three operations a score, one by one (bf16 383 us beside 341), and with a cap
+// as well each tile is gone through twice, with tanh itself (1064 us).  Runs of
 // few tiles: a run's first tile takes 1500 to 2300 cycles more.
 #pragma once
 
