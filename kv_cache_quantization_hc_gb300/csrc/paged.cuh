@@ -89,7 +89,6 @@ struct AttendPagedParams {
   const int32_t* prefix_lens;  // null: none
   const float* slopes;         // null: none
   int32_t n_req, n_tokens, max_new, table_width, num_slots;
-  int32_t most_keys;    // of a request: what its table holds, kMostKeys at most
   int32_t H, G, B_log2, bf16, causal, window;
   FastDivmod by_group, by_heads;  // division by G, by H
   float scale_log2;     // softmax_scale * log2(e)
@@ -106,6 +105,7 @@ struct AttendPagedParams {
   int64_t part_bytes;    // the list of runs to join is behind them
   int32_t part_rows;    // of the tiles kernel where runs may be shared out: rows of a part's sums
   SplitRule split;
+  int32_t most_keys;    // of a request: what its table holds, kMostKeys at most (here it moves no other field: else 0.7% slower)
   int32_t* err;
 };
 
